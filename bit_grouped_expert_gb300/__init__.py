@@ -26,6 +26,10 @@ MOE_ERR_CUDA = 6
 MOE_ERR_DEVICE_TIMEOUT = 7
 MOE_ERR_NONFINITE = 8
 MOE_ERR_DEVICE_BOUNDS = 9
+MOE_ERR_OUT_OF_PAGES = 10
+
+MOE_BF16 = 0
+MOE_FP16 = 1
 
 MOE_FLAG_DEBUG_CHECKS = 0x1
 MOE_FLAG_FORCE_GROUPED = 0x2
@@ -42,7 +46,9 @@ EXPORTS = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_workspace
            "moe_router_split", "moe_route_view", "moe_rmsnorm", "moe_dequant",
            "moe_device_status", "moe_last_launch_count", "moe_status_str", "moe_profile_events", "moe_profile_stride",
            "moe_last_cuda_error",
-           "moe_decode_static", "moe_decode_stack", "gdn_scan", "attn_decode_workspace_bytes", "attn_decode")
+           "moe_decode_static", "moe_decode_stack", "gdn_scan", "attn_decode_workspace_bytes", "attn_decode",
+           "attn_cache_append_workspace_bytes", "attn_cache_append", "attn_cache_fork_workspace_bytes",
+           "attn_cache_fork", "attn_cache_trim", "attn_tree_workspace_bytes", "attn_tree", "moe_draft_verify")
 
 MOE_DECODE_STATIC_SCRATCH_BYTES = 65536
 
@@ -57,6 +63,9 @@ MOE_KERNEL_RMSNORM = 10
 MOE_KERNEL_GATHER = 11
 MOE_KERNEL_GDN_SCAN = 12
 MOE_KERNEL_ATTN_DECODE = 13
+MOE_KERNEL_ATTN_TREE = 14
+MOE_KERNEL_DRAFT_VERIFY = 15
+MOE_KERNEL_CACHE_COPY = 16
 
 
 class MoeError(RuntimeError):
@@ -84,6 +93,12 @@ class moe_route_ptrs(ctypes.Structure):
                                                "trace_d")] + \
                [("max_tiles", ctypes.c_int32), ("block_rows", ctypes.c_int32), ("blockmap2_d", ctypes.c_void_p),
                 ("n_tiles2_d", ctypes.c_void_p), ("max_tiles2", ctypes.c_int32), ("block_rows2", ctypes.c_int32)]
+
+
+class attn_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_d", "v_d", "refs_d", "table_d", "lens_d", "status_d")] + \
+               [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_slots",
+                                              "max_pages", "dtype")]
 
 
 _lib = None
@@ -149,6 +164,23 @@ def lib():
         L.attn_decode_workspace_bytes.argtypes = [i32, i32, i32]
         L.attn_decode.restype = i32
         L.attn_decode.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, vp, sz, vp, vp]
+        cache = ctypes.POINTER(attn_cache)
+        L.attn_cache_append_workspace_bytes.restype = sz
+        L.attn_cache_append_workspace_bytes.argtypes = [cache, i32, i32]
+        L.attn_cache_append.restype = i32
+        L.attn_cache_append.argtypes = [cache, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
+        L.attn_cache_fork_workspace_bytes.restype = sz
+        L.attn_cache_fork_workspace_bytes.argtypes = [cache, i32]
+        L.attn_cache_fork.restype = i32
+        L.attn_cache_fork.argtypes = [cache, vp, vp, i32, vp, sz, vp]
+        L.attn_cache_trim.restype = i32
+        L.attn_cache_trim.argtypes = [cache, vp, vp, i32, vp]
+        L.attn_tree_workspace_bytes.restype = sz
+        L.attn_tree_workspace_bytes.argtypes = [cache, i32, i32, i32, i32]
+        L.attn_tree.restype = i32
+        L.attn_tree.argtypes = [cache, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, sz, vp, vp]
+        L.moe_draft_verify.restype = i32
+        L.moe_draft_verify.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -317,6 +349,140 @@ def attn_decode(q, k, v, L: int, Hq: int, Hkv: int, D: int, ws, o, scale: float 
     _check("attn_decode", lib().attn_decode(_ptr(q), _ptr(k), _ptr(v), int(L), int(Hq), int(Hkv), int(D),
                                             float(scale), _ptr(ws), _nbytes(ws) if not isinstance(ws, int) else 0,
                                             _ptr(o), _stream(stream)))
+
+
+def _given(name, t, dtype, *shape, optional=False):
+    """Address of a tensor argument of the paged-cache operators, whose sizes
+    come from their tensors: dense, of the type and shape asked for (None in
+    ``shape``: any size), on the current device."""
+    if t is None and optional:
+        return None
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(want is not None and want != n for want, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape "
+                         f"{tuple('any' if n is None else n for n in shape)} wanted, got {t.dtype} {tuple(t.shape)}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    _here(name, t)
+    return t.data_ptr()
+
+
+def _here(name, t):
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class AttnCache:
+    """A paged KV cache (cache.h): the attn_cache struct and the tensors behind it."""
+
+    def __init__(self, struct: attn_cache, tensors: dict):
+        import torch
+        self.struct = struct
+        self.ref = ctypes.byref(struct)
+        self.tensors = tensors
+        self.dtype = tensors["k"].dtype
+        self.i32 = torch.int32
+
+
+def make_attn_cache(k, v, refs, table, lens, status) -> AttnCache:
+    """The cache over the caller's tensors: k, v [n_layers, n_pages, page_size,
+    Hkv, D] (bf16 or fp16), refs [n_pages], table [n_slots, max_pages], lens
+    [n_slots], status [>= 1] int32, all contiguous on one device.  A new cache
+    starts with refs, lens and status zero and table -1."""
+    import torch
+    kinds = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
+    if k.dtype not in kinds or k.dim() != 5:
+        raise ValueError(f"k: bf16 or fp16 [layers, pages, page_size, heads, dim] wanted, got {k.dtype} "
+                         f"{tuple(k.shape)}")
+    layers, pages, page, heads, dim = k.shape
+    ints = torch.int32
+    st = attn_cache(_given("k", k, k.dtype, *k.shape), _given("v", v, k.dtype, *k.shape),
+                    _given("refs", refs, ints, pages), _given("table", table, ints, lens.shape[0], None),
+                    _given("lens", lens, ints, None), _given("status", status, ints, None), layers, pages, page, heads,
+                    dim, lens.shape[0], table.shape[1], kinds[k.dtype])
+    return AttnCache(st, dict(k=k, v=v, refs=refs, table=table, lens=lens, status=status))
+
+
+def attn_cache_append_workspace_bytes(cache: AttnCache, B: int, n_rows: int) -> int:
+    return int(lib().attn_cache_append_workspace_bytes(cache.ref, int(B), int(n_rows)))
+
+
+def attn_cache_append(cache: AttnCache, k_new, v_new, offsets, B: int, ws, slots=None, path=None, n_keep=None,
+                      stream=None):
+    """Append the kept rows of B sequences, in all layers: k_new, v_new
+    [n_layers, n_rows, Hkv, D], offsets int32 [B + 1], slots int32 [B] or None
+    (0 .. B-1), path int32 [B, stride] and n_keep int32 [B] as moe_draft_verify
+    leaves them, or None (every row, in order)."""
+    c = cache.struct
+    n_rows = k_new.shape[1]
+    shape = (c.n_layers, n_rows, c.n_kv_heads, c.head_dim)
+    _here("cache", cache.tensors["k"])
+    _check("attn_cache_append", lib().attn_cache_append(
+        cache.ref, _given("k_new", k_new, cache.dtype, *shape), _given("v_new", v_new, cache.dtype, *shape),
+        _given("slots", slots, cache.i32, B, optional=True), _given("offsets", offsets, cache.i32, B + 1),
+        _given("n_keep", n_keep, cache.i32, B, optional=True),
+        _given("path", path, cache.i32, B, None, optional=True), 0 if path is None else path.shape[1], int(B), n_rows,
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
+    return int(lib().attn_cache_fork_workspace_bytes(cache.ref, int(n)))
+
+
+def attn_cache_fork(cache: AttnCache, src, dst, n: int, ws, stream=None):
+    """Slot dst[i] (empty) becomes a copy of slot src[i]: full pages shared, the
+    partly filled last page copied.  src, dst int32 [n]."""
+    _here("cache", cache.tensors["k"])
+    _check("attn_cache_fork", lib().attn_cache_fork(cache.ref, _given("src", src, cache.i32, n),
+                                                    _given("dst", dst, cache.i32, n), int(n), _ptr(ws), _nbytes(ws),
+                                                    _stream(stream)))
+
+
+def attn_cache_trim(cache: AttnCache, slots, new_lens, n: int, stream=None):
+    """Cut n sequences to new_lens (0 frees one); slots int32 [n], or None for 0 .. n-1."""
+    _here("cache", cache.tensors["k"])
+    _check("attn_cache_trim", lib().attn_cache_trim(cache.ref, _given("slots", slots, cache.i32, n, optional=True),
+                                                    _given("new_lens", new_lens, cache.i32, n), int(n),
+                                                    _stream(stream)))
+
+
+def attn_tree_workspace_bytes(cache: AttnCache, B: int, n_nodes: int, max_nodes: int, Hq: int) -> int:
+    return int(lib().attn_tree_workspace_bytes(cache.ref, int(B), int(n_nodes), int(max_nodes), int(Hq)))
+
+
+def attn_tree(cache: AttnCache, layer: int, q, k_new, v_new, offsets, parent, B: int, max_nodes: int, ws, o,
+              slots=None, scale: float = 0.0, stream=None):
+    """Attention of B drafted trees over the cache's layer (tree.h): q, o
+    [n_nodes, Hq, D], k_new, v_new [n_nodes, Hkv, D] of the cache's type, offsets int32
+    [B + 1], parent int32 [n_nodes], slots int32 [B] or None (0 .. B-1), ws a
+    uint8 device tensor of attn_tree_workspace_bytes bytes or more."""
+    c = cache.struct
+    n, Hq = q.shape[0], q.shape[1]
+    _here("cache", cache.tensors["k"])
+    _check("attn_tree", lib().attn_tree(
+        cache.ref, int(layer), _given("q", q, cache.dtype, n, Hq, c.head_dim),
+        _given("k_new", k_new, cache.dtype, n, c.n_kv_heads, c.head_dim),
+        _given("v_new", v_new, cache.dtype, n, c.n_kv_heads, c.head_dim),
+        _given("slots", slots, cache.i32, B, optional=True), _given("offsets", offsets, cache.i32, B + 1),
+        _given("parent", parent, cache.i32, n), int(B), n, int(max_nodes), Hq, float(scale), _ptr(ws), _nbytes(ws),
+        _given("o", o, cache.dtype, n, Hq, c.head_dim), _stream(stream)))
+
+
+def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, path, n_path, next_token, status,
+                     stream=None):
+    """Verify B drafted trees (tree.h): p fp32 [n_nodes, V], q the same or
+    None, tokens, parent int32 [n_nodes], offsets int32 [B + 1], u_accept fp32
+    [n_nodes], u_sample fp32 [B]; written: path int32 [B, stride], n_path,
+    next_token int32 [B], status int32 [>= 1] (on an error)."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    n, V = p.shape
+    _check("moe_draft_verify", lib().moe_draft_verify(
+        _given("p", p, f32, n, V), _given("q", q, f32, n, V, optional=True), _given("tokens", tokens, i32, n),
+        _given("parent", parent, i32, n), _given("offsets", offsets, i32, B + 1),
+        _given("u_accept", u_accept, f32, n), _given("u_sample", u_sample, f32, B), int(B), n, V,
+        _given("path", path, i32, B, None), path.shape[1], _given("n_path", n_path, i32, B),
+        _given("next_token", next_token, i32, B), _given("status", status, i32, None), _stream(stream)))
 
 
 def moe_route_view(plan: Plan, ws, T: int) -> moe_route_ptrs:

@@ -18,7 +18,7 @@ thread_local int32_t g_last_launches = 0;
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 
 // Profiling hook state, per kernel id (moe_profile_events), per thread.
-constexpr int kProfKernels = 16;
+constexpr int kProfKernels = MOE_KERNEL_CACHE_COPY + 1;
 struct ProfState {
   int n = 0;
   int stride = 1;                   // bracket every stride-th launch
@@ -276,7 +276,7 @@ void prof_after(int kernel, cudaStream_t s) {
 extern "C" {
 
 moe_status moe_profile_events(int32_t kernel, void *const *start_events, void *const *stop_events, int32_t n) {
-  if (kernel < MOE_KERNEL_ROUTER || kernel > MOE_KERNEL_ATTN_DECODE || n < 0 || n > 4096) return MOE_ERR_INVALID_ARGUMENT;
+  if (kernel < MOE_KERNEL_ROUTER || kernel >= kProfKernels || n < 0 || n > 4096) return MOE_ERR_INVALID_ARGUMENT;
   if (n > 0 && (!start_events || !stop_events)) return MOE_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < n; ++i)
     if (!start_events[i] || !stop_events[i]) return MOE_ERR_INVALID_ARGUMENT;
@@ -301,7 +301,7 @@ moe_status moe_profile_events(int32_t kernel, void *const *start_events, void *c
 }
 
 moe_status moe_profile_stride(int32_t kernel, int32_t stride) {
-  if (kernel < MOE_KERNEL_ROUTER || kernel > MOE_KERNEL_ATTN_DECODE || stride < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (kernel < MOE_KERNEL_ROUTER || kernel >= kProfKernels || stride < 1) return MOE_ERR_INVALID_ARGUMENT;
   ProfState *p = g_prof[kernel];
   if (!p) return MOE_ERR_INVALID_ARGUMENT;
   p->stride = stride;
@@ -321,6 +321,7 @@ const char *moe_status_str(moe_status s) {
     case MOE_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case MOE_ERR_NONFINITE: return "non-finite router key";
     case MOE_ERR_DEVICE_BOUNDS: return "device bounds check failed";
+    case MOE_ERR_OUT_OF_PAGES: return "too few free cache pages";
   }
   return "unknown status";
 }

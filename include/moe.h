@@ -53,7 +53,8 @@ typedef enum {
   MOE_ERR_CUDA = 6,               /* a CUDA call or launch failed            */
   MOE_ERR_DEVICE_TIMEOUT = 7,     /* device status: a bounded wait gave up   */
   MOE_ERR_NONFINITE = 8,          /* device status: NaN/Inf router key       */
-  MOE_ERR_DEVICE_BOUNDS = 9       /* device status: debug bounds check hit   */
+  MOE_ERR_DEVICE_BOUNDS = 9,      /* device status: debug bounds check hit   */
+  MOE_ERR_OUT_OF_PAGES = 10       /* device status: too few free cache pages */
 } moe_status;
 
 /* Layer dimensions.  Supported: hidden % 128 == 0, inter % 64 == 0,
@@ -291,7 +292,10 @@ typedef enum {
   MOE_KERNEL_RMSNORM = 10,
   MOE_KERNEL_GATHER = 11,        /* routed x rows copied into perm order (tensor-core path) */
   MOE_KERNEL_GDN_SCAN = 12,      /* Gated DeltaNet scan (gdn.h)                */
-  MOE_KERNEL_ATTN_DECODE = 13    /* decode attention, per-block pass (attn.h)  */
+  MOE_KERNEL_ATTN_DECODE = 13,   /* decode attention, per-block pass (attn.h)  */
+  MOE_KERNEL_ATTN_TREE = 14,     /* tree attention over pages (tree.h)         */
+  MOE_KERNEL_DRAFT_VERIFY = 15,  /* verification of drafts (tree.h)            */
+  MOE_KERNEL_CACHE_COPY = 16     /* rows of an append or a fork (cache.h)      */
 } moe_kernel;
 
 /* Profiling hook (one per kernel).  From now on, on the calling thread, the
