@@ -1,109 +1,808 @@
 // Attention of drafted trees over a paged cache (tree.h).
 //
-// One CTA per (node, query head); its four warps take every fourth position
-// with a running maximum and sum and merge at the end.
+// The query heads of a KV head and the nodes of a tree together make the rows
+// of one matrix (row = node * G + head), so that a K or V tile read once
+// serves all of them: per tile of 64 positions
+//   S[128 rows x 64]  = Q . K^T     tcgen05, Q and K in shared memory
+//   P = 2^(S - m)                   one thread a row, running maximum m and sum l
+//   O[128 rows x D]  += P . V       tcgen05, P in tensor memory, V in shared memory
+// A unit is (sequence, KV head, up to 128 rows); its tiles are the cached
+// positions and then the tree's own nodes.  All units' tiles, in a row, are cut
+// into one equal run per CTA, whatever the lengths: a unit that spans CTAs
+// leaves partial results (m, l, O in fp32), which a second kernel joins.
+//
+// Roles: warp 4 loads (TMA: pages by the table's numbers, K one tile ahead
+// of V, into a ring), one thread of warp 5 issues the MMAs (S of the next tile
+// before O of this one), warps 0-3 own the rows.  Rescaling O on a new maximum
+// is put off while the maximum grows by less than 2^8: P then stays within
+// 2^8 and the fp32 sums lose nothing.
+// Every wait is bounded: after one second the kernel records
+// MOE_ERR_DEVICE_TIMEOUT, drains its copies and MMAs, frees tensor memory
+// and exits.
 #include <cuda_fp16.h>
 #include <math.h>
 
 #include "cache.cuh"
 #include "kernels.h"
+#include "tc.h"
+#include "tc_ptx.cuh"
 #include "tree.h"
 
 namespace moe {
 namespace {
 
-constexpr int AT_MAXN = 256;  // nodes of a tree
+constexpr int TR_MAXN = 256;      // nodes of a tree
+constexpr int TR_ROWS = 128;      // rows of a unit (MMA M)
+constexpr int TR_TILE = 64;       // positions of a tile
+constexpr int TR_THREADS = 192;
+constexpr int TR_MAX_SMS = 160;   // SMs used at most (the workspace is sized for them)
+constexpr float TR_SLACK = 8.f;   // growth of the maximum (log2) that O is not rescaled for
+constexpr unsigned long long TR_TIMEOUT_NS = 1000000000ull;
+
+template <int D>
+struct Cfg {
+  static constexpr int CHUNKS = D / 64;             // 128-byte columns of a row
+  static constexpr int CTAS = D == 256 ? 1 : 2;     // per SM
+  static constexpr int Q_CHUNK = TR_ROWS * 128;     // bytes of one column of Q
+  static constexpr int KV_CHUNK = TR_TILE * 128;    // of a K or V tile
+  static constexpr int SLOT = CHUNKS * KV_CHUNK;    // one K or V tile
+  // ring slots: what fits in 227 KB (D = 256) or half of that next to Q
+  static constexpr int NS = D == 256 ? 5 : D == 128 ? 4 : 10;
+  static constexpr int OFF_RING = CHUNKS * Q_CHUNK;
+  static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
+  static constexpr int SMEM = OFF_MISC + 1024 + 1024 /* alignment slack */;
+  static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
+  // tensor memory columns: O, two S tiles, and P: apart from S where there is
+  // room (D = 256), else over the S it came from
+  static constexpr bool P_OVER_S = D != 256;
+  static constexpr uint32_t S_COL = D, P_COL = P_OVER_S ? D : D + 2 * TR_TILE;
+  static constexpr uint32_t P_STEP = P_OVER_S ? TR_TILE : TR_TILE / 2;
+  static constexpr uint32_t TMEM = D == 256 ? 512 : 256;
+};
+
+struct TreeMaps {
+  CUtensorMap q;             // {64, Hq, nodes, chunks}, boxes of G heads x nt nodes
+  CUtensorMap k, v;          // {64, pool rows, chunks}
+  CUtensorMap k_new, v_new;  // {64, nodes, chunks}
+};
+
+// A CTA's split unit that starts with it, for the joining kernel.
+struct SplitDesc {
+  int32_t parts;  // CTAs it spans (0: none)
+  int32_t rows, node0, head0;
+};
 
 struct TreeArgs {
   CacheView c;
-  const uint16_t *q, *k_new, *v_new;
+  const uint16_t *v_new;
   const int32_t *slots, *offsets, *parent;
   uint16_t *o;
-  int B, n_nodes, max_nodes, Hq, Hkv, layer;
+  SplitDesc *desc;  // [grid]
+  float *ml;        // [2 * grid][rows_cap][2]
+  float *part;      // [2 * grid][rows_cap][D]
+  int B, n_nodes, max_nodes, Hq, Hkv, G;
+  int nt;           // nodes of a unit
+  int rows_cap;     // nt * G
+  int page_box;     // positions of one page-table entry that a tile takes (min(page, 64))
   float scale_log2;
 };
 
+struct Misc {
+  uint64_t full[10], empty[10];
+  uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, final_bar;
+  uint32_t tmem;
+  int abort_flag, nonfinite;
+  int b0;
+  long long off0, wsum[TR_THREADS / 32];
+  int16_t parent[TR_MAXN];
+};
+static_assert(sizeof(Misc) <= 1024, "misc area");
+
+struct Seq {
+  int slot, L, lo, n;  // n == 0: nothing to do
+};
+
+__device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
+  Seq s;
+  s.slot = a.slots ? a.slots[b] : b;
+  s.lo = a.offsets[b];
+  s.n = a.offsets[b + 1] - s.lo;
+  s.L = -1;
+  const bool ok = s.slot >= 0 && s.slot < a.c.n_slots && s.lo >= 0 && s.n >= 0 && s.n <= a.max_nodes &&
+                  s.lo <= a.n_nodes - s.n;
+  if (ok) s.L = slot_len(a.c, s.slot);
+  if (!ok || s.L < 0) {
+    set_status(a.c.status, MOE_ERR_DEVICE_BOUNDS);
+    s.n = s.L = 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int tiles_of(int n) { return (n + TR_TILE - 1) / TR_TILE; }
+
+__device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
+  if (s.n == 0) return 0;
+  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (tiles_of(s.L) + tiles_of(s.n));
+}
+
+// A CTA's walk over the units of its run of tiles.
+struct Walk {
+  const TreeArgs &a;
+  int b;
+  long long left;  // tiles of the run still to come
+  Seq s;
+  int g, rt, t0;   // unit, and its first tile that is this CTA's
+  int nt_all;      // tiles of the unit
+  int n;           // of them this CTA's
+  bool fresh;
+
+  __device__ Walk(const TreeArgs &a_, int b0, long long off, long long count) : a(a_), b(b0), left(count) {
+    if (left <= 0) return;
+    s = load_seq(a, b);
+    nt_all = tiles_of(s.L) + tiles_of(s.n);
+    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)(off / nt_all);
+    g = u / rts;
+    rt = u - g * rts;
+    t0 = (int)(off - (long long)u * nt_all);
+    fresh = true;
+  }
+  // the next unit; false when the run is done
+  __device__ bool next() {
+    if (left <= 0) return false;
+    if (!fresh) {
+      t0 = 0;
+      if (++rt * a.nt >= s.n) {
+        rt = 0;
+        if (++g >= a.Hkv) {
+          g = 0;
+          do {  // left > 0: a later sequence has tiles
+            s = load_seq(a, ++b);
+          } while (s.n == 0 && b + 1 < a.B);
+          if (s.n == 0) return false;
+          nt_all = tiles_of(s.L) + tiles_of(s.n);
+        }
+      }
+    }
+    fresh = false;
+    n = (int)(left < nt_all - t0 ? left : (long long)(nt_all - t0));
+    left -= n;
+    return true;
+  }
+  __device__ int node0() const { return rt * a.nt; }
+  __device__ int nodes() const { return min(a.nt, s.n - rt * a.nt); }
+};
+
+__device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  uint32_t n = 0;
+  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if ((++n & 7u) == 0) {
+      if (*reinterpret_cast<volatile int *>(&m->abort_flag)) return false;
+      if (ptx::globaltimer() - t0 > TR_TIMEOUT_NS) {
+        *reinterpret_cast<volatile int *>(&m->abort_flag) = 1;
+        set_status(status, MOE_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp: one answer for all lanes, and the lanes together again.
+__device__ __forceinline__ bool tr_wait_warp(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+  return __all_sync(0xffffffffu, tr_wait(bar, parity, m, status));
+}
+
+// Bounded wait used while draining after an abort.
+__device__ __forceinline__ void tr_drain(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (ptx::globaltimer() - t0 > TR_TIMEOUT_NS) return;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <bool FP16>
-__device__ __forceinline__ float to_f32(uint16_t h) {
-  if constexpr (FP16)
-    return __half2float(__ushort_as_half(h));
-  else
-    return bf16_to_f32(h);
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (FP16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
 }
 template <bool FP16>
-__device__ __forceinline__ uint16_t from_f32(float f) {
+__device__ __forceinline__ float value(uint32_t bits) {
   if constexpr (FP16)
-    return __half_as_ushort(__float2half_rn(f));
+    return __half2float(__ushort_as_half((uint16_t)bits));
   else
-    return f32_to_bf16(f);
+    return __uint_as_float(bits << 16);
+}
+template <bool FP16>
+constexpr uint32_t EXP_MASK = FP16 ? 0x7C00u : 0x7F80u;  // all ones: infinity or NaN
+
+// Position of K(j) / V(j) of a unit of n tiles in the ring's load order
+// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
+__device__ __forceinline__ uint32_t k_pos(int j) { return j == 0 ? 0u : 2u * j - 1u; }
+__device__ __forceinline__ uint32_t v_pos(int j, int n) { return j == n - 1 ? 2u * n - 1u : 2u * j + 2u; }
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
+    tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc *m = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the joining kernel may be scheduled now; it waits for this grid to finish
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // This CTA's run of tiles: every thread adds up some sequences' tiles, a
+  // scan gives their places, and the thread whose sequences hold the run's first tile
+  // writes down where that is.
+  const int per = (a.B + TR_THREADS - 1) / TR_THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
+  long long mine = 0;
+  for (int b = sb; b < se; ++b) mine += seq_tiles(a, load_seq(a, b));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) m->wsum[warp] = inc;
+  if (tid == 0) {
+    m->abort_flag = 0;
+    for (int i = 0; i < C::NS; ++i) {
+      ptx::mbar_init(&m->full[i], 1);
+      ptx::mbar_init(&m->empty[i], 1);
+    }
+    ptx::mbar_init(&m->q_full, 1);
+    ptx::mbar_init(&m->q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&m->s_full[i], 1);
+      ptx::mbar_init(&m->p_ready[i], TR_ROWS);
+      ptx::mbar_init(&m->pv_done[i], 1);
+    }
+    ptx::mbar_init(&m->o_free, TR_ROWS);
+    ptx::mbar_init(&m->rows_bar, TR_ROWS);
+    ptx::mbar_init(&m->final_bar, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  long long before = inc - mine, T = 0;
+  for (int w = 0; w < TR_THREADS / 32; ++w) {
+    if (w < warp) before += m->wsum[w];
+    T += m->wsum[w];
+  }
+  const int ctas = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x), cta = blockIdx.x;
+  if (cta >= ctas) {  // fewer tiles than CTAs
+    if (tid == 0) a.desc[cta].parts = 0;
+    return;
+  }
+  const long long first = T * cta / ctas, end = T * (cta + 1) / ctas;
+  if (first >= before && first < before + mine) {
+    long long at = before;
+    int b = sb;
+    for (;; ++b) {
+      const long long t = seq_tiles(a, load_seq(a, b));
+      if (first < at + t) break;
+      at += t;
+    }
+    m->b0 = b;
+    m->off0 = first - at;
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(&m->tmem, C::TMEM);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = m->tmem;
+  Walk w(a, m->b0, m->off0, end - first);
+  uint8_t *ring = smem + C::OFF_RING;
+  int32_t *status = a.c.status;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- loads
+    const int pool_rows = a.c.n_pages << a.c.page_shift;
+    const int boxes = TR_TILE / a.page_box;  // table entries of a tile
+    const int my_page = boxes == 1 ? 0 : lane / C::CHUNKS, my_chunk = boxes == 1 ? 0 : lane % C::CHUNKS;
+    const bool issues = boxes == 1 ? lane == 0 : lane < boxes * C::CHUNKS;
+    const uint32_t box_bytes = (uint32_t)a.page_box * 128;
+    uint32_t ld = 0, units = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int L = w.s.L, n_old = tiles_of(L), x = w.g * C::CHUNKS, blocks = pages_of(L, a.c.page_shift);
+      const int32_t *table = a.c.table + (size_t)w.s.slot * a.c.max_pages;
+      int eb = -32, ent = 0;  // 32 table entries from block eb on, one a lane
+      // the pool row of this lane's box of tile t (past the pool, read as zeros, where there is none)
+      auto locate = [&](int t) {
+        const int blk0 = (t * TR_TILE) >> a.c.page_shift;
+        if (blk0 < eb || blk0 + boxes > eb + 32) {
+          eb = blk0;
+          ent = eb + lane < blocks ? table[eb + lane] : -1;
+          if (eb + lane < blocks && (unsigned)ent >= (unsigned)a.c.n_pages) {
+            set_status(status, MOE_ERR_DEVICE_BOUNDS);
+            ent = -1;
+          }
+        }
+        const int p = __shfl_sync(0xffffffffu, ent, blk0 - eb + my_page % boxes);
+        return p < 0 ? pool_rows : (p << a.c.page_shift) + ((t * TR_TILE) & ((1 << a.c.page_shift) - 1));
+      };
+      auto load = [&](bool value_tile, int t, int row) {
+        const uint32_t slot = ld % C::NS;
+        bool got = true;
+        if (lane == 0) got = tr_wait(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status);
+        if (!__shfl_sync(0xffffffffu, (int)got, 0)) return false;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&m->full[slot], C::SLOT);
+        __syncwarp();
+        uint8_t *dst = ring + slot * C::SLOT;
+        if (t >= n_old) {
+          if (lane == 0)
+            ptx::tma_load_3d(dst, value_tile ? &maps.v_new : &maps.k_new, &m->full[slot], 0,
+                             w.s.lo + (t - n_old) * TR_TILE, x);
+        } else if (issues) {
+          ptx::tma_load_3d(dst + my_chunk * C::KV_CHUNK + my_page * box_bytes, value_tile ? &maps.v : &maps.k,
+                           &m->full[slot], 0, row, x + my_chunk);
+        }
+        ++ld;
+        return true;
+      };
+      // the unit's queries, once the last unit's scores are done
+      if (lane == 0) ok = units == 0 || tr_wait(&m->q_free, (units - 1) & 1u, m, status);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      if (!ok) break;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
+        for (int ch = 0; ch < C::CHUNKS; ++ch)
+          ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
+      }
+      ++units;
+      int row = w.t0 < n_old ? locate(w.t0) : 0;
+      ok = load(false, w.t0, row);
+      for (int j = 0; ok && j < w.n; ++j) {
+        const int t = w.t0 + j;
+        int next_row = 0;
+        if (j + 1 < w.n) {
+          if (t + 1 < n_old) next_row = locate(t + 1);
+          ok = load(false, t + 1, next_row);
+        }
+        ok = ok && load(true, t, row);
+        row = next_row;
+      }
+    }
+    if (!ok && lane == 0) {  // loads of the last slots may still be in flight
+      if (units) tr_drain(&m->q_full, (units - 1) & 1u);
+      for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
+        tr_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
+    }
+  } else if (warp == 5) {
+    // ----------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
+      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
+      uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
+      bool ok = true;
+      auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
+        const uint32_t slot = pos % C::NS;
+        if (C::P_OVER_S && t >= 2 && !tr_wait(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+        if (!tr_wait(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+        ptx::tc_fence_after();
+        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_u32(ring + slot * C::SLOT));
+#pragma unroll
+        for (int ch = 0; ch < C::CHUNKS; ++ch)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ptx::mma_ss(tmem + C::S_COL + (t & 1) * TR_TILE, qd + (ch * C::Q_CHUNK + i * 32) / 16,
+                        kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s, (ch | i) != 0);
+        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->s_full[t & 1]);
+        return true;
+      };
+      while (ok && w.next()) {
+        ok = tr_wait(&m->q_full, units & 1u, m, status) && scores(ld, jj);
+        for (int j = 0; ok && j < w.n; ++j, ++jj) {
+          if (j + 1 < w.n) ok = scores(ld + k_pos(j + 1), jj + 1);
+          if (ok && j + 2 >= w.n && (j + 1 < w.n || w.n == 1)) ptx::mma_commit(&m->q_free);
+          if (!ok) break;
+          const uint32_t pos = ld + v_pos(j, w.n), slot = pos % C::NS;
+          ok = tr_wait(&m->p_ready[jj & 1], (jj >> 1) & 1u, m, status) &&
+               tr_wait(&m->full[slot], (pos / C::NS) & 1u, m, status) &&
+               (j > 0 || units == 0 || tr_wait(&m->o_free, (units - 1) & 1u, m, status));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
+          const uint32_t p_col = tmem + C::P_COL + (jj & 1) * C::P_STEP;
+#pragma unroll
+          for (int i = 0; i < TR_TILE / 16; ++i)
+            ptx::mma_ts(tmem, p_col + 8 * i, vd + i * 2048 / 16, id_o, j > 0 || i > 0);
+          ptx::mma_commit(&m->empty[slot]);
+          ptx::mma_commit(&m->pv_done[jj & 1]);
+        }
+        ld += 2 * w.n;
+        ++units;
+      }
+      ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
+      tr_drain(&m->final_bar, 0);
+    }
+  } else {
+    // ----------------------------------------------------------------- rows
+    const int r = tid;
+    const int my_node = r / a.G, my_head = r - my_node * a.G;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t ld = 0, jj = 0, syncs = 0;
+    bool ok = true;
+    SplitDesc split{0, 0, 0, 0};
+    auto rows_sync = [&]() {  // the four warps meet (a wait that can give up, as all others)
+      ptx::mbar_arrive(&m->rows_bar);
+      return tr_wait_warp(&m->rows_bar, syncs++ & 1u, m, status);
+    };
+    while (ok && w.next()) {
+      const int L = w.s.L, n_old = tiles_of(L), nodes = w.nodes(), rows = nodes * a.G, node0 = w.node0();
+      const bool in = r < rows;
+      // the tree's parents, and what this row's node sees of each tile of nodes
+      if (!rows_sync()) break;  // the last unit's readers are done
+      for (int i = r; i < w.s.n; i += TR_ROWS) {
+        int p = a.parent[w.s.lo + i];
+        if (p >= i || p < -2) {
+          set_status(status, MOE_ERR_DEVICE_BOUNDS);
+          p = -2;
+        }
+        m->parent[i] = (int16_t)p;
+      }
+      if (r == 0) m->nonfinite = 0;
+      if (!rows_sync()) break;
+      unsigned long long sees[TR_MAXN / TR_TILE] = {};
+      bool real = false;
+      if (in) {
+        int i = node0 + my_node;
+        real = m->parent[i] != -2;
+        while (real && i >= 0) {
+#pragma unroll
+          for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
+            if (i / TR_TILE == q) sees[q] |= 1ull << (i % TR_TILE);
+          i = m->parent[i];
+        }
+      }
+      const bool active = warp * 32 < rows;                             // the warp has rows
+      const bool all_real = __all_sync(0xffffffffu, real || !in);       // none of them is padding
+      float mx = -INFINITY, sum = 0.f;
+      for (int j = 0; j < w.n; ++j, ++jj) {
+        const int t = w.t0 + j;
+        const bool edge = t >= n_old || (t + 1) * TR_TILE > L;
+        if (!tr_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, m, status)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        if (edge) {
+          // V rows that nobody may see become zeros (0 x NaN is NaN), and in the
+          // tree's own tiles non-finite values as well: they are added below to
+          // the rows that see them
+          const uint32_t pos = ld + v_pos(j, w.n), slot = pos % C::NS;
+          if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) {
+            ok = false;
+            break;
+          }
+          uint8_t *v = ring + slot * C::SLOT;
+          for (int e = r; e < TR_TILE * C::CHUNKS * 8; e += TR_ROWS) {  // 16-byte pieces
+            const int ch = e / (TR_TILE * 8), q = (e / 8) % TR_TILE;
+            uint4 *piece = reinterpret_cast<uint4 *>(v + ch * C::KV_CHUNK + q * 128 + (e & 7) * 16);
+            const int at = t < n_old ? t * TR_TILE + q : (t - n_old) * TR_TILE + q;
+            const bool hold = t < n_old ? at < L : at < w.s.n && m->parent[at] != -2;
+            if (!hold) {
+              *piece = make_uint4(0u, 0u, 0u, 0u);
+            } else if (t >= n_old) {
+              uint32_t x[4] = {piece->x, piece->y, piece->z, piece->w};
+              bool bad = false;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if ((x[i] & EXP_MASK<FP16>) == EXP_MASK<FP16>) x[i] &= 0xFFFF0000u, bad = true;
+                if ((x[i] >> 16 & EXP_MASK<FP16>) == EXP_MASK<FP16>) x[i] &= 0x0000FFFFu, bad = true;
+              }
+              if (bad) {
+                *piece = make_uint4(x[0], x[1], x[2], x[3]);
+                m->nonfinite = 1;
+              }
+            }
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (active) {
+          uint32_t s0[32], s1[32];
+          ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, s0);
+          ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE + 32, s1);
+          ptx::tmem_wait_ld();
+          float tmax = -INFINITY;
+          if (edge || !all_real) {
+            unsigned long long see = 0;
+            if (real) {
+              if (t < n_old) {
+                const int left = L - t * TR_TILE;
+                see = left >= TR_TILE ? ~0ull : (1ull << left) - 1;
+              } else {
+#pragma unroll
+                for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
+                  if (t - n_old == q) see = sees[q];
+              }
+            }
+            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!(lo >> i & 1)) s0[i] = 0xFF800000u;  // -infinity
+              if (!(hi >> i & 1)) s1[i] = 0xFF800000u;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            tmax = fmaxf(tmax, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
+          tmax *= a.scale_log2;
+          const bool grows = in && tmax > mx + TR_SLACK;  // also the first score a row sees
+          if (__any_sync(0xffffffffu, grows)) {
+            const float f = grows ? (mx == -INFINITY ? 0.f : ex2(mx - tmax)) : 1.f;
+            if (grows) mx = tmax;
+            sum *= f;
+            if (j > 0) {  // O holds the earlier tiles
+              if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld_x32(lanes + d, v);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                ptx::tmem_st_x32(lanes + d, v);
+              }
+            }
+          }
+          const float base = mx == -INFINITY ? 0.f : -mx;
+          uint32_t p[32];
+          float acc[4] = {};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float x0 = ex2(fmaf(__uint_as_float(s0[i]), a.scale_log2, base));
+            const float x1 = ex2(fmaf(__uint_as_float(s0[i + 1]), a.scale_log2, base));
+            const float y0 = ex2(fmaf(__uint_as_float(s1[i]), a.scale_log2, base));
+            const float y1 = ex2(fmaf(__uint_as_float(s1[i + 1]), a.scale_log2, base));
+            acc[0] += x0;
+            acc[1] += x1;
+            acc[2] += y0;
+            acc[3] += y1;
+            p[i / 2] = pack2<FP16>(x0, x1);
+            p[16 + i / 2] = pack2<FP16>(y0, y1);
+          }
+          sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          // the P tile's last reader (with P over S, the scores' MMA has waited for it)
+          if (!C::P_OVER_S && jj >= 2 && !tr_wait_warp(&m->pv_done[jj & 1], ((jj - 2) >> 1) & 1u, m, status)) {
+            ok = false;
+            break;
+          }
+          ptx::tmem_st_x32(lanes + C::P_COL + (jj & 1) * C::P_STEP, p);
+          ptx::tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&m->p_ready[jj & 1]);
+      }
+      if (!ok) break;
+      ld += 2 * w.n;
+      // the unit's result, or this CTA's part of it
+      if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) break;
+      ptx::tc_fence_after();
+      const bool whole = w.n == w.nt_all, starts = w.t0 == 0;
+      if (!whole && starts) {
+        const long long u1 = end - w.left - w.n + w.nt_all;  // the unit's end among all tiles
+        split = SplitDesc{(int)((u1 * ctas + T - 1) / T) - cta, rows, w.s.lo + node0, w.g * a.G};
+      }
+      // PV has ended, and with it every write of the flag
+      const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
+      const size_t pslot = ((size_t)2 * cta + (starts ? 1 : 0)) * a.rows_cap + r;
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      if (active) {
+        uint16_t *out = a.o + ((size_t)(w.s.lo + node0 + my_node) * a.Hq + w.g * a.G + my_head) * D;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          ptx::tmem_ld_x32(lanes + d, v);
+          ptx::tmem_wait_ld();
+          if (!in) continue;
+          if (fix && real) {
+            for (int i = 0; i < w.s.n; ++i) {
+              const int t = n_old + i / TR_TILE;
+              if (t < w.t0 || t >= w.t0 + w.n || !(sees[i / TR_TILE] >> (i % TR_TILE) & 1)) continue;
+              const uint16_t *src = a.v_new + (size_t)(w.s.lo + i) * a.c.row + w.g * D + d;
+#pragma unroll
+              for (int q = 0; q < 32; ++q) {
+                const uint32_t h = src[q];
+                if ((h & EXP_MASK<FP16>) == EXP_MASK<FP16>) v[q] = __float_as_uint(__uint_as_float(v[q]) + value<FP16>(h));
+              }
+            }
+          }
+          if (whole) {
+            if (sum == 0.f) {  // a row that sees nothing
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 x;
+              x.x = pack2<FP16>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+              x.y = pack2<FP16>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+              x.z = pack2<FP16>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+              x.w = pack2<FP16>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+              *reinterpret_cast<uint4 *>(out + d + i) = x;
+            }
+          } else {
+            float *part = a.part + pslot * D + d;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4 *>(part + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+        if (in && !whole) *reinterpret_cast<float2 *>(a.ml + pslot * 2) = make_float2(mx, sum);
+      }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&m->o_free);
+    }
+    if (r == 0) a.desc[cta] = split;
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
+// unit.  Threads of one row: D / 4 columns of four values, times several
+// groups that take every so many parts and join in shared memory.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  constexpr int COLS = D / 4, GROUPS = 256 / COLS;
+  __shared__ SplitDesc desc_s[2 * TR_MAX_SMS];
+  __shared__ int cta_s[2 * TR_MAX_SMS], order_s[2 * TR_MAX_SMS], n_split;
+  __shared__ float4 acc_s[GROUPS][COLS];
+  __shared__ float m_s[GROUPS], l_s[GROUPS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, col = tid % COLS, grp = tid / COLS;
+  if (tid == 0) n_split = 0;
+  __syncthreads();
+  for (int c = tid; c < ctas; c += 256) {
+    const SplitDesc d = a.desc[c];
+    if (d.parts > 0) {
+      const int i = atomicAdd(&n_split, 1);
+      desc_s[i] = d;
+      cta_s[i] = c;
+    }
+  }
+  __syncthreads();
+  const int units = n_split;
+  for (int i = tid; i < units; i += 256) {  // in the CTAs' order, the same in every block
+    int rank = 0;
+    for (int j = 0; j < units; ++j) rank += cta_s[j] < cta_s[i];
+    order_s[rank] = i;
+  }
+  __syncthreads();
+  for (int item = blockIdx.x; item < units * a.rows_cap; item += gridDim.x) {
+    const int u = item / a.rows_cap, r = item - u * a.rows_cap;
+    const int pick = order_s[u];
+    const SplitDesc d = desc_s[pick];
+    if (r >= d.rows) continue;
+    const int c0 = cta_s[pick];
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = grp; i < d.parts; i += GROUPS) {
+      const size_t p = ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows_cap + r;
+      const float2 ml = *reinterpret_cast<const float2 *>(a.ml + p * 2);
+      const float4 v = *reinterpret_cast<const float4 *>(a.part + p * D + col * 4);
+      const float mn = fmaxf(M, ml.x);
+      const float f = M == -INFINITY ? 0.f : ex2(M - mn), h = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      // a part in which the row saw nothing adds nothing
+      if (ml.x != -INFINITY) {
+        acc.x = fmaf(acc.x, f, v.x * h);
+        acc.y = fmaf(acc.y, f, v.y * h);
+        acc.z = fmaf(acc.z, f, v.z * h);
+        acc.w = fmaf(acc.w, f, v.w * h);
+        l = fmaf(l, f, ml.y * h);
+        M = mn;
+      }
+    }
+    acc_s[grp][col] = acc;
+    if (col == 0) {
+      m_s[grp] = M;
+      l_s[grp] = l;
+    }
+    __syncthreads();
+    if (grp == 0) {
+      float Mx = -INFINITY, den = 0.f;
+      for (int i = 0; i < GROUPS; ++i) Mx = fmaxf(Mx, m_s[i]);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < GROUPS; ++i) {
+        if (m_s[i] == -INFINITY) continue;
+        const float f = ex2(m_s[i] - Mx);
+        const float4 v = acc_s[i][col];
+        s.x = fmaf(v.x, f, s.x);
+        s.y = fmaf(v.y, f, s.y);
+        s.z = fmaf(v.z, f, s.z);
+        s.w = fmaf(v.w, f, s.w);
+        den = fmaf(l_s[i], f, den);
+      }
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      const int node = d.node0 + r / a.G, head = d.head0 + r % a.G;
+      uint2 x;
+      x.x = pack2<FP16>(s.x * inv, s.y * inv);
+      x.y = pack2<FP16>(s.z * inv, s.w * inv);
+      *reinterpret_cast<uint2 *>(a.o + ((size_t)node * a.Hq + head) * D + col * 4) = x;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+bool row_map(CUtensorMap *map, const void *p, int64_t rows, int row, int D, int box_rows, int box_chunks) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(row / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)row * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool query_map(CUtensorMap *map, const void *p, int nodes, int Hq, int D, int G, int nt) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)Hq, (cuuint64_t)nodes, (cuuint64_t)(D / 64)};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2, 128};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)nt, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tree_ctas(int D, int sms) { return (D == 256 ? 1 : 2) * (sms < TR_MAX_SMS ? sms : TR_MAX_SMS); }
+
+int unit_nodes(int G, int max_nodes) {
+  const int nt = TR_ROWS / G;
+  return nt < max_nodes ? nt : max_nodes;
+}
+
+// Workspace: the split units, then maxima and sums, then partial outputs.
+size_t tree_ws(int D, int ctas, int rows_cap, size_t *ml_at, size_t *part_at) {
+  *ml_at = (size_t)ctas * sizeof(SplitDesc);
+  *part_at = *ml_at + ((size_t)2 * ctas * rows_cap * 8 + 255) / 256 * 256;
+  return *part_at + (size_t)2 * ctas * rows_cap * D * 4;
 }
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float o_s[4][D], m_s[4], l_s[4];
-  const int node = blockIdx.x, h = blockIdx.y, g = h / (a.Hq / a.Hkv), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const CacheView &c = a.c;
-  int b = 0;
-  while (b < a.B && !(a.offsets[b] <= node && node < a.offsets[b + 1])) ++b;
-  if (b == a.B) return;
-  const int lo = a.offsets[b], slot = a.slots ? a.slots[b] : b;
-  int L = slot >= 0 && slot < c.n_slots ? slot_len(c, slot) : -1;
-  if (lo < 0 || a.offsets[b + 1] > a.n_nodes || a.offsets[b + 1] - lo > a.max_nodes || L < 0) {
-    if (threadIdx.x == 0) set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  if (a.parent[node] == -2) L = 0;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = to_f32<FP16>(a.q[((size_t)node * a.Hq + h) * D + e * 32 + lane]) * a.scale_log2;
-  auto take = [&](const uint16_t *k, const uint16_t *v) {
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], to_f32<FP16>(k[e * 32 + lane]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, to_f32<FP16>(v[e * 32 + lane]), o[e] * f);
-    l = l * f + w;
-    m = mn;
-  };
-  for (int p = warp; p < L; p += 4) {
-    const int page = table_page(c, slot, p >> c.page_shift);
-    if (page < 0) break;
-    const size_t row = ((((size_t)a.layer * c.n_pages + page) << c.page_shift) + (p & ((1 << c.page_shift) - 1))) * c.row;
-    take(c.k + row + g * D, c.v + row + g * D);
-  }
-  int i = node - lo, step = 0;
-  if (a.parent[node] == -2) i = -1;
-  while (i >= 0) {
-    const size_t row = (size_t)(lo + i) * c.row + g * D;
-    if ((step++ & 3) == warp) take(a.k_new + row, a.v_new + row);
-    const int up = a.parent[lo + i];
-    if (up >= i || up < -1) {
-      if (threadIdx.x == 0) set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
-      break;
-    }
-    i = up;
-  }
-  for (int e = 0; e < E; ++e) o_s[warp][e * 32 + lane] = o[e];
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
-  }
-  __syncthreads();
-  float M = -INFINITY, den = 0.f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, m_s[w]);
-  for (int w = 0; w < 4; ++w) den += m_s[w] == -INFINITY ? 0.f : exp2f(m_s[w] - M) * l_s[w];
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float s = 0.f;
-    for (int w = 0; w < 4; ++w) s += m_s[w] == -INFINITY ? 0.f : exp2f(m_s[w] - M) * o_s[w][d];
-    a.o[((size_t)node * a.Hq + h) * D + d] = from_f32<FP16>(M == -INFINITY ? 0.f : s / den);
-  }
-}
-
-template <int D>
-cudaError_t launch_tree(const TreeArgs &a, bool fp16, cudaStream_t s) {
-  const dim3 grid(a.n_nodes, a.Hq);
-  return fp16 ? launch_dep(false, tree_kernel<D, true>, grid, dim3(128), 0, s, a)
-              : launch_dep(false, tree_kernel<D, false>, grid, dim3(128), 0, s, a);
+cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
+  // per device and cheap: set on every call rather than remembered
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  prof_before(MOE_KERNEL_ATTN_TREE, s);
+  const bool quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
+  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(TR_THREADS), Cfg<D>::SMEM, s, maps, a);
+  prof_after(MOE_KERNEL_ATTN_TREE, s);
+  if (e != cudaSuccess) return e;
+  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(256), 0, s, a, ctas);
 }
 
 }  // namespace
@@ -112,8 +811,13 @@ cudaError_t launch_tree(const TreeArgs &a, bool fp16, cudaStream_t s) {
 extern "C" size_t attn_tree_workspace_bytes(const attn_cache *c, int32_t B, int32_t n_nodes, int32_t max_nodes,
                                             int32_t Hq) {
   moe::CacheView v;
-  if (moe::cache_view(c, &v) != MOE_OK || B < 1 || n_nodes < 1 || max_nodes < 1 || Hq < 1) return 0;
-  return 16;
+  if (moe::cache_view(c, &v) != MOE_OK || B < 1 || n_nodes < 1 || max_nodes < 1 || max_nodes > moe::TR_MAXN || Hq < 1 ||
+      Hq % c->n_kv_heads || Hq / c->n_kv_heads > moe::TR_ROWS)
+    return 0;
+  const int G = Hq / c->n_kv_heads;
+  size_t ml, part;
+  return moe::tree_ws(c->head_dim, moe::tree_ctas(c->head_dim, moe::TR_MAX_SMS),
+                      G * moe::unit_nodes(G, max_nodes), &ml, &part);
 }
 
 extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *q_d, const void *k_new_d,
@@ -127,7 +831,8 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   if (layer < 0 || layer >= c->n_layers || B < 0 || n_nodes < 0 || max_nodes < 1 || Hq < 1 || !(scale >= 0.f) ||
       isinf(scale))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (Hq % c->n_kv_heads || Hq / c->n_kv_heads > 128 || max_nodes > moe::AT_MAXN || B > moe::CACHE_MAX_SEQS)
+  const int D = c->head_dim, G = Hq / c->n_kv_heads;
+  if (Hq % c->n_kv_heads || G > moe::TR_ROWS || max_nodes > moe::TR_MAXN || B > moe::CACHE_MAX_SEQS)
     return MOE_ERR_UNSUPPORTED;
   if (B == 0 || n_nodes == 0) return MOE_OK;
   if (!q_d || !k_new_d || !v_new_d || !offsets_d || !parent_d || !ws_d || !o_d) return MOE_ERR_INVALID_ARGUMENT;
@@ -135,9 +840,12 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
       !aligned16(offsets_d) || !aligned16(parent_d) || !aligned16(ws_d) || !aligned16(o_d))
     return MOE_ERR_MISALIGNED;
   if (ws_bytes < attn_tree_workspace_bytes(c, B, n_nodes, max_nodes, Hq)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (scale == 0.f) scale = 1.f / sqrtf((float)c->head_dim);
-  a.q = static_cast<const uint16_t *>(q_d);
-  a.k_new = static_cast<const uint16_t *>(k_new_d);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return moe::note_cuda_error(e);
+  if (scale == 0.f) scale = 1.f / sqrtf((float)D);
+  const int ctas = moe::tree_ctas(D, sms);
   a.v_new = static_cast<const uint16_t *>(v_new_d);
   a.slots = slots_d;
   a.offsets = offsets_d;
@@ -148,14 +856,32 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.max_nodes = max_nodes;
   a.Hq = Hq;
   a.Hkv = c->n_kv_heads;
-  a.layer = layer;
+  a.G = G;
+  a.nt = moe::unit_nodes(G, max_nodes);
+  a.rows_cap = a.nt * G;
+  a.page_box = c->page_size < moe::TR_TILE ? c->page_size : moe::TR_TILE;
   a.scale_log2 = scale * 1.4426950408889634f;
+  size_t ml_at, part_at;
+  moe::tree_ws(D, ctas, a.rows_cap, &ml_at, &part_at);
+  a.desc = static_cast<moe::SplitDesc *>(ws_d);
+  a.ml = moe::ws_ptr<float>(ws_d, ml_at);
+  a.part = moe::ws_ptr<float>(ws_d, part_at);
+  const int64_t pool_rows = (int64_t)c->n_pages * c->page_size;
+  const uint16_t *k = a.c.k + (size_t)layer * pool_rows * a.c.row, *v = a.c.v + (size_t)layer * pool_rows * a.c.row;
+  const int chunks = a.page_box == moe::TR_TILE ? D / 64 : 1;
+  moe::TreeMaps maps;
+  if (!moe::query_map(&maps.q, q_d, n_nodes, Hq, D, G, a.nt) ||
+      !moe::row_map(&maps.k, k, pool_rows, a.c.row, D, a.page_box, chunks) ||
+      !moe::row_map(&maps.v, v, pool_rows, a.c.row, D, a.page_box, chunks) ||
+      !moe::row_map(&maps.k_new, k_new_d, n_nodes, a.c.row, D, moe::TR_TILE, D / 64) ||
+      !moe::row_map(&maps.v_new, v_new_d, n_nodes, a.c.row, D, moe::TR_TILE, D / 64))
+    return moe::note_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp16 = c->dtype == MOE_FP16;
-  moe::prof_before(MOE_KERNEL_ATTN_TREE, s);
-  const cudaError_t e = c->head_dim == 64    ? moe::launch_tree<64>(a, fp16, s)
-                        : c->head_dim == 128 ? moe::launch_tree<128>(a, fp16, s)
-                                             : moe::launch_tree<256>(a, fp16, s);
-  moe::prof_after(MOE_KERNEL_ATTN_TREE, s);
+  e = D == 64    ? (fp16 ? moe::launch_tree<64, true>(maps, a, ctas, s) : moe::launch_tree<64, false>(maps, a, ctas, s))
+      : D == 128 ? (fp16 ? moe::launch_tree<128, true>(maps, a, ctas, s)
+                         : moe::launch_tree<128, false>(maps, a, ctas, s))
+                 : (fp16 ? moe::launch_tree<256, true>(maps, a, ctas, s)
+                         : moe::launch_tree<256, false>(maps, a, ctas, s));
   return moe::note_cuda_error(e);
 }
