@@ -351,25 +351,29 @@ def attn_decode(q, k, v, L: int, Hq: int, Hkv: int, D: int, ws, o, scale: float 
                                             _ptr(o), _stream(stream)))
 
 
-def _given(name, t, dtype, *shape, optional=False):
-    """Address of a tensor argument of the paged-cache operators, whose sizes
-    come from their tensors: dense, of the type and shape asked for (None in
-    ``shape``: any size), on the current device."""
-    if t is None and optional:
-        return None
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(want is not None and want != n for want, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape "
-                         f"{tuple('any' if n is None else n for n in shape)} wanted, got {t.dtype} {tuple(t.shape)}"
-                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    _here(name, t)
+def _given(name, t, dtype, device, shape):
+    """Address of a tensor argument of the paged-cache and drafting operators,
+    whose sizes come from their tensors: dense, of the type and shape asked
+    for, on the call's device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device} wanted, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
     return t.data_ptr()
 
 
-def _here(name, t):
+def _here(name, device):
+    """Refuse a call whose tensors are not on the current device (kernels launch there)."""
     import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _raw_stream(stream, device):
+    """As _stream, without making a Stream object for the current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 class AttnCache:
@@ -382,6 +386,8 @@ class AttnCache:
         self.tensors = tensors
         self.dtype = tensors["k"].dtype
         self.i32 = torch.int32
+        self.device = tensors["k"].get_device()
+        self.layers, self.heads, self.dim = struct.n_layers, struct.n_kv_heads, struct.head_dim
 
 
 def make_attn_cache(k, v, refs, table, lens, status) -> AttnCache:
@@ -391,15 +397,16 @@ def make_attn_cache(k, v, refs, table, lens, status) -> AttnCache:
     starts with refs, lens and status zero and table -1."""
     import torch
     kinds = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
-    if k.dtype not in kinds or k.dim() != 5:
-        raise ValueError(f"k: bf16 or fp16 [layers, pages, page_size, heads, dim] wanted, got {k.dtype} "
-                         f"{tuple(k.shape)}")
+    if k.dtype not in kinds or k.dim() != 5 or table.dim() != 2 or lens.dim() != 1 or status.dim() != 1:
+        raise ValueError(f"k: bf16 or fp16 [layers, pages, page_size, heads, dim], table of 2, lens and status of 1 "
+                         f"dimensions wanted, got k {k.dtype} {tuple(k.shape)}")
     layers, pages, page, heads, dim = k.shape
-    ints = torch.int32
-    st = attn_cache(_given("k", k, k.dtype, *k.shape), _given("v", v, k.dtype, *k.shape),
-                    _given("refs", refs, ints, pages), _given("table", table, ints, lens.shape[0], None),
-                    _given("lens", lens, ints, None), _given("status", status, ints, None), layers, pages, page, heads,
-                    dim, lens.shape[0], table.shape[1], kinds[k.dtype])
+    dev, ints = k.get_device(), torch.int32
+    st = attn_cache(_given("k", k, k.dtype, dev, k.shape), _given("v", v, k.dtype, dev, k.shape),
+                    _given("refs", refs, ints, dev, (pages,)),
+                    _given("table", table, ints, dev, (lens.shape[0], table.shape[1])),
+                    _given("lens", lens, ints, dev, lens.shape), _given("status", status, ints, dev, status.shape),
+                    layers, pages, page, heads, dim, lens.shape[0], table.shape[1], kinds[k.dtype])
     return AttnCache(st, dict(k=k, v=v, refs=refs, table=table, lens=lens, status=status))
 
 
@@ -413,16 +420,16 @@ def attn_cache_append(cache: AttnCache, k_new, v_new, offsets, B: int, ws, slots
     [n_layers, n_rows, Hkv, D], offsets int32 [B + 1], slots int32 [B] or None
     (0 .. B-1), path int32 [B, stride] and n_keep int32 [B] as moe_draft_verify
     leaves them, or None (every row, in order)."""
-    c = cache.struct
-    n_rows = k_new.shape[1]
-    shape = (c.n_layers, n_rows, c.n_kv_heads, c.head_dim)
-    _here("cache", cache.tensors["k"])
+    dev, i32, n_rows = cache.device, cache.i32, k_new.shape[1]
+    _here("cache", dev)
+    shape, stride = (cache.layers, n_rows, cache.heads, cache.dim), 0 if path is None else path.shape[-1]
     _check("attn_cache_append", lib().attn_cache_append(
-        cache.ref, _given("k_new", k_new, cache.dtype, *shape), _given("v_new", v_new, cache.dtype, *shape),
-        _given("slots", slots, cache.i32, B, optional=True), _given("offsets", offsets, cache.i32, B + 1),
-        _given("n_keep", n_keep, cache.i32, B, optional=True),
-        _given("path", path, cache.i32, B, None, optional=True), 0 if path is None else path.shape[1], int(B), n_rows,
-        _ptr(ws), _nbytes(ws), _stream(stream)))
+        cache.ref, _given("k_new", k_new, cache.dtype, dev, shape), _given("v_new", v_new, cache.dtype, dev, shape),
+        None if slots is None else _given("slots", slots, i32, dev, (B,)),
+        _given("offsets", offsets, i32, dev, (B + 1,)),
+        None if n_keep is None else _given("n_keep", n_keep, i32, dev, (B,)),
+        None if path is None else _given("path", path, i32, dev, (B, stride)), stride, B, n_rows, _ptr(ws),
+        _nbytes(ws), _raw_stream(stream, dev)))
 
 
 def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
@@ -432,18 +439,20 @@ def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
 def attn_cache_fork(cache: AttnCache, src, dst, n: int, ws, stream=None):
     """Slot dst[i] (empty) becomes a copy of slot src[i]: full pages shared, the
     partly filled last page copied.  src, dst int32 [n]."""
-    _here("cache", cache.tensors["k"])
-    _check("attn_cache_fork", lib().attn_cache_fork(cache.ref, _given("src", src, cache.i32, n),
-                                                    _given("dst", dst, cache.i32, n), int(n), _ptr(ws), _nbytes(ws),
-                                                    _stream(stream)))
+    dev = cache.device
+    _here("cache", dev)
+    _check("attn_cache_fork", lib().attn_cache_fork(
+        cache.ref, _given("src", src, cache.i32, dev, (n,)), _given("dst", dst, cache.i32, dev, (n,)), n, _ptr(ws),
+        _nbytes(ws), _raw_stream(stream, dev)))
 
 
 def attn_cache_trim(cache: AttnCache, slots, new_lens, n: int, stream=None):
     """Cut n sequences to new_lens (0 frees one); slots int32 [n], or None for 0 .. n-1."""
-    _here("cache", cache.tensors["k"])
-    _check("attn_cache_trim", lib().attn_cache_trim(cache.ref, _given("slots", slots, cache.i32, n, optional=True),
-                                                    _given("new_lens", new_lens, cache.i32, n), int(n),
-                                                    _stream(stream)))
+    dev = cache.device
+    _here("cache", dev)
+    _check("attn_cache_trim", lib().attn_cache_trim(
+        cache.ref, None if slots is None else _given("slots", slots, cache.i32, dev, (n,)),
+        _given("new_lens", new_lens, cache.i32, dev, (n,)), n, _raw_stream(stream, dev)))
 
 
 def attn_tree_workspace_bytes(cache: AttnCache, B: int, n_nodes: int, max_nodes: int, Hq: int) -> int:
@@ -456,16 +465,15 @@ def attn_tree(cache: AttnCache, layer: int, q, k_new, v_new, offsets, parent, B:
     [n_nodes, Hq, D], k_new, v_new [n_nodes, Hkv, D] of the cache's type, offsets int32
     [B + 1], parent int32 [n_nodes], slots int32 [B] or None (0 .. B-1), ws a
     uint8 device tensor of attn_tree_workspace_bytes bytes or more."""
-    c = cache.struct
-    n, Hq = q.shape[0], q.shape[1]
-    _here("cache", cache.tensors["k"])
+    dev, dt, i32 = cache.device, cache.dtype, cache.i32
+    _here("cache", dev)
+    n, Hq, _ = q.shape
+    rows, heads = (n, cache.heads, cache.dim), (n, Hq, cache.dim)
     _check("attn_tree", lib().attn_tree(
-        cache.ref, int(layer), _given("q", q, cache.dtype, n, Hq, c.head_dim),
-        _given("k_new", k_new, cache.dtype, n, c.n_kv_heads, c.head_dim),
-        _given("v_new", v_new, cache.dtype, n, c.n_kv_heads, c.head_dim),
-        _given("slots", slots, cache.i32, B, optional=True), _given("offsets", offsets, cache.i32, B + 1),
-        _given("parent", parent, cache.i32, n), int(B), n, int(max_nodes), Hq, float(scale), _ptr(ws), _nbytes(ws),
-        _given("o", o, cache.dtype, n, Hq, c.head_dim), _stream(stream)))
+        cache.ref, layer, _given("q", q, dt, dev, heads), _given("k_new", k_new, dt, dev, rows),
+        _given("v_new", v_new, dt, dev, rows), None if slots is None else _given("slots", slots, i32, dev, (B,)),
+        _given("offsets", offsets, i32, dev, (B + 1,)), _given("parent", parent, i32, dev, (n,)), B, n, max_nodes, Hq,
+        scale, _ptr(ws), _nbytes(ws), _given("o", o, dt, dev, heads), _raw_stream(stream, dev)))
 
 
 def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, path, n_path, next_token, status,
@@ -475,14 +483,17 @@ def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, 
     [n_nodes], u_sample fp32 [B]; written: path int32 [B, stride], n_path,
     next_token int32 [B], status int32 [>= 1] (on an error)."""
     import torch
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, dev = torch.float32, torch.int32, p.get_device()
+    _here("p", dev)
     n, V = p.shape
+    stride = path.shape[-1]
     _check("moe_draft_verify", lib().moe_draft_verify(
-        _given("p", p, f32, n, V), _given("q", q, f32, n, V, optional=True), _given("tokens", tokens, i32, n),
-        _given("parent", parent, i32, n), _given("offsets", offsets, i32, B + 1),
-        _given("u_accept", u_accept, f32, n), _given("u_sample", u_sample, f32, B), int(B), n, V,
-        _given("path", path, i32, B, None), path.shape[1], _given("n_path", n_path, i32, B),
-        _given("next_token", next_token, i32, B), _given("status", status, i32, None), _stream(stream)))
+        _given("p", p, f32, dev, (n, V)), None if q is None else _given("q", q, f32, dev, (n, V)),
+        _given("tokens", tokens, i32, dev, (n,)), _given("parent", parent, i32, dev, (n,)),
+        _given("offsets", offsets, i32, dev, (B + 1,)), _given("u_accept", u_accept, f32, dev, (n,)),
+        _given("u_sample", u_sample, f32, dev, (B,)), B, n, V, _given("path", path, i32, dev, (B, stride)), stride,
+        _given("n_path", n_path, i32, dev, (B,)), _given("next_token", next_token, i32, dev, (B,)),
+        _given("status", status, i32, dev, status.shape), _raw_stream(stream, dev)))
 
 
 def moe_route_view(plan: Plan, ws, T: int) -> moe_route_ptrs:

@@ -668,87 +668,126 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
 }
 
 // o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
-// unit.  Threads of one row: D / 4 columns of four values, times several
-// groups that take every so many parts and join in shared memory.
+// unit.  One to eight warps of a block take a row, about four parts each (a
+// unit is split over as few as two CTAs and as many as all of them): the lanes
+// first read every part's (m, l), so that the weights are known before the
+// parts' values, whose loads then do not wait for one another.
+constexpr int TJ_WARPS = 8;
+
+__device__ __forceinline__ int warps_per_row(int parts) {
+  return parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : TJ_WARPS;
+}
+
 template <int D, bool FP16>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
-  constexpr int COLS = D / 4, GROUPS = 256 / COLS;
-  __shared__ SplitDesc desc_s[2 * TR_MAX_SMS];
-  __shared__ int cta_s[2 * TR_MAX_SMS], order_s[2 * TR_MAX_SMS], n_split;
-  __shared__ float4 acc_s[GROUPS][COLS];
-  __shared__ float m_s[GROUPS], l_s[GROUPS];
+__global__ void __launch_bounds__(TJ_WARPS * 32) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  constexpr int E = D / 32, MAXU = 2 * TR_MAX_SMS;  // values of a row a lane holds; split units at most
+  __shared__ SplitDesc desc_s[MAXU];
+  __shared__ int cta_s[MAXU], item_s[MAXU + 1], wsum[TJ_WARPS];
+  __shared__ float acc_s[TJ_WARPS][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, col = tid % COLS, grp = tid / COLS;
-  if (tid == 0) n_split = 0;
-  __syncthreads();
-  for (int c = tid; c < ctas; c += 256) {
-    const SplitDesc d = a.desc[c];
-    if (d.parts > 0) {
-      const int i = atomicAdd(&n_split, 1);
-      desc_s[i] = d;
-      cta_s[i] = c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the split units in the CTAs' order, and the row groups (items) before each
+  constexpr int PER = (MAXU + TJ_WARPS * 32 - 1) / (TJ_WARPS * 32);
+  SplitDesc d[PER];
+  int mine = 0, items = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = tid * PER + i;
+    d[i].parts = 0;
+    if (c < ctas) d[i] = a.desc[c];
+    if (d[i].parts > 0) {
+      ++mine;
+      items += (d[i].rows * warps_per_row(d[i].parts) + TJ_WARPS - 1) / TJ_WARPS;
     }
   }
-  __syncthreads();
-  const int units = n_split;
-  for (int i = tid; i < units; i += 256) {  // in the CTAs' order, the same in every block
-    int rank = 0;
-    for (int j = 0; j < units; ++j) rank += cta_s[j] < cta_s[i];
-    order_s[rank] = i;
+  int packed = mine << 20 | items;  // at most 320 units and 320 * 128 items
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, packed, o);
+    if (lane >= o) packed += t;
   }
+  if (lane == 31) wsum[warp] = packed;
   __syncthreads();
-  for (int item = blockIdx.x; item < units * a.rows_cap; item += gridDim.x) {
-    const int u = item / a.rows_cap, r = item - u * a.rows_cap;
-    const int pick = order_s[u];
-    const SplitDesc d = desc_s[pick];
-    if (r >= d.rows) continue;
-    const int c0 = cta_s[pick];
-    float M = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = grp; i < d.parts; i += GROUPS) {
-      const size_t p = ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows_cap + r;
-      const float2 ml = *reinterpret_cast<const float2 *>(a.ml + p * 2);
-      const float4 v = *reinterpret_cast<const float4 *>(a.part + p * D + col * 4);
-      const float mn = fmaxf(M, ml.x);
-      const float f = M == -INFINITY ? 0.f : ex2(M - mn), h = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
-      // a part in which the row saw nothing adds nothing
-      if (ml.x != -INFINITY) {
-        acc.x = fmaf(acc.x, f, v.x * h);
-        acc.y = fmaf(acc.y, f, v.y * h);
-        acc.z = fmaf(acc.z, f, v.z * h);
-        acc.w = fmaf(acc.w, f, v.w * h);
-        l = fmaf(l, f, ml.y * h);
-        M = mn;
-      }
+  int before = packed - (mine << 20 | items), all = 0;
+  for (int w = 0; w < TJ_WARPS; ++w) {
+    if (w < warp) before += wsum[w];
+    all += wsum[w];
+  }
+  const int units = all >> 20, n_items = all & 0xFFFFF;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (d[i].parts > 0) {
+      const int u = before >> 20;
+      desc_s[u] = d[i];
+      cta_s[u] = tid * PER + i;
+      item_s[u] = before & 0xFFFFF;
+      before += 1 << 20 | (d[i].rows * warps_per_row(d[i].parts) + TJ_WARPS - 1) / TJ_WARPS;
     }
-    acc_s[grp][col] = acc;
-    if (col == 0) {
-      m_s[grp] = M;
-      l_s[grp] = l;
+  if (tid == 0) item_s[units] = n_items;
+  __syncthreads();
+
+  int u = 0;
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    while (item >= item_s[u + 1]) ++u;
+    const SplitDesc ds = desc_s[u];
+    const int c0 = cta_s[u], wpr = warps_per_row(ds.parts), sub = warp % wpr;
+    const int r = (item - item_s[u]) * (TJ_WARPS / wpr) + warp / wpr;
+    const bool in = r < ds.rows;
+    // part i lies in CTA c0 + i's second slot if it starts the unit, else in its first
+    auto slot = [&](int i) { return ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows_cap + (in ? r : 0); };
+    float M = -INFINITY, den = 0.f;
+    for (int i0 = 0; i0 < ds.parts; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < ds.parts) ml = *reinterpret_cast<const float2 *>(a.ml + slot(i0 + lane) * 2);
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(M, mx);
+      const float l = warp_sum(ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - mn));
+      den = (M == -INFINITY ? 0.f : den * ex2(M - mn)) + l;
+      M = mn;
     }
-    __syncthreads();
-    if (grp == 0) {
-      float Mx = -INFINITY, den = 0.f;
-      for (int i = 0; i < GROUPS; ++i) Mx = fmaxf(Mx, m_s[i]);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < GROUPS; ++i) {
-        if (m_s[i] == -INFINITY) continue;
-        const float f = ex2(m_s[i] - Mx);
-        const float4 v = acc_s[i][col];
-        s.x = fmaf(v.x, f, s.x);
-        s.y = fmaf(v.y, f, s.y);
-        s.z = fmaf(v.z, f, s.z);
-        s.w = fmaf(v.w, f, s.w);
-        den = fmaf(l_s[i], f, den);
+    float acc[E] = {};
+#pragma unroll 4
+    for (int i = sub; i < ds.parts; i += wpr) {
+      const size_t p = slot(i);
+      const float m = a.ml[p * 2];
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);  // a part in which the row saw nothing adds zeros
+      alignas(16) float v[E];
+      const float *src = a.part + p * D + lane * E;
+      if constexpr (E >= 4) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(src + e);
+      } else {
+        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+    }
+    if (wpr > 1) {
+      __syncthreads();  // the last item's readers are done
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc_s[warp][e * 32 + lane] = acc[e];
+      __syncthreads();
+      if (sub == 0)
+        for (int w = 1; w < wpr; ++w)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += acc_s[warp + w][e * 32 + lane];
+    }
+    if (in && sub == 0) {
       const float inv = den == 0.f ? 0.f : 1.f / den;
-      const int node = d.node0 + r / a.G, head = d.head0 + r % a.G;
-      uint2 x;
-      x.x = pack2<FP16>(s.x * inv, s.y * inv);
-      x.y = pack2<FP16>(s.z * inv, s.w * inv);
-      *reinterpret_cast<uint2 *>(a.o + ((size_t)node * a.Hq + head) * D + col * 4) = x;
+      alignas(16) uint32_t x[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) x[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+      const int node = ds.node0 + r / a.G, head = ds.head0 + r % a.G;
+      uint16_t *out = a.o + ((size_t)node * a.Hq + head) * D + lane * E;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<uint4 *>(x);
+      else if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<uint2 *>(x);
+      else
+        *reinterpret_cast<uint32_t *>(out) = x[0];
     }
-    __syncthreads();
   }
 }
 
@@ -802,7 +841,7 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(TR_THREADS), Cfg<D>::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
-  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(256), 0, s, a, ctas);
+  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_WARPS * 32), 0, s, a, ctas);
 }
 
 }  // namespace
