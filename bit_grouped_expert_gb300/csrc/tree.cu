@@ -46,18 +46,22 @@ struct Cfg {
   static constexpr int Q_CHUNK = TR_ROWS * 128;     // bytes of one column of Q
   static constexpr int KV_CHUNK = TR_TILE * 128;    // of a K or V tile
   static constexpr int SLOT = CHUNKS * KV_CHUNK;    // one K or V tile
-  // ring slots: what fits in 227 KB (D = 256) or half of that next to Q
-  static constexpr int NS = D == 256 ? 5 : D == 128 ? 4 : 10;
-  static constexpr int OFF_RING = CHUNKS * Q_CHUNK;
+  // Q is the MMA's A operand in tensor memory where there is room for it
+  // (D = 256: it goes through two ring slots first), else in shared memory.
+  // From shared memory the 64-wide score MMAs would read Q anew for every
+  // tile, as much again as K, V and their copies in together: a tile of 128
+  // rows then takes 1,500 cycles instead of 1,200.
+  static constexpr bool Q_TMEM = D == 256;
+  static constexpr int Q_SLOTS = Q_TMEM ? 2 : 0;
+  static constexpr int NS = D == 256 ? 7 : D == 128 ? 4 : 10;  // ring slots: what fits in 227 KB, or half of that
+  static constexpr int OFF_RING = Q_TMEM ? 0 : CHUNKS * Q_CHUNK;
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
   static constexpr int SMEM = OFF_MISC + 1024 + 1024 /* alignment slack */;
   static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
-  // tensor memory columns: O, two S tiles, and P: apart from S where there is
-  // room (D = 256), else over the S it came from
-  static constexpr bool P_OVER_S = D != 256;
-  static constexpr uint32_t S_COL = D, P_COL = P_OVER_S ? D : D + 2 * TR_TILE;
-  static constexpr uint32_t P_STEP = P_OVER_S ? TR_TILE : TR_TILE / 2;
+  // tensor memory columns: O, Q, two S tiles, each turned into P in place
+  static constexpr uint32_t Q_COL = D, S_COL = Q_COL + (Q_TMEM ? D / 2 : 0);
   static constexpr uint32_t TMEM = D == 256 ? 512 : 256;
+  static_assert(S_COL + 2 * TR_TILE <= TMEM, "tensor memory");
 };
 
 struct TreeMaps {
@@ -79,7 +83,7 @@ struct TreeArgs {
   uint16_t *o;
   SplitDesc *desc;  // [grid]
   float *ml;        // [2 * grid][rows_cap][2]
-  float *part;      // [2 * grid][rows_cap][D]
+  float *part;      // [2 * grid][D / 4][rows_cap][4]
   int B, n_nodes, max_nodes, Hq, Hkv, G;
   int nt;           // nodes of a unit
   int rows_cap;     // nt * G
@@ -89,7 +93,7 @@ struct TreeArgs {
 
 struct Misc {
   uint64_t full[10], empty[10];
-  uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, final_bar;
+  uint64_t q_full, q_free, q_ready, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, final_bar;
   uint32_t tmem;
   int abort_flag, nonfinite;
   int b0;
@@ -103,17 +107,17 @@ struct Seq {
 };
 
 __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
+  // the loads first: none of them waits for another's check
   Seq s;
-  s.slot = a.slots ? a.slots[b] : b;
-  s.lo = a.offsets[b];
-  s.n = a.offsets[b + 1] - s.lo;
-  s.L = -1;
-  const bool ok = s.slot >= 0 && s.slot < a.c.n_slots && s.lo >= 0 && s.n >= 0 && s.n <= a.max_nodes &&
-                  s.lo <= a.n_nodes - s.n;
-  if (ok) s.L = slot_len(a.c, s.slot);
-  if (!ok || s.L < 0) {
+  s.slot = a.slots ? __ldg(a.slots + b) : b;
+  s.lo = __ldg(a.offsets + b);
+  const int hi = __ldg(a.offsets + b + 1);
+  const bool in = s.slot >= 0 && s.slot < a.c.n_slots;
+  s.L = in ? slot_len(a.c, s.slot) : -1;
+  s.n = hi - s.lo;
+  if (s.L < 0 || s.lo < 0 || hi < s.lo || s.n > a.max_nodes || hi > a.n_nodes) {
     set_status(a.c.status, MOE_ERR_DEVICE_BOUNDS);
-    s.n = s.L = 0;
+    s.n = s.L = s.lo = 0;
   }
   return s;
 }
@@ -123,6 +127,12 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + TR_TILE - 1) / TR_T
 __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
   if (s.n == 0) return 0;
   return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (tiles_of(s.L) + tiles_of(s.n));
+}
+
+// x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
+__device__ __forceinline__ long long mul_div(long long x, int y, int z) {
+  const long long p = x * y;
+  return p < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
 // A CTA's walk over the units of its run of tiles.
@@ -140,7 +150,7 @@ struct Walk {
     if (left <= 0) return;
     s = load_seq(a, b);
     nt_all = tiles_of(s.L) + tiles_of(s.n);
-    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)(off / nt_all);
+    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)mul_div(off, 1, nt_all);
     g = u / rts;
     rt = u - g * rts;
     t0 = (int)(off - (long long)u * nt_all);
@@ -228,9 +238,15 @@ template <bool FP16>
 constexpr uint32_t EXP_MASK = FP16 ? 0x7C00u : 0x7F80u;  // all ones: infinity or NaN
 
 // Position of K(j) / V(j) of a unit of n tiles in the ring's load order
-// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ uint32_t k_pos(int j) { return j == 0 ? 0u : 2u * j - 1u; }
-__device__ __forceinline__ uint32_t v_pos(int j, int n) { return j == n - 1 ? 2u * n - 1u : 2u * j + 2u; }
+// [Q Q] K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
+template <int D>
+__device__ __forceinline__ uint32_t k_pos(int j) {
+  return Cfg<D>::Q_SLOTS + (j == 0 ? 0u : 2u * j - 1u);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_pos(int j, int n) {
+  return Cfg<D>::Q_SLOTS + (j == n - 1 ? 2u * n - 1u : 2u * j + 2u);
+}
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
@@ -246,6 +262,10 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
   // This CTA's run of tiles: every thread adds up some sequences' tiles, a
   // scan gives their places, and the thread whose sequences hold the run's first tile
   // writes down where that is.
+  if (warp == 5) {
+    ptx::tmem_alloc(&m->tmem, C::TMEM);
+    ptx::tmem_relinquish();
+  }
   const int per = (a.B + TR_THREADS - 1) / TR_THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
   long long mine = 0;
   for (int b = sb; b < se; ++b) mine += seq_tiles(a, load_seq(a, b));
@@ -264,6 +284,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
     }
     ptx::mbar_init(&m->q_full, 1);
     ptx::mbar_init(&m->q_free, 1);
+    ptx::mbar_init(&m->q_ready, TR_ROWS);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&m->s_full[i], 1);
       ptx::mbar_init(&m->p_ready[i], TR_ROWS);
@@ -274,7 +295,10 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
     ptx::mbar_init(&m->final_bar, 1);
     ptx::fence_mbar_init();
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = m->tmem;
   long long before = inc - mine, T = 0;
   for (int w = 0; w < TR_THREADS / 32; ++w) {
     if (w < warp) before += m->wsum[w];
@@ -283,9 +307,10 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
   const int ctas = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x), cta = blockIdx.x;
   if (cta >= ctas) {  // fewer tiles than CTAs
     if (tid == 0) a.desc[cta].parts = 0;
+    if (warp == 5) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
-  const long long first = T * cta / ctas, end = T * (cta + 1) / ctas;
+  const long long first = mul_div(T, cta, ctas), end = mul_div(T, cta + 1, ctas);
   if (first >= before && first < before + mine) {
     long long at = before;
     int b = sb;
@@ -297,14 +322,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
     m->b0 = b;
     m->off0 = first - at;
   }
-  if (warp == 5) {
-    ptx::tmem_alloc(&m->tmem, C::TMEM);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
   __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = m->tmem;
   Walk w(a, m->b0, m->off0, end - first);
   uint8_t *ring = smem + C::OFF_RING;
   int32_t *status = a.c.status;
@@ -338,9 +356,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       };
       auto load = [&](bool value_tile, int t, int row) {
         const uint32_t slot = ld % C::NS;
-        bool got = true;
-        if (lane == 0) got = tr_wait(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status);
-        if (!__shfl_sync(0xffffffffu, (int)got, 0)) return false;
+        if (!tr_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status)) return false;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&m->full[slot], C::SLOT);
         __syncwarp();
         uint8_t *dst = ring + slot * C::SLOT;
@@ -355,14 +371,26 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
         ++ld;
         return true;
       };
-      // the unit's queries, once the last unit's scores are done
-      if (lane == 0) ok = units == 0 || tr_wait(&m->q_free, (units - 1) & 1u, m, status);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      if (!ok) break;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
-        for (int ch = 0; ch < C::CHUNKS; ++ch)
-          ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
+      if constexpr (C::Q_TMEM) {  // the unit's queries through the ring, two columns a slot
+        for (int h = 0; ok && h < C::Q_SLOTS; ++h, ++ld) {
+          const uint32_t slot = ld % C::NS;
+          ok = tr_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status);
+          if (ok && lane == 0) {
+            ptx::mbar_arrive_expect_tx(&m->full[slot], (uint32_t)(a.rows_cap * 256));
+            for (int i = 0; i < 2; ++i)
+              ptx::tma_load_4d(ring + slot * C::SLOT + i * C::Q_CHUNK, &maps.q, &m->full[slot], 0, w.g * a.G,
+                               w.s.lo + w.node0(), 2 * h + i);
+          }
+        }
+        if (!ok) break;
+      } else {  // in their own place, once the last unit's scores are done
+        ok = units == 0 || tr_wait_warp(&m->q_free, (units - 1) & 1u, m, status);
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
+          for (int ch = 0; ch < C::CHUNKS; ++ch)
+            ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
+        }
       }
       ++units;
       int row = w.t0 < n_old ? locate(w.t0) : 0;
@@ -379,59 +407,76 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       }
     }
     if (!ok && lane == 0) {  // loads of the last slots may still be in flight
-      if (units) tr_drain(&m->q_full, (units - 1) & 1u);
+      if (!C::Q_TMEM && units) tr_drain(&m->q_full, (units - 1) & 1u);
       for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
         tr_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
     }
   } else if (warp == 5) {
     // ----------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
-      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
-      uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
-      bool ok = true;
-      auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
-        const uint32_t slot = pos % C::NS;
-        if (C::P_OVER_S && t >= 2 && !tr_wait(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-        if (!tr_wait(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
-        ptx::tc_fence_after();
-        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_u32(ring + slot * C::SLOT));
+    const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
+    const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
+    uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
+    bool ok = true;
+    auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
+      const uint32_t slot = pos % C::NS;
+      // the P tile in its place has been used up
+      if (t >= 2 && !tr_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+      if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+      ptx::tc_fence_after();
+      const uint64_t kd = ptx::sdesc_sw128(ptx::smem_u32(ring + slot * C::SLOT));
+      const uint32_t s_col = tmem + C::S_COL + (t & 1) * TR_TILE;
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int ch = 0; ch < C::CHUNKS; ++ch)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            ptx::mma_ss(tmem + C::S_COL + (t & 1) * TR_TILE, qd + (ch * C::Q_CHUNK + i * 32) / 16,
-                        kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s, (ch | i) != 0);
+            if constexpr (C::Q_TMEM)
+              ptx::mma_ts(s_col, tmem + C::Q_COL + 8 * (4 * ch + i), kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s,
+                          (ch | i) != 0);
+            else
+              ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s,
+                          (ch | i) != 0);
         ptx::mma_commit(&m->empty[slot]);
         ptx::mma_commit(&m->s_full[t & 1]);
-        return true;
-      };
-      while (ok && w.next()) {
-        ok = tr_wait(&m->q_full, units & 1u, m, status) && scores(ld, jj);
-        for (int j = 0; ok && j < w.n; ++j, ++jj) {
-          if (j + 1 < w.n) ok = scores(ld + k_pos(j + 1), jj + 1);
-          if (ok && j + 2 >= w.n && (j + 1 < w.n || w.n == 1)) ptx::mma_commit(&m->q_free);
-          if (!ok) break;
-          const uint32_t pos = ld + v_pos(j, w.n), slot = pos % C::NS;
-          ok = tr_wait(&m->p_ready[jj & 1], (jj >> 1) & 1u, m, status) &&
-               tr_wait(&m->full[slot], (pos / C::NS) & 1u, m, status) &&
-               (j > 0 || units == 0 || tr_wait(&m->o_free, (units - 1) & 1u, m, status));
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
-          const uint32_t p_col = tmem + C::P_COL + (jj & 1) * C::P_STEP;
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && w.next()) {
+      ok = tr_wait_warp(C::Q_TMEM ? &m->q_ready : &m->q_full, units & 1u, m, status);
+      if (ok && C::Q_TMEM && ptx::elect_one())
+        for (int h = 0; h < C::Q_SLOTS; ++h) ptx::mbar_arrive(&m->empty[(ld + h) % C::NS]);
+      __syncwarp();
+      ok = ok && scores(ld + k_pos<D>(0), jj);
+      for (int j = 0; ok && j < w.n; ++j, ++jj) {
+        if (j + 1 < w.n) ok = scores(ld + k_pos<D>(j + 1), jj + 1);
+        if (!ok) break;
+        const bool q_done = j + 2 >= w.n && (j + 1 < w.n || w.n == 1);  // the unit's last scores are under way
+        if (!C::Q_TMEM && q_done && ptx::elect_one()) ptx::mma_commit(&m->q_free);
+        const uint32_t pos = ld + v_pos<D>(j, w.n), slot = pos % C::NS;
+        ok = tr_wait_warp(&m->p_ready[jj & 1], (jj >> 1) & 1u, m, status) &&
+             tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status) &&
+             (j > 0 || units == 0 || tr_wait_warp(&m->o_free, (units - 1) & 1u, m, status));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
+        const uint32_t p_col = tmem + C::S_COL + (jj & 1) * TR_TILE;
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int i = 0; i < TR_TILE / 16; ++i)
             ptx::mma_ts(tmem, p_col + 8 * i, vd + i * 2048 / 16, id_o, j > 0 || i > 0);
           ptx::mma_commit(&m->empty[slot]);
           ptx::mma_commit(&m->pv_done[jj & 1]);
         }
-        ld += 2 * w.n;
-        ++units;
+        __syncwarp();
       }
-      ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
-      tr_drain(&m->final_bar, 0);
+      ld += C::Q_SLOTS + 2 * w.n;
+      ++units;
     }
+    __syncwarp();
+    if (ptx::elect_one()) ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
+    __syncwarp();
+    tr_drain(&m->final_bar, 0);
   } else {
     // ----------------------------------------------------------------- rows
     const int r = tid;
@@ -471,6 +516,29 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
           i = m->parent[i];
         }
       }
+      if constexpr (C::Q_TMEM) {
+        // this row of Q from the ring into tensor memory (the last unit's
+        // scores, which read the one before, are done)
+#pragma unroll 1
+        for (int h = 0; ok && h < C::Q_SLOTS; ++h) {
+          const uint32_t slot = (ld + h) % C::NS;
+          ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[32];
+            const uint8_t *src = ring + slot * C::SLOT + i * C::Q_CHUNK + r * 128;
+#pragma unroll
+            for (int p = 0; p < 8; ++p)  // 16-byte pieces, swizzled by the row
+              *reinterpret_cast<uint4 *>(x + 4 * p) = *reinterpret_cast<const uint4 *>(src + ((p ^ (r & 7)) * 16));
+            ptx::tmem_st_x32(lanes + C::Q_COL + (2 * h + i) * 32, x);
+          }
+        }
+        if (!ok) break;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&m->q_ready);
+      }
       const bool active = warp * 32 < rows;                             // the warp has rows
       const bool all_real = __all_sync(0xffffffffu, real || !in);       // none of them is padding
       float mx = -INFINITY, sum = 0.f;
@@ -486,7 +554,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
           // V rows that nobody may see become zeros (0 x NaN is NaN), and in the
           // tree's own tiles non-finite values as well: they are added below to
           // the rows that see them
-          const uint32_t pos = ld + v_pos(j, w.n), slot = pos % C::NS;
+          const uint32_t pos = ld + v_pos<D>(j, w.n), slot = pos % C::NS;
           if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) {
             ok = false;
             break;
@@ -584,19 +652,14 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
             p[16 + i / 2] = pack2<FP16>(y0, y1);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          // the P tile's last reader (with P over S, the scores' MMA has waited for it)
-          if (!C::P_OVER_S && jj >= 2 && !tr_wait_warp(&m->pv_done[jj & 1], ((jj - 2) >> 1) & 1u, m, status)) {
-            ok = false;
-            break;
-          }
-          ptx::tmem_st_x32(lanes + C::P_COL + (jj & 1) * C::P_STEP, p);
+          ptx::tmem_st_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, p);
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(&m->p_ready[jj & 1]);
       }
       if (!ok) break;
-      ld += 2 * w.n;
+      ld += C::Q_SLOTS + 2 * w.n;
       // the unit's result, or this CTA's part of it
       if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) break;
       ptx::tc_fence_after();
@@ -607,7 +670,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       }
       // PV has ended, and with it every write of the flag
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
-      const size_t pslot = ((size_t)2 * cta + (starts ? 1 : 0)) * a.rows_cap + r;
+      const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
       const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
       if (active) {
         uint16_t *out = a.o + ((size_t)(w.s.lo + node0 + my_node) * a.Hq + w.g * a.G + my_head) * D;
@@ -645,13 +708,13 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
               *reinterpret_cast<uint4 *>(out + d + i) = x;
             }
           } else {
-            float *part = a.part + pslot * D + d;
+            uint4 *part = reinterpret_cast<uint4 *>(a.part) + (pslot * (D / 4) + d / 4) * a.rows_cap + r;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4 *>(part + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < 8; ++i)
+              part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (in && !whole) *reinterpret_cast<float2 *>(a.ml + pslot * 2) = make_float2(mx, sum);
+        if (in && !whole) *reinterpret_cast<float2 *>(a.ml + (pslot * a.rows_cap + r) * 2) = make_float2(mx, sum);
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&m->o_free);
@@ -668,48 +731,49 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
 }
 
 // o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
-// unit.  One to eight warps of a block take a row, about four parts each (a
-// unit is split over as few as two CTAs and as many as all of them): the lanes
-// first read every part's (m, l), so that the weights are known before the
-// parts' values, whose loads then do not wait for one another.
-constexpr int TJ_WARPS = 8;
+// unit.  A thread has four values of one row (rows run fastest, in the parts
+// as in the threads, so that a warp's accesses are whole lines); one to eight
+// warps of a block share the parts of the same values (a unit is split over
+// as few as two CTAs and as many as all of them).
+constexpr int TJ_THREADS = 256;
 
-__device__ __forceinline__ int warps_per_row(int parts) {
-  return parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : TJ_WARPS;
-}
+__device__ __forceinline__ int part_groups(int parts) { return parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8; }
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(TJ_WARPS * 32) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
-  constexpr int E = D / 32, MAXU = 2 * TR_MAX_SMS;  // values of a row a lane holds; split units at most
+__global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  constexpr int MAXU = 2 * TR_MAX_SMS, WARPS = TJ_THREADS / 32;  // MAXU: split units at most
   __shared__ SplitDesc desc_s[MAXU];
-  __shared__ int cta_s[MAXU], item_s[MAXU + 1], wsum[TJ_WARPS];
-  __shared__ float acc_s[TJ_WARPS][D];
+  __shared__ int cta_s[MAXU], item_s[MAXU + 1], wsum[WARPS];
+  __shared__ float4 acc_s[TJ_THREADS];
+  __shared__ float2 ml_s[TJ_THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the split units in the CTAs' order, and the row groups (items) before each
-  constexpr int PER = (MAXU + TJ_WARPS * 32 - 1) / (TJ_WARPS * 32);
+  // the split units in the CTAs' order, and the items (blocks of values) before each
+  const int vals = D / 4 * a.rows_cap;
+  constexpr int PER = (MAXU + TJ_THREADS - 1) / TJ_THREADS;
   SplitDesc d[PER];
-  int mine = 0, items = 0;
+  auto items_of = [&](const SplitDesc &x) {
+    const int each = TJ_THREADS / part_groups(x.parts);
+    return (vals + each - 1) / each;
+  };
+  int packed = 0;  // units << 20 | items: at most 320, and 320 * 64 * 128 / 32 below 2^17 of them
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = tid * PER + i;
     d[i].parts = 0;
     if (c < ctas) d[i] = a.desc[c];
-    if (d[i].parts > 0) {
-      ++mine;
-      items += (d[i].rows * warps_per_row(d[i].parts) + TJ_WARPS - 1) / TJ_WARPS;
-    }
+    if (d[i].parts > 0) packed += 1 << 20 | items_of(d[i]);
   }
-  int packed = mine << 20 | items;  // at most 320 units and 320 * 128 items
+  int before = packed, all = 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, packed, o);
-    if (lane >= o) packed += t;
+    const int t = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += t;
   }
-  if (lane == 31) wsum[warp] = packed;
+  if (lane == 31) wsum[warp] = before;
+  before -= packed;
   __syncthreads();
-  int before = packed - (mine << 20 | items), all = 0;
-  for (int w = 0; w < TJ_WARPS; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += wsum[w];
     all += wsum[w];
   }
@@ -721,7 +785,7 @@ __global__ void __launch_bounds__(TJ_WARPS * 32) tree_join_kernel(const __grid_c
       desc_s[u] = d[i];
       cta_s[u] = tid * PER + i;
       item_s[u] = before & 0xFFFFF;
-      before += 1 << 20 | (d[i].rows * warps_per_row(d[i].parts) + TJ_WARPS - 1) / TJ_WARPS;
+      before += 1 << 20 | items_of(d[i]);
     }
   if (tid == 0) item_s[units] = n_items;
   __syncthreads();
@@ -730,63 +794,73 @@ __global__ void __launch_bounds__(TJ_WARPS * 32) tree_join_kernel(const __grid_c
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
     while (item >= item_s[u + 1]) ++u;
     const SplitDesc ds = desc_s[u];
-    const int c0 = cta_s[u], wpr = warps_per_row(ds.parts), sub = warp % wpr;
-    const int r = (item - item_s[u]) * (TJ_WARPS / wpr) + warp / wpr;
-    const bool in = r < ds.rows;
-    // part i lies in CTA c0 + i's second slot if it starts the unit, else in its first
-    auto slot = [&](int i) { return ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * a.rows_cap + (in ? r : 0); };
+    const int c0 = cta_s[u], groups = part_groups(ds.parts), each = TJ_THREADS / groups, grp = tid / each;
+    const int e = (item - item_s[u]) * each + tid % each, r = e % a.rows_cap;
+    const bool in = e < vals && r < ds.rows;
     float M = -INFINITY, den = 0.f;
-    for (int i0 = 0; i0 < ds.parts; i0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (i0 + lane < ds.parts) ml = *reinterpret_cast<const float2 *>(a.ml + slot(i0 + lane) * 2);
-      float mx = ml.x;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      // part i lies in CTA c0 + i's second slot if it starts the unit, else in its first
+      for (int i0 = grp; i0 < ds.parts; i0 += 4 * groups) {
+        float2 ml[4];
+        float4 v[4];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(M, mx);
-      const float l = warp_sum(ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - mn));
-      den = (M == -INFINITY ? 0.f : den * ex2(M - mn)) + l;
-      M = mn;
-    }
-    float acc[E] = {};
-#pragma unroll 4
-    for (int i = sub; i < ds.parts; i += wpr) {
-      const size_t p = slot(i);
-      const float m = a.ml[p * 2];
-      const float f = m == -INFINITY ? 0.f : ex2(m - M);  // a part in which the row saw nothing adds zeros
-      alignas(16) float v[E];
-      const float *src = a.part + p * D + lane * E;
-      if constexpr (E >= 4) {
+        for (int q = 0; q < 4; ++q) {
+          const int i = i0 + q * groups;
+          ml[q] = make_float2(-INFINITY, 0.f);
+          v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < ds.parts) {
+            const size_t p = (size_t)2 * (c0 + i) + (i == 0 ? 1 : 0);
+            ml[q] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
+            v[q] = reinterpret_cast<const float4 *>(a.part)[p * vals + e];
+          }
+        }
+        const float mn = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        den *= f;
 #pragma unroll
-        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(src + e);
-      } else {
-        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
+        for (int q = 0; q < 4; ++q) {
+          const float h = ml[q].x == -INFINITY ? 0.f : ex2(ml[q].x - mn);  // a part in which the row saw nothing
+          acc.x = fmaf(v[q].x, h, acc.x);
+          acc.y = fmaf(v[q].y, h, acc.y);
+          acc.z = fmaf(v[q].z, h, acc.z);
+          acc.w = fmaf(v[q].w, h, acc.w);
+          den = fmaf(ml[q].y, h, den);
+        }
+        M = mn;
       }
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], f, acc[e]);
     }
-    if (wpr > 1) {
+    if (groups > 1) {
       __syncthreads();  // the last item's readers are done
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc_s[warp][e * 32 + lane] = acc[e];
+      acc_s[tid] = acc;
+      ml_s[tid] = make_float2(M, den);
       __syncthreads();
-      if (sub == 0)
-        for (int w = 1; w < wpr; ++w)
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += acc_s[warp + w][e * 32 + lane];
+      if (grp == 0 && in) {
+        float mn = M;
+        for (int g = 1; g < groups; ++g) mn = fmaxf(mn, ml_s[g * each + tid].x);
+        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        den *= f;
+        for (int g = 1; g < groups; ++g) {
+          const float2 ml = ml_s[g * each + tid];
+          const float4 v = acc_s[g * each + tid];
+          const float h = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+          acc.x = fmaf(v.x, h, acc.x);
+          acc.y = fmaf(v.y, h, acc.y);
+          acc.z = fmaf(v.z, h, acc.z);
+          acc.w = fmaf(v.w, h, acc.w);
+          den = fmaf(ml.y, h, den);
+        }
+      }
     }
-    if (in && sub == 0) {
+    if (in && grp == 0) {
       const float inv = den == 0.f ? 0.f : 1.f / den;
-      alignas(16) uint32_t x[E / 2];
-#pragma unroll
-      for (int e = 0; e < E; e += 2) x[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+      uint2 x;
+      x.x = pack2<FP16>(acc.x * inv, acc.y * inv);
+      x.y = pack2<FP16>(acc.z * inv, acc.w * inv);
       const int node = ds.node0 + r / a.G, head = ds.head0 + r % a.G;
-      uint16_t *out = a.o + ((size_t)node * a.Hq + head) * D + lane * E;
-      if constexpr (E == 8)
-        *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<uint4 *>(x);
-      else if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<uint2 *>(x);
-      else
-        *reinterpret_cast<uint32_t *>(out) = x[0];
+      *reinterpret_cast<uint2 *>(a.o + ((size_t)node * a.Hq + head) * D + e / a.rows_cap * 4) = x;
     }
   }
 }
@@ -841,7 +915,7 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(TR_THREADS), Cfg<D>::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
-  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_WARPS * 32), 0, s, a, ctas);
+  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_THREADS), 0, s, a, ctas);
 }
 
 }  // namespace
