@@ -12,8 +12,8 @@
 // leaves partial results (m, l, O in fp32), which a second kernel joins.
 //
 // Roles: warp 4 loads (TMA: pages by the table's numbers, K one tile ahead
-// of V, into a ring), one thread of warp 5 issues the MMAs (S of the next tile
-// before O of this one), warps 0-3 own the rows.  Rescaling O on a new maximum
+// of V, into a ring), warp 5 issues the MMAs (S of the next tile before O of
+// this one; at D = 256 warp 6 issues those of O), warps 0-3 own the rows.  Rescaling O on a new maximum
 // is put off while the maximum grows by less than 2^8: P then stays within
 // 2^8 and the fp32 sums lose nothing.
 // Every wait is bounded: after one second the kernel records
@@ -34,7 +34,6 @@ namespace {
 constexpr int TR_MAXN = 256;      // nodes of a tree
 constexpr int TR_ROWS = 128;      // rows of a unit (MMA M)
 constexpr int TR_TILE = 64;       // positions of a tile
-constexpr int TR_THREADS = 192;
 constexpr int TR_MAX_SMS = 160;   // SMs used at most (the workspace is sized for them)
 constexpr float TR_SLACK = 8.f;   // growth of the maximum (log2) that O is not rescaled for
 constexpr unsigned long long TR_TIMEOUT_NS = 1000000000ull;
@@ -43,6 +42,10 @@ template <int D>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;             // 128-byte columns of a row
   static constexpr int CTAS = D == 256 ? 1 : 2;     // per SM
+  // one thread issues an MMA every 50 cycles or so: the scores' MMAs (N = 64,
+  // 32 cycles each) have a warp of their own where one CTA has the SM
+  static constexpr int ISSUERS = D == 256 ? 2 : 1;
+  static constexpr int WARPS = 5 + ISSUERS, THREADS = WARPS * 32;
   static constexpr int Q_CHUNK = TR_ROWS * 128;     // bytes of one column of Q
   static constexpr int KV_CHUNK = TR_TILE * 128;    // of a K or V tile
   static constexpr int SLOT = CHUNKS * KV_CHUNK;    // one K or V tile
@@ -97,7 +100,7 @@ struct Misc {
   uint32_t tmem;
   int abort_flag, nonfinite;
   int b0;
-  long long off0, wsum[TR_THREADS / 32];
+  long long off0, wsum[8];
   int16_t parent[TR_MAXN];
 };
 static_assert(sizeof(Misc) <= 1024, "misc area");
@@ -130,9 +133,9 @@ __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) 
 }
 
 // x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
-__device__ __forceinline__ long long mul_div(long long x, int y, int z) {
+__device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
   const long long p = x * y;
-  return p < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
+  return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
 // A CTA's walk over the units of its run of tiles.
@@ -249,7 +252,7 @@ __device__ __forceinline__ uint32_t v_pos(int j, int n) {
 }
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
-  const int per = (a.B + TR_THREADS - 1) / TR_THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
+  const int per = (a.B + C::THREADS - 1) / C::THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
   long long mine = 0;
   for (int b = sb; b < se; ++b) mine += seq_tiles(a, load_seq(a, b));
   long long inc = mine;
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
     }
     ptx::mbar_init(&m->o_free, TR_ROWS);
     ptx::mbar_init(&m->rows_bar, TR_ROWS);
-    ptx::mbar_init(&m->final_bar, 1);
+    ptx::mbar_init(&m->final_bar, C::ISSUERS);
     ptx::fence_mbar_init();
   }
   ptx::tc_fence_before();
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
   ptx::tc_fence_after();
   const uint32_t tmem = m->tmem;
   long long before = inc - mine, T = 0;
-  for (int w = 0; w < TR_THREADS / 32; ++w) {
+  for (int w = 0; w < C::WARPS; ++w) {
     if (w < warp) before += m->wsum[w];
     T += m->wsum[w];
   }
@@ -411,8 +414,9 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
         tr_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
     }
-  } else if (warp == 5) {
+  } else if (warp >= 5) {
     // ----------------------------------------------------------------- MMAs
+    const bool does_s = warp == 5, does_o = C::ISSUERS == 1 || warp == 6;
     const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
     const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
     uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
@@ -442,33 +446,41 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       __syncwarp();
       return true;
     };
-    while (ok && w.next()) {
-      ok = tr_wait_warp(C::Q_TMEM ? &m->q_ready : &m->q_full, units & 1u, m, status);
-      if (ok && C::Q_TMEM && ptx::elect_one())
-        for (int h = 0; h < C::Q_SLOTS; ++h) ptx::mbar_arrive(&m->empty[(ld + h) % C::NS]);
-      __syncwarp();
-      ok = ok && scores(ld + k_pos<D>(0), jj);
-      for (int j = 0; ok && j < w.n; ++j, ++jj) {
-        if (j + 1 < w.n) ok = scores(ld + k_pos<D>(j + 1), jj + 1);
-        if (!ok) break;
-        const bool q_done = j + 2 >= w.n && (j + 1 < w.n || w.n == 1);  // the unit's last scores are under way
-        if (!C::Q_TMEM && q_done && ptx::elect_one()) ptx::mma_commit(&m->q_free);
-        const uint32_t pos = ld + v_pos<D>(j, w.n), slot = pos % C::NS;
-        ok = tr_wait_warp(&m->p_ready[jj & 1], (jj >> 1) & 1u, m, status) &&
-             tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status) &&
-             (j > 0 || units == 0 || tr_wait_warp(&m->o_free, (units - 1) & 1u, m, status));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
-        const uint32_t p_col = tmem + C::S_COL + (jj & 1) * TR_TILE;
-        if (ptx::elect_one()) {
+    auto values = [&](uint32_t pos, uint32_t t, bool first) {  // O += P V of running tile t
+      const uint32_t slot = pos % C::NS;
+      if (!tr_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
+          !tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status) ||
+          (first && units > 0 && !tr_wait_warp(&m->o_free, (units - 1) & 1u, m, status)))
+        return false;
+      ptx::tc_fence_after();
+      const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
+      const uint32_t p_col = tmem + C::S_COL + (t & 1) * TR_TILE;
+      if (ptx::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < TR_TILE / 16; ++i)
-            ptx::mma_ts(tmem, p_col + 8 * i, vd + i * 2048 / 16, id_o, j > 0 || i > 0);
-          ptx::mma_commit(&m->empty[slot]);
-          ptx::mma_commit(&m->pv_done[jj & 1]);
-        }
+        for (int i = 0; i < TR_TILE / 16; ++i)
+          ptx::mma_ts(tmem, p_col + 8 * i, vd + i * 2048 / 16, id_o, !first || i > 0);
+        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->pv_done[t & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && w.next()) {
+      if (does_s) {
+        ok = tr_wait_warp(C::Q_TMEM ? &m->q_ready : &m->q_full, units & 1u, m, status);
+        if (ok && C::Q_TMEM && ptx::elect_one())  // the rows have copied Q out of its slots
+          for (int h = 0; h < C::Q_SLOTS; ++h) ptx::mbar_arrive(&m->empty[(ld + h) % C::NS]);
         __syncwarp();
+        ok = ok && scores(ld + k_pos<D>(0), jj);
+      }
+      for (int j = 0; ok && j < w.n; ++j, ++jj) {
+        if (does_s) {
+          if (j + 1 < w.n) ok = scores(ld + k_pos<D>(j + 1), jj + 1);
+          // the unit's last scores are under way
+          if (ok && !C::Q_TMEM && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
+          __syncwarp();
+        }
+        if (ok && does_o) ok = values(ld + v_pos<D>(j, w.n), jj, j == 0);
       }
       ld += C::Q_SLOTS + 2 * w.n;
       ++units;
@@ -489,82 +501,161 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
       ptx::mbar_arrive(&m->rows_bar);
       return tr_wait_warp(&m->rows_bar, syncs++ & 1u, m, status);
     };
-    while (ok && w.next()) {
-      const int L = w.s.L, n_old = tiles_of(L), nodes = w.nodes(), rows = nodes * a.G, node0 = w.node0();
-      const bool in = r < rows;
-      // the tree's parents, and what this row's node sees of each tile of nodes
-      if (!rows_sync()) break;  // the last unit's readers are done
-      for (int i = r; i < w.s.n; i += TR_ROWS) {
-        int p = a.parent[w.s.lo + i];
-        if (p >= i || p < -2) {
-          set_status(status, MOE_ERR_DEVICE_BOUNDS);
-          p = -2;
-        }
-        m->parent[i] = (int16_t)p;
+    // The unit whose tiles were the last: its result is taken out of tensor
+    // memory only once the next unit's queries are in, so that its scores run meanwhile.
+    struct Unit {
+      int lo, nodes, node0, rows, g, n_old, t0, n, nt_all;
+      long long done;  // tiles of all units up to the end of this CTA's part
+    } un{};
+    float mx = -INFINITY, sum = 0.f;
+    bool in = false, real = false;
+    unsigned long long sees[TR_MAXN / TR_TILE] = {};
+    auto finish = [&]() {
+      if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
+      ptx::tc_fence_after();
+      const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
+      if (!whole && starts) {
+        const long long u1 = un.done - un.n + un.nt_all;  // the unit's end among all tiles
+        split = SplitDesc{(int)mul_div(u1 * ctas + T - 1, 1, T) - cta, un.rows, un.lo + un.node0, un.g * a.G};
       }
-      if (r == 0) m->nonfinite = 0;
-      if (!rows_sync()) break;
-      unsigned long long sees[TR_MAXN / TR_TILE] = {};
-      bool real = false;
-      if (in) {
-        int i = node0 + my_node;
-        real = m->parent[i] != -2;
-        while (real && i >= 0) {
-#pragma unroll
-          for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
-            if (i / TR_TILE == q) sees[q] |= 1ull << (i % TR_TILE);
-          i = m->parent[i];
-        }
-      }
-      if constexpr (C::Q_TMEM) {
-        // this row of Q from the ring into tensor memory (the last unit's
-        // scores, which read the one before, are done)
+      // PV has ended, and with it every write of the flag
+      const bool fix = un.t0 + un.n > un.n_old && *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
+      const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      if (warp * 32 < un.rows) {
+        uint16_t *out = a.o + ((size_t)(un.lo + un.node0 + my_node) * a.Hq + un.g * a.G + my_head) * D;
 #pragma unroll 1
-        for (int h = 0; ok && h < C::Q_SLOTS; ++h) {
-          const uint32_t slot = (ld + h) % C::NS;
-          ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status);
-          if (!ok) break;
+        for (int d = 0; d < D; d += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          ptx::tmem_ld_x32(lanes + d, v);
+          ptx::tmem_wait_ld();
+          if (!in) continue;
+          if (fix && real) {
+            for (int i = 0; i < un.nodes; ++i) {
+              const int t = un.n_old + i / TR_TILE;
+              if (t < un.t0 || t >= un.t0 + un.n || !(sees[i / TR_TILE] >> (i % TR_TILE) & 1)) continue;
+              const uint16_t *src = a.v_new + (size_t)(un.lo + i) * a.c.row + un.g * D + d;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t x[32];
-            const uint8_t *src = ring + slot * C::SLOT + i * C::Q_CHUNK + r * 128;
+              for (int q = 0; q < 32; ++q) {
+                const uint32_t h = src[q];
+                if ((h & EXP_MASK<FP16>) == EXP_MASK<FP16>)
+                  v[q] = __float_as_uint(__uint_as_float(v[q]) + value<FP16>(h));
+              }
+            }
+          }
+          if (whole) {
+            if (sum == 0.f) {  // a row that sees nothing
 #pragma unroll
-            for (int p = 0; p < 8; ++p)  // 16-byte pieces, swizzled by the row
-              *reinterpret_cast<uint4 *>(x + 4 * p) = *reinterpret_cast<const uint4 *>(src + ((p ^ (r & 7)) * 16));
-            ptx::tmem_st_x32(lanes + C::Q_COL + (2 * h + i) * 32, x);
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 x;
+              x.x = pack2<FP16>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+              x.y = pack2<FP16>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+              x.z = pack2<FP16>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+              x.w = pack2<FP16>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+              *reinterpret_cast<uint4 *>(out + d + i) = x;
+            }
+          } else {
+            uint4 *part = reinterpret_cast<uint4 *>(a.part) + (pslot * (D / 4) + d / 4) * a.rows_cap + r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (!ok) break;
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&m->q_ready);
+        if (in && !whole)
+          *reinterpret_cast<float2 *>(a.ml + (pslot * a.rows_cap + r) * 2) = make_float2(mx, sum);
       }
-      const bool active = warp * 32 < rows;                             // the warp has rows
-      const bool all_real = __all_sync(0xffffffffu, real || !in);       // none of them is padding
-      float mx = -INFINITY, sum = 0.f;
-      for (int j = 0; j < w.n; ++j, ++jj) {
-        const int t = w.t0 + j;
-        const bool edge = t >= n_old || (t + 1) * TR_TILE > L;
-        if (!tr_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, m, status)) {
-          ok = false;
-          break;
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&m->o_free);
+      __syncwarp();
+      return true;
+    };
+    while (ok) {
+      const bool more = w.next();
+      int up[2] = {-2, -2}, own = -2;  // parents of nodes r and r + 128, and of this row's node
+      if (more) {
+        const int32_t *parent = a.parent + w.s.lo;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (r + i * TR_ROWS < w.s.n) up[i] = __ldg(parent + r + i * TR_ROWS);
+        if (my_node < w.nodes()) own = __ldg(parent + w.node0() + my_node);
+        if constexpr (C::Q_TMEM) {
+          // this row of Q from the ring into tensor memory (the last unit's
+          // scores, which read the one before, are done)
+#pragma unroll 1
+          for (int h = 0; ok && h < C::Q_SLOTS; ++h) {
+            const uint32_t slot = (ld + h) % C::NS;
+            ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t x[32];
+              const uint8_t *src = ring + slot * C::SLOT + i * C::Q_CHUNK + r * 128;
+#pragma unroll
+              for (int p = 0; p < 8; ++p)  // 16-byte pieces, swizzled by the row
+                *reinterpret_cast<uint4 *>(x + 4 * p) = *reinterpret_cast<const uint4 *>(src + ((p ^ (r & 7)) * 16));
+              ptx::tmem_st_x32(lanes + C::Q_COL + (2 * h + i) * 32, x);
+            }
+          }
+          if (!ok) break;
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&m->q_ready);
         }
+      }
+      if (un.n > 0) ok = finish();
+      if (!more || !ok) break;
+      const int L = w.s.L, n_old = tiles_of(L);
+      un = Unit{w.s.lo, w.s.n, w.node0(), w.nodes() * a.G, w.g, n_old, w.t0, w.n, w.nt_all, end - w.left};
+      in = r < un.rows;
+      real = in && own >= -1 && own < un.node0 + my_node;
+      const bool active = warp * 32 < un.rows;                     // the warp has rows
+      const bool all_real = __all_sync(0xffffffffu, real || !in);  // none of them is padding
+#pragma unroll
+      for (int q = 0; q < TR_MAXN / TR_TILE; ++q) sees[q] = 0;
+      mx = -INFINITY;
+      sum = 0.f;
+      for (int j = 0; j < un.n; ++j, ++jj) {
+        const int t = un.t0 + j;
+        const bool edge = t >= n_old || (t + 1) * TR_TILE > L;
+        if (t >= n_old && (j == 0 || t == n_old)) {
+          // the first of the tree's own tiles: its parents, and what this row's node sees of each tile
+          if (!(ok = rows_sync())) break;  // the last unit's readers are done
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (r + i * TR_ROWS < un.nodes) {
+              if (up[i] >= r + i * TR_ROWS || up[i] < -2) {
+                set_status(status, MOE_ERR_DEVICE_BOUNDS);
+                up[i] = -2;
+              }
+              m->parent[r + i * TR_ROWS] = (int16_t)up[i];
+            }
+          if (r == 0) m->nonfinite = 0;
+          if (!(ok = rows_sync())) break;
+          for (int i = real ? un.node0 + my_node : -1; i >= 0; i = m->parent[i]) {
+#pragma unroll
+            for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
+              if (i / TR_TILE == q) sees[q] |= 1ull << (i % TR_TILE);
+          }
+          __syncwarp();
+        }
+        if (!(ok = tr_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, m, status))) break;
         ptx::tc_fence_after();
         if (edge) {
           // V rows that nobody may see become zeros (0 x NaN is NaN), and in the
-          // tree's own tiles non-finite values as well: they are added below to
+          // tree's own tiles non-finite values as well: finish() adds them to
           // the rows that see them
-          const uint32_t pos = ld + v_pos<D>(j, w.n), slot = pos % C::NS;
-          if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) {
-            ok = false;
-            break;
-          }
+          const uint32_t pos = ld + v_pos<D>(j, un.n), slot = pos % C::NS;
+          if (!(ok = tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))) break;
           uint8_t *v = ring + slot * C::SLOT;
           for (int e = r; e < TR_TILE * C::CHUNKS * 8; e += TR_ROWS) {  // 16-byte pieces
             const int ch = e / (TR_TILE * 8), q = (e / 8) % TR_TILE;
             uint4 *piece = reinterpret_cast<uint4 *>(v + ch * C::KV_CHUNK + q * 128 + (e & 7) * 16);
             const int at = t < n_old ? t * TR_TILE + q : (t - n_old) * TR_TILE + q;
-            const bool hold = t < n_old ? at < L : at < w.s.n && m->parent[at] != -2;
+            const bool hold = t < n_old ? at < L : at < un.nodes && m->parent[at] != -2;
             if (!hold) {
               *piece = make_uint4(0u, 0u, 0u, 0u);
             } else if (t >= n_old) {
@@ -619,10 +710,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
             if (grows) mx = tmax;
             sum *= f;
             if (j > 0) {  // O holds the earlier tiles
-              if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) {
-                ok = false;
-                break;
-              }
+              if (!(ok = tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
               ptx::tc_fence_after();
 #pragma unroll 1
               for (int d = 0; d < D; d += 32) {
@@ -658,66 +746,7 @@ __global__ void __launch_bounds__(TR_THREADS, Cfg<D>::CTAS)
         ptx::tc_fence_before();
         ptx::mbar_arrive(&m->p_ready[jj & 1]);
       }
-      if (!ok) break;
-      ld += C::Q_SLOTS + 2 * w.n;
-      // the unit's result, or this CTA's part of it
-      if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) break;
-      ptx::tc_fence_after();
-      const bool whole = w.n == w.nt_all, starts = w.t0 == 0;
-      if (!whole && starts) {
-        const long long u1 = end - w.left - w.n + w.nt_all;  // the unit's end among all tiles
-        split = SplitDesc{(int)((u1 * ctas + T - 1) / T) - cta, rows, w.s.lo + node0, w.g * a.G};
-      }
-      // PV has ended, and with it every write of the flag
-      const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
-      const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
-      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      if (active) {
-        uint16_t *out = a.o + ((size_t)(w.s.lo + node0 + my_node) * a.Hq + w.g * a.G + my_head) * D;
-#pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          ptx::tmem_ld_x32(lanes + d, v);
-          ptx::tmem_wait_ld();
-          if (!in) continue;
-          if (fix && real) {
-            for (int i = 0; i < w.s.n; ++i) {
-              const int t = n_old + i / TR_TILE;
-              if (t < w.t0 || t >= w.t0 + w.n || !(sees[i / TR_TILE] >> (i % TR_TILE) & 1)) continue;
-              const uint16_t *src = a.v_new + (size_t)(w.s.lo + i) * a.c.row + w.g * D + d;
-#pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                const uint32_t h = src[q];
-                if ((h & EXP_MASK<FP16>) == EXP_MASK<FP16>) v[q] = __float_as_uint(__uint_as_float(v[q]) + value<FP16>(h));
-              }
-            }
-          }
-          if (whole) {
-            if (sum == 0.f) {  // a row that sees nothing
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 x;
-              x.x = pack2<FP16>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
-              x.y = pack2<FP16>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-              x.z = pack2<FP16>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
-              x.w = pack2<FP16>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
-              *reinterpret_cast<uint4 *>(out + d + i) = x;
-            }
-          } else {
-            uint4 *part = reinterpret_cast<uint4 *>(a.part) + (pslot * (D / 4) + d / 4) * a.rows_cap + r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-        if (in && !whole) *reinterpret_cast<float2 *>(a.ml + (pslot * a.rows_cap + r) * 2) = make_float2(mx, sum);
-      }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(&m->o_free);
+      ld += C::Q_SLOTS + 2 * un.n;
     }
     if (r == 0) a.desc[cta] = split;
   }
@@ -912,7 +941,7 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   if (e != cudaSuccess) return e;
   prof_before(MOE_KERNEL_ATTN_TREE, s);
   const bool quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
-  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(TR_THREADS), Cfg<D>::SMEM, s, maps, a);
+  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(Cfg<D>::THREADS), Cfg<D>::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
   return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_THREADS), 0, s, a, ctas);
