@@ -11,9 +11,10 @@
 // into one equal run per CTA, whatever the lengths: a unit that spans CTAs
 // leaves partial results (m, l, O in fp32), which a second kernel joins.
 //
-// Roles: warp 4 loads (TMA: pages by the table's numbers, K one tile ahead
-// of V, into a ring), warp 5 issues the MMAs (S of the next tile before O of
-// this one; at D = 256 warp 6 issues those of O), warps 0-3 own the rows.  Rescaling O on a new maximum
+// Roles: the first four warps own the rows (at D = 256 eight, two threads a
+// row), the next loads (TMA: pages by the table's numbers, K one tile ahead of
+// V, into a ring), the next issues the MMAs (S of the next tile before O of
+// this one; at D = 256 the last issues those of O).  Rescaling O on a new maximum
 // is put off while the maximum grows by less than 2^8: P then stays within
 // 2^8 and the fp32 sums lose nothing.
 // Every wait is bounded: after one second the kernel records
@@ -45,7 +46,13 @@ struct Cfg {
   // one thread issues an MMA every 50 cycles or so: the scores' MMAs (N = 64,
   // 32 cycles each) have a warp of their own where one CTA has the SM
   static constexpr int ISSUERS = D == 256 ? 2 : 1;
-  static constexpr int WARPS = 5 + ISSUERS, THREADS = WARPS * 32;
+  // threads of a row, each with 64 / HALVES columns of S and D / HALVES of O
+  // (two CTAs have no registers for more than one)
+  static constexpr int HALVES = D == 256 ? 2 : 1;
+  static constexpr int ROW_WARPS = 4 * HALVES, LOADER = ROW_WARPS, WARPS = ROW_WARPS + 1 + ISSUERS;
+  static constexpr int THREADS = WARPS * 32;
+  // what a unit costs besides its tiles (its start and its result), in tiles
+  static constexpr int OVERHEAD = D == 256 ? 2 : 1;
   static constexpr int Q_CHUNK = TR_ROWS * 128;     // bytes of one column of Q
   static constexpr int KV_CHUNK = TR_TILE * 128;    // of a K or V tile
   static constexpr int SLOT = CHUNKS * KV_CHUNK;    // one K or V tile
@@ -59,7 +66,7 @@ struct Cfg {
   static constexpr int NS = D == 256 ? 7 : D == 128 ? 4 : 10;  // ring slots: what fits in 227 KB, or half of that
   static constexpr int OFF_RING = Q_TMEM ? 0 : CHUNKS * Q_CHUNK;
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
-  static constexpr int SMEM = OFF_MISC + 1024 + 1024 /* alignment slack */;
+  static constexpr int SMEM = OFF_MISC + 3 * 1024;
   static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
   // tensor memory columns: O, Q, two S tiles, each turned into P in place
   static constexpr uint32_t Q_COL = D, S_COL = Q_COL + (Q_TMEM ? D / 2 : 0);
@@ -94,20 +101,22 @@ struct TreeArgs {
   float scale_log2;
 };
 
-struct Misc {
-  uint64_t full[10], empty[10];
-  uint64_t q_full, q_free, q_ready, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, final_bar;
-  uint32_t tmem;
-  int abort_flag, nonfinite;
-  int b0;
-  long long off0, wsum[8];
-  int16_t parent[TR_MAXN];
-};
-static_assert(sizeof(Misc) <= 1024, "misc area");
-
 struct Seq {
   int slot, L, lo, n;  // n == 0: nothing to do
 };
+
+struct Misc {
+  uint64_t full[10], empty[10];
+  uint64_t q_full, q_free, q_ready, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, pair_bar[4], final_bar;
+  uint32_t tmem;
+  int abort_flag, nonfinite;
+  int b0;
+  Seq s0;
+  long long off0, wsum[12];
+  int16_t parent[TR_MAXN];
+  float row[2][2][TR_ROWS];  // what the two threads of a row exchange, [turn][half]
+};
+static_assert(sizeof(Misc) <= 3 * 1024, "misc area");
 
 __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
   // the loads first: none of them waits for another's check
@@ -127,9 +136,10 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
 
 __device__ __forceinline__ int tiles_of(int n) { return (n + TR_TILE - 1) / TR_TILE; }
 
+template <int OVH>
 __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
   if (s.n == 0) return 0;
-  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (tiles_of(s.L) + tiles_of(s.n));
+  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (OVH + tiles_of(s.L) + tiles_of(s.n));
 }
 
 // x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
@@ -138,48 +148,52 @@ __device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
   return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
-// A CTA's walk over the units of its run of tiles.
+// A CTA's walk over the units of its run.  A unit counts OVH + its tiles, the
+// overhead first, so that a CTA with more units has fewer tiles.
+template <int OVH>
 struct Walk {
   const TreeArgs &a;
   int b;
-  long long left;  // tiles of the run still to come
+  long long left;  // of the run, still to come
   Seq s;
-  int g, rt, t0;   // unit, and its first tile that is this CTA's
+  int g, rt, off;  // unit, and where in its count the run's part begins
   int nt_all;      // tiles of the unit
-  int n;           // of them this CTA's
+  int t0, n;       // this CTA's: the first, and how many
   bool fresh;
 
-  __device__ Walk(const TreeArgs &a_, int b0, long long off, long long count) : a(a_), b(b0), left(count) {
-    if (left <= 0) return;
-    s = load_seq(a, b);
+  __device__ Walk(const TreeArgs &a_, int b0, const Seq &s0, long long off0, long long count)
+      : a(a_), b(b0), left(count), s(s0), fresh(true) {
     nt_all = tiles_of(s.L) + tiles_of(s.n);
-    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)mul_div(off, 1, nt_all);
+    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)mul_div(off0, 1, OVH + nt_all);
     g = u / rts;
     rt = u - g * rts;
-    t0 = (int)(off - (long long)u * nt_all);
-    fresh = true;
+    off = (int)(off0 - (long long)u * (OVH + nt_all));
   }
-  // the next unit; false when the run is done
+  // the next unit with tiles for this CTA; false when the run is done
   __device__ bool next() {
-    if (left <= 0) return false;
-    if (!fresh) {
-      t0 = 0;
-      if (++rt * a.nt >= s.n) {
-        rt = 0;
-        if (++g >= a.Hkv) {
-          g = 0;
-          do {  // left > 0: a later sequence has tiles
-            s = load_seq(a, ++b);
-          } while (s.n == 0 && b + 1 < a.B);
-          if (s.n == 0) return false;
-          nt_all = tiles_of(s.L) + tiles_of(s.n);
+    while (left > 0) {
+      if (!fresh) {
+        off = 0;
+        if (++rt * a.nt >= s.n) {
+          rt = 0;
+          if (++g >= a.Hkv) {
+            g = 0;
+            do {  // left > 0: a later sequence has tiles
+              s = load_seq(a, ++b);
+            } while (s.n == 0 && b + 1 < a.B);
+            if (s.n == 0) return false;
+            nt_all = tiles_of(s.L) + tiles_of(s.n);
+          }
         }
       }
+      fresh = false;
+      const int take = (int)(left < OVH + nt_all - off ? left : (long long)(OVH + nt_all - off));
+      left -= take;
+      t0 = max(0, off - OVH);
+      n = max(0, off + take - OVH) - t0;
+      if (n > 0) return true;
     }
-    fresh = false;
-    n = (int)(left < nt_all - t0 ? left : (long long)(nt_all - t0));
-    left -= n;
-    return true;
+    return false;
   }
   __device__ int node0() const { return rt * a.nt; }
   __device__ int nodes() const { return min(a.nt, s.n - rt * a.nt); }
@@ -255,23 +269,62 @@ template <int D, bool FP16>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
   Misc *m = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the joining kernel may be scheduled now; it waits for this grid to finish
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // This CTA's run of tiles: every thread adds up some sequences' tiles, a
-  // scan gives their places, and the thread whose sequences hold the run's first tile
-  // writes down where that is.
-  if (warp == 5) {
+  if (ptx::smem_u32(smem) & 1023u) {  // not placed as declared: no kernel then, rather than wrong tiles
+    if (tid == 0) {
+      set_status(a.c.status, MOE_ERR_UNSUPPORTED);
+      a.desc[blockIdx.x].parts = 0;
+    }
+    return;
+  }
+  if (warp == C::LOADER && lane == 0) {
+    ptx::prefetch_tmap(&maps.q);
+    ptx::prefetch_tmap(&maps.k);
+    ptx::prefetch_tmap(&maps.v);
+    ptx::prefetch_tmap(&maps.k_new);
+    ptx::prefetch_tmap(&maps.v_new);
+  }
+  if (warp == C::LOADER + 1) {
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
+  // This CTA's run: every thread adds up some sequences' units, a scan gives
+  // their places, and the thread whose sequences hold the run's start writes
+  // down where that is.
   const int per = (a.B + C::THREADS - 1) / C::THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
+  Seq seq{0, 0, 0, 0};
   long long mine = 0;
-  for (int b = sb; b < se; ++b) mine += seq_tiles(a, load_seq(a, b));
+  for (int b = sb; b < se; ++b) {
+    seq = load_seq(a, b);
+    mine += seq_tiles<C::OVERHEAD>(a, seq);
+  }
+  if (tid >= 32 && tid < 32 + C::NS) {
+    ptx::mbar_init(&m->full[tid - 32], 1);
+    ptx::mbar_init(&m->empty[tid - 32], 1);
+    ptx::fence_mbar_init();
+  } else if (tid == 64) {
+    m->abort_flag = 0;
+    ptx::mbar_init(&m->q_full, 1);
+    ptx::mbar_init(&m->q_free, 1);
+    ptx::mbar_init(&m->q_ready, C::ROW_WARPS);
+    ptx::mbar_init(&m->final_bar, C::ISSUERS);
+    ptx::fence_mbar_init();
+  } else if (tid == 96) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&m->s_full[i], 1);
+      ptx::mbar_init(&m->p_ready[i], C::ROW_WARPS);
+      ptx::mbar_init(&m->pv_done[i], 1);
+    }
+    ptx::mbar_init(&m->o_free, C::ROW_WARPS);
+    ptx::mbar_init(&m->rows_bar, C::ROW_WARPS);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(&m->pair_bar[i], C::HALVES);
+    ptx::fence_mbar_init();
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -279,58 +332,43 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     if (lane >= o) inc += t;
   }
   if (lane == 31) m->wsum[warp] = inc;
-  if (tid == 0) {
-    m->abort_flag = 0;
-    for (int i = 0; i < C::NS; ++i) {
-      ptx::mbar_init(&m->full[i], 1);
-      ptx::mbar_init(&m->empty[i], 1);
-    }
-    ptx::mbar_init(&m->q_full, 1);
-    ptx::mbar_init(&m->q_free, 1);
-    ptx::mbar_init(&m->q_ready, TR_ROWS);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&m->s_full[i], 1);
-      ptx::mbar_init(&m->p_ready[i], TR_ROWS);
-      ptx::mbar_init(&m->pv_done[i], 1);
-    }
-    ptx::mbar_init(&m->o_free, TR_ROWS);
-    ptx::mbar_init(&m->rows_bar, TR_ROWS);
-    ptx::mbar_init(&m->final_bar, C::ISSUERS);
-    ptx::fence_mbar_init();
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = m->tmem;
   long long before = inc - mine, T = 0;
+#pragma unroll
   for (int w = 0; w < C::WARPS; ++w) {
     if (w < warp) before += m->wsum[w];
     T += m->wsum[w];
   }
   const int ctas = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x), cta = blockIdx.x;
-  if (cta >= ctas) {  // fewer tiles than CTAs
+  if (cta >= ctas) {  // less to do than CTAs
     if (tid == 0) a.desc[cta].parts = 0;
-    if (warp == 5) ptx::tmem_dealloc(tmem, C::TMEM);
+    if (warp == C::LOADER + 1) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
   const long long first = mul_div(T, cta, ctas), end = mul_div(T, cta + 1, ctas);
   if (first >= before && first < before + mine) {
     long long at = before;
     int b = sb;
-    for (;; ++b) {
-      const long long t = seq_tiles(a, load_seq(a, b));
-      if (first < at + t) break;
-      at += t;
-    }
+    if (per > 1)
+      for (;; ++b) {
+        seq = load_seq(a, b);
+        const long long t = seq_tiles<C::OVERHEAD>(a, seq);
+        if (first < at + t) break;
+        at += t;
+      }
     m->b0 = b;
+    m->s0 = seq;
     m->off0 = first - at;
   }
   __syncthreads();
-  Walk w(a, m->b0, m->off0, end - first);
+  Walk<C::OVERHEAD> w(a, m->b0, m->s0, m->off0, end - first);
   uint8_t *ring = smem + C::OFF_RING;
   int32_t *status = a.c.status;
 
-  if (warp == 4) {
+  if (warp == C::LOADER) {
     // ---------------------------------------------------------------- loads
     const int pool_rows = a.c.n_pages << a.c.page_shift;
     const int boxes = TR_TILE / a.page_box;  // table entries of a tile
@@ -414,9 +452,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
         tr_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
     }
-  } else if (warp >= 5) {
+  } else if (warp > C::LOADER) {
     // ----------------------------------------------------------------- MMAs
-    const bool does_s = warp == 5, does_o = C::ISSUERS == 1 || warp == 6;
+    const bool does_s = warp == C::LOADER + 1, does_o = C::ISSUERS == 1 || !does_s;
     const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
     const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
     uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
@@ -491,21 +529,36 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     tr_drain(&m->final_bar, 0);
   } else {
     // ----------------------------------------------------------------- rows
-    const int r = tid;
+    constexpr int COLS = TR_TILE / C::HALVES, OCOLS = D / C::HALVES;  // this thread's columns of S and of O
+    const int r = tid & (TR_ROWS - 1), half = tid / TR_ROWS;
     const int my_node = r / a.G, my_head = r - my_node * a.G;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t ld = 0, jj = 0, syncs = 0;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t ld = 0, jj = 0, syncs = 0, pairs = 0;
     bool ok = true;
     SplitDesc split{0, 0, 0, 0};
-    auto rows_sync = [&]() {  // the four warps meet (a wait that can give up, as all others)
-      ptx::mbar_arrive(&m->rows_bar);
+    // one arrival a warp, for all of its lanes
+    auto arrive = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    auto rows_sync = [&]() {  // all row warps meet (a wait that can give up, as all others)
+      arrive(&m->rows_bar);
       return tr_wait_warp(&m->rows_bar, syncs++ & 1u, m, status);
+    };
+    // the value of the row's other thread; the two warps meet here (two buffers
+    // in turn: who writes one again has met the other's reader since)
+    auto exchange = [&](float v, bool &got) {
+      const uint32_t turn = pairs++ & 1u;
+      m->row[turn][half][r] = v;
+      arrive(&m->pair_bar[warp & 3]);
+      got = tr_wait_warp(&m->pair_bar[warp & 3], turn, m, status);
+      return m->row[turn][half ^ 1][r];
     };
     // The unit whose tiles were the last: its result is taken out of tensor
     // memory only once the next unit's queries are in, so that its scores run meanwhile.
     struct Unit {
       int lo, nodes, node0, rows, g, n_old, t0, n, nt_all;
-      long long done;  // tiles of all units up to the end of this CTA's part
+      long long done;  // where this CTA's part ends in the count of all units
     } un{};
     float mx = -INFINITY, sum = 0.f;
     bool in = false, real = false;
@@ -513,19 +566,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     auto finish = [&]() {
       if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
+      if constexpr (C::HALVES == 2) {
+        bool got;
+        sum += exchange(sum, got);
+        if (!got) return false;
+      }
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       if (!whole && starts) {
-        const long long u1 = un.done - un.n + un.nt_all;  // the unit's end among all tiles
+        const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
         split = SplitDesc{(int)mul_div(u1 * ctas + T - 1, 1, T) - cta, un.rows, un.lo + un.node0, un.g * a.G};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = un.t0 + un.n > un.n_old && *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
       const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
       const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      if (warp * 32 < un.rows) {
+      if ((warp & 3) * 32 < un.rows) {
         uint16_t *out = a.o + ((size_t)(un.lo + un.node0 + my_node) * a.Hq + un.g * a.G + my_head) * D;
 #pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
+        for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
           uint32_t v[32];
           __syncwarp();
           ptx::tmem_ld_x32(lanes + d, v);
@@ -565,31 +623,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (in && !whole)
+        if (in && !whole && half == 0)
           *reinterpret_cast<float2 *>(a.ml + (pslot * a.rows_cap + r) * 2) = make_float2(mx, sum);
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(&m->o_free);
-      __syncwarp();
+      arrive(&m->o_free);
       return true;
     };
     while (ok) {
       const bool more = w.next();
-      int up[2] = {-2, -2}, own = -2;  // parents of nodes r and r + 128, and of this row's node
+      constexpr int UPS = 2 / C::HALVES;
+      int up[UPS], own = -2;  // parents of nodes tid (and tid + 128), and of this row's node
       if (more) {
         const int32_t *parent = a.parent + w.s.lo;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (r + i * TR_ROWS < w.s.n) up[i] = __ldg(parent + r + i * TR_ROWS);
+        for (int i = 0; i < UPS; ++i) up[i] = tid + i * TR_ROWS < w.s.n ? __ldg(parent + tid + i * TR_ROWS) : -2;
         if (my_node < w.nodes()) own = __ldg(parent + w.node0() + my_node);
         if constexpr (C::Q_TMEM) {
           // this row of Q from the ring into tensor memory (the last unit's
           // scores, which read the one before, are done)
 #pragma unroll 1
-          for (int h = 0; ok && h < C::Q_SLOTS; ++h) {
+          for (int h = half; h < C::Q_SLOTS; h += C::HALVES) {
             const uint32_t slot = (ld + h) % C::NS;
-            ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status);
-            if (!ok) break;
+            if (!(ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status))) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t x[32];
@@ -603,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           if (!ok) break;
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
-          ptx::mbar_arrive(&m->q_ready);
+          arrive(&m->q_ready);
         }
       }
       if (un.n > 0) ok = finish();
@@ -612,7 +668,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       un = Unit{w.s.lo, w.s.n, w.node0(), w.nodes() * a.G, w.g, n_old, w.t0, w.n, w.nt_all, end - w.left};
       in = r < un.rows;
       real = in && own >= -1 && own < un.node0 + my_node;
-      const bool active = warp * 32 < un.rows;                     // the warp has rows
+      const bool active = (warp & 3) * 32 < un.rows;                     // the warp has rows
       const bool all_real = __all_sync(0xffffffffu, real || !in);  // none of them is padding
 #pragma unroll
       for (int q = 0; q < TR_MAXN / TR_TILE; ++q) sees[q] = 0;
@@ -625,15 +681,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           // the first of the tree's own tiles: its parents, and what this row's node sees of each tile
           if (!(ok = rows_sync())) break;  // the last unit's readers are done
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (r + i * TR_ROWS < un.nodes) {
-              if (up[i] >= r + i * TR_ROWS || up[i] < -2) {
+          for (int i = 0; i < UPS; ++i)
+            if (tid + i * TR_ROWS < un.nodes) {
+              if (up[i] >= tid + i * TR_ROWS || up[i] < -2) {
                 set_status(status, MOE_ERR_DEVICE_BOUNDS);
                 up[i] = -2;
               }
-              m->parent[r + i * TR_ROWS] = (int16_t)up[i];
+              m->parent[tid + i * TR_ROWS] = (int16_t)up[i];
             }
-          if (r == 0) m->nonfinite = 0;
+          if (tid == 0) m->nonfinite = 0;
           if (!(ok = rows_sync())) break;
           for (int i = real ? un.node0 + my_node : -1; i >= 0; i = m->parent[i]) {
 #pragma unroll
@@ -651,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           const uint32_t pos = ld + v_pos<D>(j, un.n), slot = pos % C::NS;
           if (!(ok = tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))) break;
           uint8_t *v = ring + slot * C::SLOT;
-          for (int e = r; e < TR_TILE * C::CHUNKS * 8; e += TR_ROWS) {  // 16-byte pieces
+          for (int e = tid; e < TR_TILE * C::CHUNKS * 8; e += TR_ROWS * C::HALVES) {  // 16-byte pieces
             const int ch = e / (TR_TILE * 8), q = (e / 8) % TR_TILE;
             uint4 *piece = reinterpret_cast<uint4 *>(v + ch * C::KV_CHUNK + q * 128 + (e & 7) * 16);
             const int at = t < n_old ? t * TR_TILE + q : (t - n_old) * TR_TILE + q;
@@ -676,11 +732,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           __syncwarp();
         }
         if (active) {
-          uint32_t s0[32], s1[32];
-          ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, s0);
-          ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE + 32, s1);
+          uint32_t x[COLS / 32][32];
+#pragma unroll
+          for (int h = 0; h < COLS / 32; ++h)
+            ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE + half * COLS + 32 * h, x[h]);
           ptx::tmem_wait_ld();
-          float tmax = -INFINITY;
           if (edge || !all_real) {
             unsigned long long see = 0;
             if (real) {
@@ -693,17 +749,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
                   if (t - n_old == q) see = sees[q];
               }
             }
-            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!(lo >> i & 1)) s0[i] = 0xFF800000u;  // -infinity
-              if (!(hi >> i & 1)) s1[i] = 0xFF800000u;
+            for (int h = 0; h < COLS / 32; ++h) {
+              const uint32_t bits = (uint32_t)(see >> (half * COLS + 32 * h));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1)) x[h][i] = 0xFF800000u;  // -infinity
             }
           }
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            tmax = fmaxf(tmax, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i])));
-          tmax *= a.scale_log2;
+          for (int h = 0; h < COLS / 32; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(x[h][i]));
+          float tmax = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.scale_log2;
+          if constexpr (C::HALVES == 2) {  // also: both have read S before either writes P over it
+            tmax = fmaxf(tmax, exchange(tmax, ok));
+            if (!ok) break;
+          }
           const bool grows = in && tmax > mx + TR_SLACK;  // also the first score a row sees
           if (__any_sync(0xffffffffu, grows)) {
             const float f = grows ? (mx == -INFINITY ? 0.f : ex2(mx - tmax)) : 1.f;
@@ -713,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               if (!(ok = tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
               ptx::tc_fence_after();
 #pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
+              for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
                 uint32_t v[32];
                 ptx::tmem_ld_x32(lanes + d, v);
                 ptx::tmem_wait_ld();
@@ -724,68 +787,66 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
             }
           }
           const float base = mx == -INFINITY ? 0.f : -mx;
-          uint32_t p[32];
+          uint32_t p[COLS / 2];
           float acc[4] = {};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float x0 = ex2(fmaf(__uint_as_float(s0[i]), a.scale_log2, base));
-            const float x1 = ex2(fmaf(__uint_as_float(s0[i + 1]), a.scale_log2, base));
-            const float y0 = ex2(fmaf(__uint_as_float(s1[i]), a.scale_log2, base));
-            const float y1 = ex2(fmaf(__uint_as_float(s1[i + 1]), a.scale_log2, base));
-            acc[0] += x0;
-            acc[1] += x1;
-            acc[2] += y0;
-            acc[3] += y1;
-            p[i / 2] = pack2<FP16>(x0, x1);
-            p[16 + i / 2] = pack2<FP16>(y0, y1);
+          for (int i = 0; i < COLS; i += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(x[i / 32][i % 32]), a.scale_log2, base));
+            const float p1 = ex2(fmaf(__uint_as_float(x[i / 32][i % 32 + 1]), a.scale_log2, base));
+            acc[i & 2] += p0;
+            acc[(i & 2) + 1] += p1;
+            p[i / 2] = pack2<FP16>(p0, p1);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          ptx::tmem_st_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, p);
+          if constexpr (C::HALVES == 2)
+            ptx::tmem_st_x16(lanes + C::S_COL + (jj & 1) * TR_TILE + half * 16, p);
+          else
+            ptx::tmem_st_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, p);
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&m->p_ready[jj & 1]);
+        arrive(&m->p_ready[jj & 1]);
       }
       ld += C::Q_SLOTS + 2 * un.n;
     }
-    if (r == 0) a.desc[cta] = split;
+    if (tid == 0) a.desc[cta] = split;
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == C::LOADER + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM);
   }
 }
 
 // o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
-// unit.  A thread has four values of one row (rows run fastest, in the parts
-// as in the threads, so that a warp's accesses are whole lines); one to eight
-// warps of a block share the parts of the same values (a unit is split over
-// as few as two CTAs and as many as all of them).
+// unit.  A thread has sixteen values of one row (rows run fastest, in the
+// parts as in the threads, so that a warp reads whole lines); up to eight
+// groups of a block's threads share the parts of the same values (a unit is
+// split over as few as two CTAs and as many as all of them).
 constexpr int TJ_THREADS = 256;
 
-__device__ __forceinline__ int part_groups(int parts) { return parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8; }
+__device__ __forceinline__ int part_groups(int parts) { return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8; }
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
   constexpr int MAXU = 2 * TR_MAX_SMS, WARPS = TJ_THREADS / 32;  // MAXU: split units at most
   __shared__ SplitDesc desc_s[MAXU];
   __shared__ int cta_s[MAXU], item_s[MAXU + 1], wsum[WARPS];
-  __shared__ float4 acc_s[TJ_THREADS];
+  __shared__ float4 acc_s[4][TJ_THREADS];
   __shared__ float2 ml_s[TJ_THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the split units in the CTAs' order, and the items (blocks of values) before each
-  const int vals = D / 4 * a.rows_cap;
+  // the split units in the CTAs' order, and the items (blocks of cells of sixteen values) before each
+  const int cells = D / 16 * a.rows_cap;
   constexpr int PER = (MAXU + TJ_THREADS - 1) / TJ_THREADS;
   SplitDesc d[PER];
   auto items_of = [&](const SplitDesc &x) {
     const int each = TJ_THREADS / part_groups(x.parts);
-    return (vals + each - 1) / each;
+    return (cells + each - 1) / each;
   };
-  int packed = 0;  // units << 20 | items: at most 320, and 320 * 64 * 128 / 32 below 2^17 of them
+  int packed = 0;  // units << 20 | items: at most 320, and 320 * 16 * 128 / 32 below 2^15 of them
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = tid * PER + i;
@@ -819,77 +880,78 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_cons
   if (tid == 0) item_s[units] = n_items;
   __syncthreads();
 
-  int u = 0;
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    while (item >= item_s[u + 1]) ++u;
+    int u = 0;  // the last unit whose first item is at or before this one
+#pragma unroll
+    for (int step = 256; step; step >>= 1)
+      if (u + step < units && item_s[u + step] <= item) u += step;
     const SplitDesc ds = desc_s[u];
     const int c0 = cta_s[u], groups = part_groups(ds.parts), each = TJ_THREADS / groups, grp = tid / each;
-    const int e = (item - item_s[u]) * each + tid % each, r = e % a.rows_cap;
-    const bool in = e < vals && r < ds.rows;
+    const int e = (item - item_s[u]) * each + tid % each, c4 = e / a.rows_cap * 4, r = e % a.rows_cap;
+    const bool in = e < cells && r < ds.rows;
     float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[4] = {};
+    auto add = [&](float2 ml, const float4 (&v)[4]) {
+      if (ml.x == -INFINITY) return;  // the row saw nothing there
+      const float mn = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : ex2(M - mn), h = ex2(ml.x - mn);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[q].x = fmaf(v[q].x, h, acc[q].x * f);
+        acc[q].y = fmaf(v[q].y, h, acc[q].y * f);
+        acc[q].z = fmaf(v[q].z, h, acc[q].z * f);
+        acc[q].w = fmaf(v[q].w, h, acc[q].w * f);
+      }
+      den = fmaf(ml.y, h, den * f);
+      M = mn;
+    };
     if (in) {
       // part i lies in CTA c0 + i's second slot if it starts the unit, else in its first
-      for (int i0 = grp; i0 < ds.parts; i0 += 4 * groups) {
-        float2 ml[4];
-        float4 v[4];
+      for (int i0 = grp; i0 < ds.parts; i0 += 2 * groups) {
+        float2 ml[2];
+        float4 v[2][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int i = i0 + q * groups;
-          ml[q] = make_float2(-INFINITY, 0.f);
-          v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 2; ++k) {
+          const int i = i0 + k * groups;
+          ml[k] = make_float2(-INFINITY, 0.f);
           if (i < ds.parts) {
             const size_t p = (size_t)2 * (c0 + i) + (i == 0 ? 1 : 0);
-            ml[q] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
-            v[q] = reinterpret_cast<const float4 *>(a.part)[p * vals + e];
+            ml[k] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
+            const float4 *src = reinterpret_cast<const float4 *>(a.part) + (p * (D / 4) + c4) * a.rows_cap + r;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[k][q] = src[q * a.rows_cap];
           }
         }
-        const float mn = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-        den *= f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float h = ml[q].x == -INFINITY ? 0.f : ex2(ml[q].x - mn);  // a part in which the row saw nothing
-          acc.x = fmaf(v[q].x, h, acc.x);
-          acc.y = fmaf(v[q].y, h, acc.y);
-          acc.z = fmaf(v[q].z, h, acc.z);
-          acc.w = fmaf(v[q].w, h, acc.w);
-          den = fmaf(ml[q].y, h, den);
-        }
-        M = mn;
+        add(ml[0], v[0]);
+        add(ml[1], v[1]);
       }
     }
     if (groups > 1) {
       __syncthreads();  // the last item's readers are done
-      acc_s[tid] = acc;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc_s[q][tid] = acc[q];
       ml_s[tid] = make_float2(M, den);
       __syncthreads();
-      if (grp == 0 && in) {
-        float mn = M;
-        for (int g = 1; g < groups; ++g) mn = fmaxf(mn, ml_s[g * each + tid].x);
-        const float f = M == -INFINITY ? 0.f : ex2(M - mn);
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-        den *= f;
+      if (grp == 0 && in)
         for (int g = 1; g < groups; ++g) {
-          const float2 ml = ml_s[g * each + tid];
-          const float4 v = acc_s[g * each + tid];
-          const float h = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
-          acc.x = fmaf(v.x, h, acc.x);
-          acc.y = fmaf(v.y, h, acc.y);
-          acc.z = fmaf(v.z, h, acc.z);
-          acc.w = fmaf(v.w, h, acc.w);
-          den = fmaf(ml.y, h, den);
+          float4 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = acc_s[q][g * each + tid];
+          add(ml_s[g * each + tid], v);
         }
-      }
     }
     if (in && grp == 0) {
       const float inv = den == 0.f ? 0.f : 1.f / den;
-      uint2 x;
-      x.x = pack2<FP16>(acc.x * inv, acc.y * inv);
-      x.y = pack2<FP16>(acc.z * inv, acc.w * inv);
       const int node = ds.node0 + r / a.G, head = ds.head0 + r % a.G;
-      *reinterpret_cast<uint2 *>(a.o + ((size_t)node * a.Hq + head) * D + e / a.rows_cap * 4) = x;
+      uint4 *out = reinterpret_cast<uint4 *>(a.o + ((size_t)node * a.Hq + head) * D + c4 * 4);
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        uint4 x;
+        x.x = pack2<FP16>(acc[q].x * inv, acc[q].y * inv);
+        x.y = pack2<FP16>(acc[q].z * inv, acc[q].w * inv);
+        x.z = pack2<FP16>(acc[q + 1].x * inv, acc[q + 1].y * inv);
+        x.w = pack2<FP16>(acc[q + 1].z * inv, acc[q + 1].w * inv);
+        out[q / 2] = x;
+      }
     }
   }
 }
