@@ -1,11 +1,23 @@
 // Verification of drafted trees (tree.h).
 //
-// One CTA per tree walks its nodes in index order: parents come first, so a
-// node whose parent is the current one is the next child to try.  The test of
-// a first child needs two values, p and q at its token; only a child that is
-// not taken costs a pass over the vocabulary, and so does the final draw.
-// Sums and the residual run in fp64: the sampled token is a whole number that
-// sums in another order must not change.
+// One cluster of up to eight CTAs per tree.  The first warp of its first CTA
+// walks the nodes in index order: parents come first, so a node whose parent is
+// the current one is the next child to try, and every test needs two values, p
+// and q at the node's token, which are all read at the start.  Only a child
+// that is refused, and the final draw, need sums over the vocabulary: the
+// walker then sends the cluster a command (through distributed shared memory),
+// the CTAs go over their parts of the rows, and the walker adds up what they
+// send back.  One CTA alone decides, so the cluster's barriers always meet.
+//
+// The sampled token is a whole number that sums in another order must not
+// change, but an SM does two fp64 operations a cycle: residuals and sums are
+// pairs of fp32 (value and error, some 45 bits; T. J. Dekker, "A floating-point
+// technique for extending the available precision", 1971).  With fp64 for the
+// sums of warps and CTAs and for the draw's prefixes alone, one tree over 32,000
+// tokens took 37.6 us, most of it there.
+//
+// Bound by the row's bytes, and for few trees by latency: the start's two
+// round trips, a pass and three cluster barriers.
 #include "common.cuh"
 #include "kernels.h"
 #include "tree.h"
@@ -13,8 +25,9 @@
 namespace moe {
 namespace {
 
-constexpr int DV_THREADS = 1024;
-constexpr int DV_MAXN = 1024;  // nodes of a tree
+constexpr int DV_THREADS = 512, DV_WARPS = DV_THREADS / 32;
+constexpr int DV_MAXN = 1024;     // nodes of a tree
+constexpr int DV_MAX_CTAS = 8;    // CTAs of a cluster
 
 struct VerifyArgs {
   const float *p, *q;
@@ -26,143 +39,375 @@ struct VerifyArgs {
   int32_t *n_path, *next, *status;
 };
 
-// Sum over the CTA in a fixed order; every thread gets it.
-__device__ double block_sum(double v, double *red) {
+// A value and its error.
+struct Pair {
+  float h, l;
+};
+
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  const float l = __fadd_rn(s.l, __fadd_rn(a.l, b.l)), h = __fadd_rn(s.h, l);
+  return Pair{h, __fsub_rn(l, __fsub_rn(h, s.h))};
+}
+__device__ __forceinline__ Pair minus(Pair a) { return Pair{-a.h, -a.l}; }
+__device__ __forceinline__ bool above(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+// s q, the pair times a float
+__device__ __forceinline__ Pair scaled(Pair s, float q) {
+  const float h = __fmul_rn(s.h, q), l = __fmaf_rn(s.l, q, __fmaf_rn(s.h, q, -h)), t = __fadd_rn(h, l);
+  return Pair{t, __fsub_rn(l, __fsub_rn(t, h))};
+}
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+  return Pair{__shfl_sync(0xffffffffu, a.h, from), __shfl_sync(0xffffffffu, a.l, from)};
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ Pair scan_lanes(Pair a) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = red[threadIdx.x & 31];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair t{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+    if ((int)(threadIdx.x & 31) >= o) a = add(a, t);
+  }
+  return a;
 }
 
-__global__ void __launch_bounds__(DV_THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ double red[32], mass_s[DV_MAXN];  // S before each of the current node's refused children
-  __shared__ int drop_s[DV_MAXN];              // their tokens
-  __shared__ double wsum[32];
-  __shared__ int pick, last;
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int lo = a.offsets[b], hi = a.offsets[b + 1], n = hi - lo;
-  int32_t *path = a.path + (size_t)b * a.path_stride;
-  bool ok = lo >= 0 && lo <= hi && hi <= a.n_nodes && n <= a.path_stride;
-  if (ok)
-    for (int i = tid; i < n; i += DV_THREADS) {
-      const int par = a.parent[lo + i], x = a.tokens[lo + i];
-      // node 0 is the root; the token of a node that is padding does not matter
-      if (par >= i || par < -2 || (i == 0 && par != -1) || (i > 0 && par >= 0 && (x < 0 || x >= a.V))) ok = false;
-    }
-  ok = __syncthreads_and(ok);
-  for (int i = tid; i < a.path_stride; i += DV_THREADS) path[i] = -1;
-  if (!ok || n == 0) {
-    if (tid == 0) {
-      a.n_path[b] = 0;
-      a.next[b] = -1;
-      if (!ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-    }
-    return;
+// max(r - s q, 0)
+__device__ __forceinline__ Pair drop(Pair r, Pair s, float q) {
+  const Pair d = add(r, minus(scaled(s, q)));
+  return d.h > 0.f ? d : Pair{0.f, 0.f};
+}
+
+enum { CMD_END = 0, CMD_PASS = 1, CMD_DRAW = 2 };
+
+struct Cmd {
+  int op, node, rounds;  // PASS: sum the residual of `node` after `rounds` refused children
+  Pair mass;             // S before the last of them
+  int target;            // DRAW: the CTA that finds the token
+  Pair threshold;        // whose sum passes this, counted from that CTA's first token
+};
+
+struct Shared {
+  // the walker's
+  float p_at[DV_MAXN], q_at[DV_MAXN], u[DV_MAXN];  // p and q of a node's parent at the node's token
+  int token[DV_MAXN];
+  int16_t parent[DV_MAXN];
+  Pair cta_sum[DV_MAX_CTAS];
+  // every CTA's
+  Cmd cmd;
+  Pair mass[DV_MAXN];     // S before each of the node's refused children
+  int dropped[DV_MAXN];   // their tokens (drafts without probabilities)
+  Pair warp_sum[DV_WARPS];
+  Pair scan[DV_WARPS];
+  int pick, last;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive();
+  cluster_wait();
+}
+// Store into the same place of another CTA of the cluster.
+template <typename T>
+__device__ __forceinline__ void remote_store(T *p, uint32_t cta, const T &v) {
+  static_assert(sizeof(T) % 4 == 0, "whole words");
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 4); ++i) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p) + 4 * i), "r"(cta));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(w[i]) : "memory");
   }
-  __syncthreads();
-  int cur = 0, count = 1, ndrop = 0;
-  double S = 1.0;
-  const float *p = a.p + (size_t)lo * a.V, *q = a.q ? a.q + (size_t)lo * a.V : nullptr;
-  // R of token t after the children refused so far
-  auto residual = [&](int t) {
-    double r = p[t];
-    if (q) {
-      const double qt = q[t];
-      for (int i = 0; i < ndrop; ++i) r = fmax(r - mass_s[i] * qt, 0.0);
-    } else {
-      for (int i = 0; i < ndrop; ++i)
-        if (drop_s[i] == t) r = 0.0;
+}
+
+// A row of p and q in aligned quads: quad k holds tokens 4 k - a .. 4 k - a + 3.
+struct Row {
+  const float *p, *q;  // q may be null
+  int a, V, quads;
+  __device__ Row(const VerifyArgs &args, int node) : V(args.V) {
+    const size_t at = (size_t)node * V;
+    a = (int)(at & 3);
+    p = args.p + at;
+    q = args.q ? args.q + at : nullptr;
+    quads = (a + V + 3) / 4;
+  }
+  __device__ __forceinline__ void load(int k, float (&pv)[4], float (&qv)[4]) const {
+    const int t = 4 * k - a;
+    if (t >= 0 && t + 4 <= V) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(p + t));
+      pv[0] = x.x, pv[1] = x.y, pv[2] = x.z, pv[3] = x.w;
+      if (q) {
+        const float4 y = __ldg(reinterpret_cast<const float4 *>(q + t));
+        qv[0] = y.x, qv[1] = y.y, qv[2] = y.z, qv[3] = y.w;
+      }
+    } else {  // the row's ends
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = t + i >= 0 && t + i < V;
+        pv[i] = in ? __ldg(p + t + i) : 0.f;
+        qv[i] = in && q ? __ldg(q + t + i) : 0.f;
+      }
     }
-    return r;
-  };
-  if (tid == 0) path[0] = 0;
-  for (int j = 1; j < n; ++j) {
-    if (a.parent[lo + j] != cur) continue;
-    const int x = a.tokens[lo + j];
-    const double Rx = residual(x), qx = q ? (double)q[x] : 1.0;
-    if ((double)a.u_accept[lo + j] * S * qx < Rx) {
-      if (tid == 0) path[count] = j;
-      ++count;
-      cur = j;
-      ndrop = 0;
-      S = 1.0;
-      p = a.p + (size_t)(lo + j) * a.V;
-      if (q) q = a.q + (size_t)(lo + j) * a.V;
+  }
+};
+
+__global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_constant__ VerifyArgs a, int ctas) {
+  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const int b = blockIdx.x / ctas;
+  cluster_arrive();  // no CTA's memory is written to before all have started (waited for below)
+  int lo = 0, n = 0;
+  bool ok = true;
+  if (rank == 0) {
+    lo = a.offsets[b];
+    const int hi = a.offsets[b + 1];
+    n = hi - lo;
+    ok = lo >= 0 && lo <= hi && hi <= a.n_nodes && n <= a.path_stride;
+    if (ok)
+      for (int i = tid; i < n; i += DV_THREADS) {
+        const int par = a.parent[lo + i], x = a.tokens[lo + i];
+        // node 0 is the root; the token of a node that is padding does not matter
+        if (par >= i || par < -2 || (i == 0 && par != -1) || (i > 0 && par >= 0 && (x < 0 || x >= a.V)))
+          ok = false;
+        else if (par >= 0) {
+          const size_t at = (size_t)(lo + par) * a.V + x;
+          s.p_at[i] = __ldg(a.p + at);
+          s.q_at[i] = a.q ? __ldg(a.q + at) : 1.f;
+          s.u[i] = a.u_accept[lo + i];
+          s.token[i] = x;
+        }
+        s.parent[i] = (int16_t)par;
+      }
+    for (int i = tid; i < a.path_stride; i += DV_THREADS) a.path[(size_t)b * a.path_stride + i] = -1;
+    ok = __syncthreads_and(ok);
+  }
+
+  cluster_wait();
+
+  // the walker's state
+  int32_t *path = a.path + (size_t)b * a.path_stride;
+  int cur = 0, at = 0, count = 1, rounds = 0;  // at: the last node looked at
+  const Pair zero{0.f, 0.f}, one{1.f, 0.f}, none{INFINITY, 0.f};  // none: a threshold that nothing passes
+  Pair S = one;
+  bool summed = false, started = false;        // summed: the last pass was over the current residual
+  for (;;) {
+    if (rank == 0 && warp == 0) {
+      Cmd c{CMD_END, 0, 0, zero, 0, zero};
+      if (!ok || n == 0) {
+        if (lane == 0) {
+          a.n_path[b] = 0;
+          a.next[b] = -1;
+          if (!ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+        }
+      } else {
+        if (!started && lane == 0) path[0] = 0;
+        started = true;
+        Pair upto = zero, total = zero;  // the CTAs' sums up to this lane's, and all of them
+        if (summed) {
+          upto = scan_lanes(lane < ctas ? s.cta_sum[lane] : zero);
+          total = shfl(upto, 31);
+          if (a.q && rounds > 0) S = total;
+        }
+        bool pass = false;
+        while (!pass) {
+          // the next child of the current node
+          unsigned found = 0;
+          int base = (at + 1) & ~31;
+          for (; base < n; base += 32) {
+            const int i = base + lane;
+            found = __ballot_sync(0xffffffffu, i > at && i < n && s.parent[i] == cur);
+            if (found) break;
+          }
+          if (!found) {
+            at = n;
+            break;
+          }
+          at = base + __ffs(found) - 1;
+          Pair R{s.p_at[at], 0.f};
+          const float q = s.q_at[at];
+          for (int i = 0; i < rounds; ++i) {
+            if (a.q)
+              R = drop(R, s.mass[i], q);
+            else if (s.dropped[i] == s.token[at])
+              R = zero;
+          }
+          // u q is exact as a pair; with S = 1 the test is too
+          const float uq = __fmul_rn(s.u[at], q);
+          const Pair uqS = add(scaled(S, uq), scaled(S, __fmaf_rn(s.u[at], q, -uq)));
+          if (above(R, uqS)) {
+            if (lane == 0) path[count] = at;
+            ++count;
+            cur = at;
+            rounds = 0;
+            S = one;
+            summed = false;
+            continue;
+          }
+          c.mass = S;
+          if (a.q)
+            pass = true;  // S comes from the pass
+          else
+            S = add(S, minus(R));
+          if (!a.q && lane < ctas) remote_store(&s.dropped[rounds], lane, s.token[at]);
+          if (lane == 0) s.mass[rounds] = c.mass;
+          __syncwarp();
+          ++rounds;
+          summed = false;
+        }
+        if (pass || !summed) {
+          c.op = CMD_PASS;
+          c.node = lo + cur;
+          c.rounds = rounds;
+          summed = true;
+        } else if (total.h > 0.f && total.h < INFINITY) {
+          // draw: the first CTA whose sum takes the running sum past the
+          // threshold; where rounding leaves none, the last with any mass
+          const Pair want = scaled(total, a.u_sample[b]), mine = lane < ctas ? s.cta_sum[lane] : zero;
+          const unsigned past = __ballot_sync(0xffffffffu, lane < ctas && above(upto, want));
+          const unsigned some = __ballot_sync(0xffffffffu, mine.h > 0.f);
+          c.op = CMD_DRAW;
+          c.node = lo + cur;
+          c.rounds = rounds;
+          c.target = past ? __ffs(past) - 1 : 31 - __clz(some);
+          const Pair before = shfl(upto, max(c.target - 1, 0));
+          c.threshold = !past ? none : c.target ? add(want, minus(before)) : want;
+          if (lane == 0) a.n_path[b] = count;
+        } else if (rounds > 0) {  // no residual mass: draw from p itself
+          rounds = 0;
+          c.op = CMD_PASS;
+          c.node = lo + cur;
+        } else {
+          __syncwarp();
+          for (int i = lane; i < a.path_stride; i += 32) path[i] = -1;
+          if (lane == 0) {
+            a.n_path[b] = 0;
+            a.next[b] = -1;
+            set_status(a.status, MOE_ERR_NONFINITE);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < ctas) remote_store(&s.cmd, lane, c);
+    }
+    cluster_barrier();
+    const Cmd c = s.cmd;
+    if (c.op == CMD_END) break;
+    const Row row(a, c.node);
+    if (tid == 0 && c.op == CMD_PASS && c.rounds > 0) s.mass[c.rounds - 1] = c.mass;
+    if (c.op == CMD_PASS) __syncthreads();
+    auto residual = [&](int t, float pv, float qv) {
+      Pair r{pv, 0.f};
+      if (a.q) {
+        for (int i = 0; i < c.rounds; ++i) r = drop(r, s.mass[i], qv);
+      } else {
+        for (int i = 0; i < c.rounds; ++i)
+          if (s.dropped[i] == t) r.h = 0.f;
+      }
+      return r;
+    };
+    // a warp's run of quads, the warps of all CTAs in the row's order
+    const int each = ((row.quads + ctas * DV_WARPS - 1) / (ctas * DV_WARPS) + 31) & ~31;
+    if (c.op == CMD_PASS) {
+      const int k0 = min(row.quads, ((int)rank * DV_WARPS + warp) * each), k1 = min(row.quads, k0 + each);
+      Pair sum{0.f, 0.f};
+      constexpr int U = 4;  // quads in flight per thread
+      for (int k = k0 + lane; k < k1; k += 32 * U) {
+        float pv[U][4], qv[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pv[u][i] = qv[u][i] = 0.f;
+          if (k + 32 * u < k1) row.load(k + 32 * u, pv[u], qv[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = add(sum, residual(4 * (k + 32 * u) - row.a + i, pv[u][i], qv[u][i]));
+      }
+      sum = scan_lanes(sum);
+      if (lane == 31) s.warp_sum[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = scan_lanes(lane < DV_WARPS ? s.warp_sum[lane] : zero);
+        if (lane == 31) remote_store(&s.cta_sum[rank], 0, sum);
+      }
+      cluster_barrier();
       continue;
     }
-    __syncthreads();
-    if (tid == 0) {
-      mass_s[ndrop] = S;
-      drop_s[ndrop] = x;
-    }
-    ++ndrop;
-    __syncthreads();
-    if (q) {
-      double s = 0.0;
-      for (int t = tid; t < a.V; t += DV_THREADS) s += residual(t);
-      S = block_sum(s, red);
-    } else {
-      S -= Rx;
-    }
-  }
-  // the draw: each thread sums a run of tokens, the runs in order
-  const int run = (a.V + DV_THREADS - 1) / DV_THREADS, t0 = min(a.V, tid * run), t1 = min(a.V, t0 + run);
-  for (int tries = 0; tries < 2; ++tries) {
-    double s = 0.0;
-    for (int t = t0; t < t1; ++t) s += residual(t);
-    double inc = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, inc, o);
-      if ((tid & 31) >= o) inc += v;
-    }
-    __syncthreads();
-    if ((tid & 31) == 31) wsum[tid >> 5] = inc;
-    if (tid == 0) {
-      pick = a.V;
-      last = -1;
-    }
-    __syncthreads();
-    double before = 0.0, total = 0.0;
-    for (int w = 0; w < DV_THREADS / 32; ++w) {
-      if (w < (tid >> 5)) before += wsum[w];
-      total += wsum[w];
-    }
-    before += inc - s;
-    if (total > 0.0 && total < 1e300) {
-      const double want = (double)a.u_sample[b] * total;
-      double c = before;
-      int mine = -1, first = a.V;
-      for (int t = t0; t < t1; ++t) {
-        const double r = residual(t);
-        c += r;
-        if (r > 0.0) mine = t;
-        if (first == a.V && c > want && r > 0.0) first = t;
-      }
-      if (first < a.V) atomicMin(&pick, first);
-      if (mine >= 0) atomicMax(&last, mine);
-      __syncthreads();
+    if (rank == (uint32_t)c.target) {
+      // the warp run, then the token: the first past the threshold, or the
+      // last with any mass where rounding leaves none
+      const Pair mine_w = lane < DV_WARPS ? s.warp_sum[lane] : zero, upto = scan_lanes(mine_w);
+      const unsigned past = __ballot_sync(0xffffffffu, lane < DV_WARPS && above(upto, c.threshold));
+      const unsigned some = __ballot_sync(0xffffffffu, mine_w.h > 0.f);
+      const int w = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+      const Pair want = past ? c.threshold : none;
+      Pair from = shfl(upto, max(w - 1, 0));  // what comes before the run
+      if (w == 0) from = zero;
+      const int k0 = min(row.quads, ((int)rank * DV_WARPS + w) * each), k1 = min(row.quads, k0 + each);
       if (tid == 0) {
-        a.next[b] = min(pick, last);
-        a.n_path[b] = count;
+        s.pick = row.V;
+        s.last = -1;
       }
-      return;
+      __syncthreads();
+      for (int kb = k0; kb < k1; kb += DV_THREADS) {
+        const int k = kb + tid, t0 = 4 * k - row.a;
+        float pv[4] = {}, qv[4] = {};
+        if (k < k1) row.load(k, pv, qv);
+        Pair r[4], four{0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r[i] = residual(t0 + i, pv[i], qv[i]);
+          four = add(four, r[i]);
+        }
+        const Pair inc = scan_lanes(four);
+        if (lane == 31) s.scan[warp] = inc;
+        __syncthreads();
+        const Pair warps = scan_lanes(lane < DV_WARPS ? s.scan[lane] : zero);
+        const Pair ahead = shfl(warps, max(warp - 1, 0)), all = shfl(warps, 31);
+        Pair run = add(warp ? add(from, ahead) : from, add(inc, minus(four)));
+        from = add(from, all);
+        int first = row.V, mine = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          run = add(run, r[i]);
+          if (r[i].h > 0.f) {
+            mine = t0 + i;
+            if (first == row.V && above(run, want)) first = t0 + i;
+          }
+        }
+        if (first < row.V) atomicMin(&s.pick, first);
+        if (mine >= 0) atomicMax(&s.last, mine);
+        __syncthreads();
+        if (s.pick < row.V) break;
+      }
+      if (tid == 0) a.next[b] = min(s.pick, s.last);
     }
-    if (ndrop == 0) break;
-    ndrop = 0;  // no residual mass: draw from p itself
-    __syncthreads();
+    break;
   }
-  for (int i = tid; i < a.path_stride; i += DV_THREADS) path[i] = -1;
-  if (tid == 0) {
-    a.n_path[b] = 0;
-    a.next[b] = -1;
-    set_status(a.status, MOE_ERR_NONFINITE);
-  }
+}
+
+// CTAs of a tree's cluster: eight, fewer where a CTA would have less than 1024
+// tokens or the trees alone fill the GPU three times over.
+int cluster_ctas(int B, int V) {
+  int n = DV_MAX_CTAS;
+  while (n > 1 && (V < n * 1024 || (int64_t)B * n > 3 * 152)) n /= 2;
+  return n;
 }
 
 }  // namespace
@@ -200,8 +445,19 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   a.next = next_d;
   a.status = status_d;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = moe::cluster_ctas(B, V);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * ctas));
+  cfg.blockDim = dim3(moe::DV_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   moe::prof_before(MOE_KERNEL_DRAFT_VERIFY, s);
-  const cudaError_t e = moe::launch_dep(false, moe::verify_kernel, dim3(B), dim3(moe::DV_THREADS), 0, s, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, moe::verify_kernel, a, ctas);
   moe::prof_after(MOE_KERNEL_DRAFT_VERIFY, s);
   return moe::note_cuda_error(e);
 }

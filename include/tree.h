@@ -61,7 +61,7 @@ moe_status attn_tree(const attn_cache *c, int32_t layer, const void *q_d, const 
  *   R[0] + .. + R[t] > u_sample[b] * sum R
  * (from p[c] where R is zero everywhere).  q_d NULL: the drafts are not
  * sampled (looked up, or the draft's likeliest): q[c][x] = 1, and a child not
- * taken leaves R[x] <- 0, S <- S - R[x].  The tests and sums carry at least 48 bits, so
+ * taken leaves R[x] <- 0, S <- S - R[x].  Tests and sums carry 40 bits or more, so
  * the tokens are those of 64-bit arithmetic but for ties closer than that.
  *   p_d          fp32 [n_nodes][V] target distribution after each node (read)
  *   q_d          fp32 [n_nodes][V] draft distribution the node's children were drawn from, or NULL
