@@ -53,6 +53,11 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const float l = __fadd_rn(s.l, __fadd_rn(a.l, b.l)), h = __fadd_rn(s.h, l);
   return Pair{h, __fsub_rn(l, __fsub_rn(h, s.h))};
 }
+// The same without bringing the error back below the value's last bit (a few times in a row).
+__device__ __forceinline__ Pair add_loose(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return Pair{s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
+}
 __device__ __forceinline__ Pair minus(Pair a) { return Pair{-a.h, -a.l}; }
 __device__ __forceinline__ bool above(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
 // s q, the pair times a float
@@ -134,38 +139,74 @@ __device__ __forceinline__ void remote_store(T *p, uint32_t cta, const T &v) {
   }
 }
 
-// A row of p and q in aligned quads: quad k holds tokens 4 k - a .. 4 k - a + 3.
+// A row of p (and q) in aligned quads: quad k holds tokens 4 k - a .. 4 k - a + 3.
+template <bool Q>
 struct Row {
-  const float *p, *q;  // q may be null
+  const float *p, *q;
   int a, V, quads;
   __device__ Row(const VerifyArgs &args, int node) : V(args.V) {
     const size_t at = (size_t)node * V;
     a = (int)(at & 3);
     p = args.p + at;
-    q = args.q ? args.q + at : nullptr;
+    q = Q ? args.q + at : nullptr;
     quads = (a + V + 3) / 4;
   }
-  __device__ __forceinline__ void load(int k, float (&pv)[4], float (&qv)[4]) const {
+  __device__ __forceinline__ bool whole(int k) const { return 4 * k >= a && 4 * k - a + 4 <= V; }
+  // a whole quad (zeros where !in)
+  __device__ __forceinline__ void load(int k, bool in, float4 &pv, float4 &qv) const {
     const int t = 4 * k - a;
-    if (t >= 0 && t + 4 <= V) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(p + t));
-      pv[0] = x.x, pv[1] = x.y, pv[2] = x.z, pv[3] = x.w;
-      if (q) {
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(q + t));
-        qv[0] = y.x, qv[1] = y.y, qv[2] = y.z, qv[3] = y.w;
-      }
-    } else {  // the row's ends
+    pv = in ? __ldg(reinterpret_cast<const float4 *>(p + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (Q) qv = in ? __ldg(reinterpret_cast<const float4 *>(q + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // any quad, the row's ends among them (zeros outside the row)
+  __device__ __forceinline__ void load_any(int k, float4 &pv, float4 &qv) const {
+    if (whole(k)) return load(k, true, pv, qv);
+    const int t = 4 * k - a;
+    float x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = t + i >= 0 && t + i < V;
-        pv[i] = in ? __ldg(p + t + i) : 0.f;
-        qv[i] = in && q ? __ldg(q + t + i) : 0.f;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const bool in = t + i >= 0 && t + i < V;
+      x[i] = in ? __ldg(p + t + i) : 0.f;
+      y[i] = Q && in ? __ldg(q + t + i) : 0.f;
     }
+    pv = make_float4(x[0], x[1], x[2], x[3]);
+    qv = make_float4(y[0], y[1], y[2], y[3]);
   }
 };
 
-__global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_constant__ VerifyArgs a, int ctas) {
+// R of a quad's tokens t .. t + 3 after `rounds` refused children: by their
+// masses with q (S = 1 before the first), by their tokens without.
+template <bool Q>
+__device__ __forceinline__ void residual(const Shared &s, int rounds, int t, float4 pv, float4 qv, Pair (&r)[4]) {
+  const float p[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = Pair{p[i], 0.f};
+  if (Q) {
+    const float q[4] = {qv.x, qv.y, qv.z, qv.w};
+    if (rounds > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = two_sum(p[i], -q[i]);
+        if (!(r[i].h > 0.f)) r[i] = Pair{0.f, 0.f};
+      }
+    }
+    for (int k = 1; k < rounds; ++k) {
+      const Pair m = s.mass[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = drop(r[i], m, q[i]);
+    }
+  } else {
+    for (int k = 0; k < rounds; ++k) {
+      const int d = s.dropped[k] - t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (d == i) r[i].h = 0.f;
+    }
+  }
+}
+
+template <bool Q>
+__global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int ctas) {
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
@@ -187,7 +228,7 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
         else if (par >= 0) {
           const size_t at = (size_t)(lo + par) * a.V + x;
           s.p_at[i] = __ldg(a.p + at);
-          s.q_at[i] = a.q ? __ldg(a.q + at) : 1.f;
+          s.q_at[i] = Q ? __ldg(a.q + at) : 1.f;
           s.u[i] = a.u_accept[lo + i];
           s.token[i] = x;
         }
@@ -199,6 +240,7 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
 
   cluster_wait();
 
+  const float u_sample = rank == 0 ? __ldg(a.u_sample + b) : 0.f;
   // the walker's state
   int32_t *path = a.path + (size_t)b * a.path_stride;
   int cur = 0, at = 0, count = 1, rounds = 0;  // at: the last node looked at
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
         if (summed) {
           upto = scan_lanes(lane < ctas ? s.cta_sum[lane] : zero);
           total = shfl(upto, 31);
-          if (a.q && rounds > 0) S = total;
+          if (Q && rounds > 0) S = total;
         }
         bool pass = false;
         while (!pass) {
@@ -241,7 +283,7 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
           Pair R{s.p_at[at], 0.f};
           const float q = s.q_at[at];
           for (int i = 0; i < rounds; ++i) {
-            if (a.q)
+            if (Q)
               R = drop(R, s.mass[i], q);
             else if (s.dropped[i] == s.token[at])
               R = zero;
@@ -259,11 +301,11 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
             continue;
           }
           c.mass = S;
-          if (a.q)
+          if (Q)
             pass = true;  // S comes from the pass
           else
             S = add(S, minus(R));
-          if (!a.q && lane < ctas) remote_store(&s.dropped[rounds], lane, s.token[at]);
+          if (!Q && lane < ctas) remote_store(&s.dropped[rounds], lane, s.token[at]);
           if (lane == 0) s.mass[rounds] = c.mass;
           __syncwarp();
           ++rounds;
@@ -277,7 +319,7 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
         } else if (total.h > 0.f && total.h < INFINITY) {
           // draw: the first CTA whose sum takes the running sum past the
           // threshold; where rounding leaves none, the last with any mass
-          const Pair want = scaled(total, a.u_sample[b]), mine = lane < ctas ? s.cta_sum[lane] : zero;
+          const Pair want = scaled(total, u_sample), mine = lane < ctas ? s.cta_sum[lane] : zero;
           const unsigned past = __ballot_sync(0xffffffffu, lane < ctas && above(upto, want));
           const unsigned some = __ballot_sync(0xffffffffu, mine.h > 0.f);
           c.op = CMD_DRAW;
@@ -307,38 +349,37 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
     cluster_barrier();
     const Cmd c = s.cmd;
     if (c.op == CMD_END) break;
-    const Row row(a, c.node);
+    const Row<Q> row(a, c.node);
     if (tid == 0 && c.op == CMD_PASS && c.rounds > 0) s.mass[c.rounds - 1] = c.mass;
     if (c.op == CMD_PASS) __syncthreads();
-    auto residual = [&](int t, float pv, float qv) {
-      Pair r{pv, 0.f};
-      if (a.q) {
-        for (int i = 0; i < c.rounds; ++i) r = drop(r, s.mass[i], qv);
-      } else {
-        for (int i = 0; i < c.rounds; ++i)
-          if (s.dropped[i] == t) r.h = 0.f;
-      }
-      return r;
-    };
     // a warp's run of quads, the warps of all CTAs in the row's order
     const int each = ((row.quads + ctas * DV_WARPS - 1) / (ctas * DV_WARPS) + 31) & ~31;
     if (c.op == CMD_PASS) {
       const int k0 = min(row.quads, ((int)rank * DV_WARPS + warp) * each), k1 = min(row.quads, k0 + each);
       Pair sum{0.f, 0.f};
-      constexpr int U = 4;  // quads in flight per thread
+      constexpr int U = Q ? 2 : 4;  // quads of p (and q) in flight per thread
       for (int k = k0 + lane; k < k1; k += 32 * U) {
-        float pv[U][4], qv[U][4];
+        float4 pv[U], qv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) row.load(k + 32 * u, k + 32 * u < k1 && row.whole(k + 32 * u), pv[u], qv[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pv[u][i] = qv[u][i] = 0.f;
-          if (k + 32 * u < k1) row.load(k + 32 * u, pv[u], qv[u]);
+          Pair r[4];
+          residual<Q>(s, c.rounds, 4 * (k + 32 * u) - row.a, pv[u], qv[u], r);
+          sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum = add(sum, residual(4 * (k + 32 * u) - row.a + i, pv[u][i], qv[u][i]));
       }
+      if (lane < 2 && k0 < k1) {  // the row's ends
+        const int k = lane ? row.quads - 1 : 0;
+        if (k >= k0 && k < k1 && !row.whole(k) && (lane == 0 || k > 0)) {
+          float4 pv, qv;
+          Pair r[4];
+          row.load_any(k, pv, qv);
+          residual<Q>(s, c.rounds, 4 * k - row.a, pv, qv, r);
+          sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
+        }
+      }
+      __syncwarp();
       sum = scan_lanes(sum);
       if (lane == 31) s.warp_sum[warp] = sum;
       __syncthreads();
@@ -367,14 +408,11 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
       __syncthreads();
       for (int kb = k0; kb < k1; kb += DV_THREADS) {
         const int k = kb + tid, t0 = 4 * k - row.a;
-        float pv[4] = {}, qv[4] = {};
-        if (k < k1) row.load(k, pv, qv);
-        Pair r[4], four{0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r[i] = residual(t0 + i, pv[i], qv[i]);
-          four = add(four, r[i]);
-        }
+        float4 pv = make_float4(0.f, 0.f, 0.f, 0.f), qv = pv;
+        if (k < k1) row.load_any(k, pv, qv);
+        Pair r[4];
+        residual<Q>(s, c.rounds, t0, pv, qv, r);
+        const Pair four = add(add_loose(r[0], r[1]), add_loose(r[2], r[3]));
         const Pair inc = scan_lanes(four);
         if (lane == 31) s.scan[warp] = inc;
         __syncthreads();
@@ -403,10 +441,10 @@ __global__ void __launch_bounds__(DV_THREADS, 1) verify_kernel(const __grid_cons
 }
 
 // CTAs of a tree's cluster: eight, fewer where a CTA would have less than 1024
-// tokens or the trees alone fill the GPU three times over.
+// tokens or the clusters would not all run at once, two CTAs an SM.
 int cluster_ctas(int B, int V) {
   int n = DV_MAX_CTAS;
-  while (n > 1 && (V < n * 1024 || (int64_t)B * n > 3 * 152)) n /= 2;
+  while (n > 1 && (V < n * 1024 || (int64_t)B * n > 2 * 152)) n /= 2;
   return n;
 }
 
@@ -457,7 +495,8 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   cfg.attrs = at;
   cfg.numAttrs = 1;
   moe::prof_before(MOE_KERNEL_DRAFT_VERIFY, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, moe::verify_kernel, a, ctas);
+  const cudaError_t e = q_d ? cudaLaunchKernelEx(&cfg, moe::verify_kernel<true>, a, ctas)
+                            : cudaLaunchKernelEx(&cfg, moe::verify_kernel<false>, a, ctas);
   moe::prof_after(MOE_KERNEL_DRAFT_VERIFY, s);
   return moe::note_cuda_error(e);
 }
