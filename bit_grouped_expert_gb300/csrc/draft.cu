@@ -1,6 +1,6 @@
 // Verification of drafted trees (tree.h).
 //
-// One cluster of up to eight CTAs per tree.  The first warp of its first CTA
+// One cluster of up to 16 CTAs per tree.  The first warp of its first CTA
 // walks the nodes in index order: parents come first, so a node whose parent is
 // the current one is the next child to try, and every test needs two values, p
 // and q at the node's token, which are all read at the start.  Only a child
@@ -18,6 +18,8 @@
 //
 // Bound by the row's bytes, and for few trees by latency: the start's two
 // round trips, a pass and three cluster barriers.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tree.h"
@@ -27,7 +29,7 @@ namespace {
 
 constexpr int DV_THREADS = 512, DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAXN = 1024;     // nodes of a tree
-constexpr int DV_MAX_CTAS = 8;    // CTAs of a cluster
+constexpr int DV_MAX_CTAS = 16;   // CTAs of a cluster
 
 struct VerifyArgs {
   const float *p, *q;
@@ -80,7 +82,8 @@ __device__ __forceinline__ Pair scan_lanes(Pair a) {
 
 // max(r - s q, 0)
 __device__ __forceinline__ Pair drop(Pair r, Pair s, float q) {
-  const Pair d = add(r, minus(scaled(s, q)));
+  const float ph = __fmul_rn(s.h, q), pl = __fmaf_rn(s.l, q, __fmaf_rn(s.h, q, -ph));
+  const Pair d = add(r, Pair{-ph, -pl});
   return d.h > 0.f ? d : Pair{0.f, 0.f};
 }
 
@@ -174,6 +177,21 @@ struct Row {
   }
 };
 
+// A CTA's part of the residual in shared memory, where it fits, so that every
+// pass after a node's first is one step on instead of all steps again.
+struct Cache {
+  float4 *h, *l;
+  bool on;
+  __device__ void put(int i, const Pair (&r)[4]) const {
+    h[i] = make_float4(r[0].h, r[1].h, r[2].h, r[3].h);
+    l[i] = make_float4(r[0].l, r[1].l, r[2].l, r[3].l);
+  }
+  __device__ void get(int i, Pair (&r)[4]) const {
+    const float4 x = h[i], y = l[i];
+    r[0] = Pair{x.x, y.x}, r[1] = Pair{x.y, y.y}, r[2] = Pair{x.z, y.z}, r[3] = Pair{x.w, y.w};
+  }
+};
+
 // R of a quad's tokens t .. t + 3 after `rounds` refused children: by their
 // masses with q (S = 1 before the first), by their tokens without.
 template <bool Q>
@@ -206,8 +224,11 @@ __device__ __forceinline__ void residual(const Shared &s, int rounds, int t, flo
 }
 
 template <bool Q>
-__global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int ctas) {
+__global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int ctas,
+                                                             int cache_quads) {
   __shared__ Shared s;
+  extern __shared__ float4 cache_mem[];
+  const Cache cache{cache_mem, cache_mem + cache_quads, Q && cache_quads > 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / ctas;
@@ -353,30 +374,61 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
     if (tid == 0 && c.op == CMD_PASS && c.rounds > 0) s.mass[c.rounds - 1] = c.mass;
     if (c.op == CMD_PASS) __syncthreads();
     // a warp's run of quads, the warps of all CTAs in the row's order
-    const int each = ((row.quads + ctas * DV_WARPS - 1) / (ctas * DV_WARPS) + 31) & ~31;
+    const int each = (row.quads + ctas * DV_WARPS - 1) / (ctas * DV_WARPS);
     if (c.op == CMD_PASS) {
       const int k0 = min(row.quads, ((int)rank * DV_WARPS + warp) * each), k1 = min(row.quads, k0 + each);
       Pair sum{0.f, 0.f};
-      constexpr int U = Q ? 2 : 4;  // quads of p (and q) in flight per thread
-      for (int k = k0 + lane; k < k1; k += 32 * U) {
-        float4 pv[U], qv[U];
+      const int c0 = (int)rank * DV_WARPS * each;  // the CTA's first quad
+      if (cache.on && c.rounds > 1) {
+        const Pair m = c.mass;
+        for (int k = k0 + lane; k < k1; k += 64) {
+          float4 pv, qv[2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) row.load(k + 32 * u, k + 32 * u < k1 && row.whole(k + 32 * u), pv[u], qv[u]);
+          for (int u = 0; u < 2; ++u)
+            if (k + 32 * u < k1) row.load_any(k + 32 * u, pv, qv[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          Pair r[4];
-          residual<Q>(s, c.rounds, 4 * (k + 32 * u) - row.a, pv[u], qv[u], r);
-          sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
+          for (int u = 0; u < 2; ++u) {
+            if (k + 32 * u >= k1) break;
+            Pair r[4];
+            cache.get(k + 32 * u - c0, r);
+            r[0] = drop(r[0], m, qv[u].x);
+            r[1] = drop(r[1], m, qv[u].y);
+            r[2] = drop(r[2], m, qv[u].z);
+            r[3] = drop(r[3], m, qv[u].w);
+            cache.put(k + 32 * u - c0, r);
+            sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
+          }
         }
-      }
-      if (lane < 2 && k0 < k1) {  // the row's ends
-        const int k = lane ? row.quads - 1 : 0;
-        if (k >= k0 && k < k1 && !row.whole(k) && (lane == 0 || k > 0)) {
-          float4 pv, qv;
+      } else {
+        auto take = [&](int k, float4 pv, float4 qv) {
           Pair r[4];
-          row.load_any(k, pv, qv);
           residual<Q>(s, c.rounds, 4 * k - row.a, pv, qv, r);
-          sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
+          if (cache.on) cache.put(k - c0, r);
+          if (Q)
+            sum = add(sum, add_loose(add_loose(r[0], r[1]), add_loose(r[2], r[3])));
+          else  // no errors yet
+            sum = add(sum, add_loose(two_sum(r[0].h, r[1].h), two_sum(r[2].h, r[3].h)));
+        };
+        constexpr int U = Q ? 2 : 4;  // quads of p (and q) in flight per thread
+        for (int k = k0 + lane; k < k1; k += 32 * U) {
+          float4 pv[U], qv[U];
+          bool in[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            in[u] = k + 32 * u < k1 && row.whole(k + 32 * u);
+            row.load(k + 32 * u, in[u], pv[u], qv[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (in[u]) take(k + 32 * u, pv[u], qv[u]);
+        }
+        if (lane < 2 && k0 < k1) {  // the row's ends
+          const int k = lane ? row.quads - 1 : 0;
+          if (k >= k0 && k < k1 && !row.whole(k) && (lane == 0 || k > 0)) {
+            float4 pv, qv;
+            row.load_any(k, pv, qv);
+            take(k, pv, qv);
+          }
         }
       }
       __syncwarp();
@@ -408,10 +460,16 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
       __syncthreads();
       for (int kb = k0; kb < k1; kb += DV_THREADS) {
         const int k = kb + tid, t0 = 4 * k - row.a;
-        float4 pv = make_float4(0.f, 0.f, 0.f, 0.f), qv = pv;
-        if (k < k1) row.load_any(k, pv, qv);
-        Pair r[4];
-        residual<Q>(s, c.rounds, t0, pv, qv, r);
+        Pair r[4] = {zero, zero, zero, zero};
+        if (k < k1) {
+          if (cache.on) {
+            cache.get(k - (int)rank * DV_WARPS * each, r);
+          } else {
+            float4 pv, qv;
+            row.load_any(k, pv, qv);
+            residual<Q>(s, c.rounds, t0, pv, qv, r);
+          }
+        }
         const Pair four = add(add_loose(r[0], r[1]), add_loose(r[2], r[3]));
         const Pair inc = scan_lanes(four);
         if (lane == 31) s.scan[warp] = inc;
@@ -440,12 +498,11 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
   }
 }
 
-// CTAs of a tree's cluster: eight, fewer where a CTA would have less than 1024
-// tokens or the clusters would not all run at once, two CTAs an SM.
+// CTAs of a tree's cluster: as many as run at once for B trees, two an SM, up
+// to 16 and down to 1024 tokens a CTA.
 int cluster_ctas(int B, int V) {
-  int n = DV_MAX_CTAS;
-  while (n > 1 && (V < n * 1024 || (int64_t)B * n > 2 * 152)) n /= 2;
-  return n;
+  const int n = std::min({DV_MAX_CTAS, 2 * 152 / B, V / 1024});
+  return n < 1 ? 1 : n;
 }
 
 }  // namespace
@@ -488,15 +545,26 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   cfg.gridDim = dim3((unsigned)(B * ctas));
   cfg.blockDim = dim3(moe::DV_THREADS);
   cfg.stream = s;
+  // the residual's cache: a CTA's quads (a row begins up to three tokens into
+  // its first), if two CTAs an SM have room for it
+  int cache_quads = (V / 4 + 2 + ctas * moe::DV_WARPS - 1) / (ctas * moe::DV_WARPS) * moe::DV_WARPS;
+  if (!q_d || cache_quads * 32 > 80 * 1024) cache_quads = 0;
+  cfg.dynamicSmemBytes = (size_t)cache_quads * 32;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  auto kernel = q_d ? moe::verify_kernel<true> : moe::verify_kernel<false>;
+  // clusters above eight CTAs want leave; per device and cheap: asked on every call rather than remembered
+  cudaError_t e = cudaSuccess;
+  if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cache_quads)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return moe::note_cuda_error(e);
   moe::prof_before(MOE_KERNEL_DRAFT_VERIFY, s);
-  const cudaError_t e = q_d ? cudaLaunchKernelEx(&cfg, moe::verify_kernel<true>, a, ctas)
-                            : cudaLaunchKernelEx(&cfg, moe::verify_kernel<false>, a, ctas);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, ctas, cache_quads);
   moe::prof_after(MOE_KERNEL_DRAFT_VERIFY, s);
   return moe::note_cuda_error(e);
 }
