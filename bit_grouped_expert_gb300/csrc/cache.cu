@@ -12,7 +12,9 @@
 namespace moe {
 namespace {
 
-constexpr int PLAN_THREADS = 1024;
+// Threads of a planning CTA: one a sequence, and 128 where that is enough (its
+// barriers and scans are most of a small call).
+constexpr int PLAN_FEW = 128, PLAN_MANY = CACHE_MAX_SEQS;
 constexpr int COPY_THREADS = 256;
 
 // Exclusive prefix sum of one int per thread over the CTA; *total gets the
@@ -45,25 +47,25 @@ __device__ __forceinline__ int block_scan(int v, int *red, int *total) {
 }
 
 // The `want` lowest pages without holders into list[0 .. want-1]; returns how
-// many there are (at least want when it stopped early).
+// many there are (at least want when it stopped early).  Sixteen pages a
+// thread and round.
 __device__ __forceinline__ int find_free(const CacheView &c, int want, int *red, int32_t *list) {
   int found = 0;
-  for (int p0 = 0; p0 < c.n_pages && found < want; p0 += PLAN_THREADS * 4) {
-    const int p = p0 + threadIdx.x * 4;
-    int free4[4], n = 0;
+  for (int p0 = 0; p0 < c.n_pages && found < want; p0 += blockDim.x * 16) {
+    const int p = p0 + threadIdx.x * 16;
+    uint32_t free16 = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      free4[i] = p + i < c.n_pages && c.refs[p + i] == 0;
-      n += free4[i];
-    }
-    int total;
-    int at = found + block_scan(n, red, &total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (free4[i]) {
-        if (at < want) list[at] = p + i;
-        ++at;
+    for (int i = 0; i < 16; i += 4)
+      if (p + i + 4 <= c.n_pages) {
+        const int4 r = *reinterpret_cast<const int4 *>(c.refs + p + i);
+        free16 |= ((r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) | (r.w == 0 ? 8u : 0u)) << i;
+      } else {
+        for (int j = i; j < i + 4; ++j)
+          if (p + j < c.n_pages && c.refs[p + j] == 0) free16 |= 1u << j;
       }
+    int total;
+    int at = found + block_scan(__popc(free16), red, &total);
+    for (uint32_t m = free16; m && at < want; m &= m - 1) list[at++] = p + __ffs(m) - 1;
     found += total;
   }
   return found;
@@ -78,15 +80,33 @@ __device__ __forceinline__ int segment_of(const int *start, int n, int v) {
   return s;
 }
 
-// One row (a multiple of 64 values) by one warp, K and V together.
-__device__ __forceinline__ void copy_row(uint16_t *kd, uint16_t *vd, const uint16_t *ks, const uint16_t *vs, int row) {
+// One row (a multiple of 64 values) of K and V in `layers` layers, by one
+// warp; strides in values from layer to layer.  Two layers at a time, so that
+// eight 16-byte loads a lane are on their way before the first store.
+__device__ __forceinline__ void copy_rows(uint16_t *kd, uint16_t *vd, const uint16_t *ks, const uint16_t *vs, int row,
+                                          int layers, size_t to, size_t from) {
   const int lane = threadIdx.x & 31;
-  const uint4 *k4 = reinterpret_cast<const uint4 *>(ks), *v4 = reinterpret_cast<const uint4 *>(vs);
-  for (int i = lane; i < row / 8; i += 32) {
-    const uint4 x = k4[i], y = v4[i];
-    reinterpret_cast<uint4 *>(kd)[i] = x;
-    reinterpret_cast<uint4 *>(vd)[i] = y;
+  auto at = [](const uint16_t *p, size_t i) { return reinterpret_cast<const uint4 *>(p) + i; };
+  auto put = [](uint16_t *p, size_t i, uint4 x) { reinterpret_cast<uint4 *>(p)[i] = x; };
+  int l = 0;
+  for (; l + 2 <= layers; l += 2) {
+#pragma unroll 2
+    for (int i = lane; i < row / 8; i += 32) {
+      const uint4 k0 = *at(ks, i), v0 = *at(vs, i), k1 = *at(ks + from, i), v1 = *at(vs + from, i);
+      put(kd, i, k0);
+      put(vd, i, v0);
+      put(kd + to, i, k1);
+      put(vd + to, i, v1);
+    }
+    kd += 2 * to, vd += 2 * to, ks += 2 * from, vs += 2 * from;
   }
+  if (l < layers)
+#pragma unroll 2
+    for (int i = lane; i < row / 8; i += 32) {
+      const uint4 k0 = *at(ks, i), v0 = *at(vs, i);
+      put(kd, i, k0);
+      put(vd, i, v0);
+    }
 }
 
 // ---------------------------------------------------------------- append
@@ -107,10 +127,12 @@ struct AppendArgs {
   int32_t *rows;   // [1] rows to copy, 0 if the call changes nothing
   AppendSeg *seg;  // [B]
   int32_t *pages;  // the pages found
+  int per_job;     // layers a warp copies of a row
 };
 
-__global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ int red[33], slot_s[CACHE_MAX_SEQS], first_s[CACHE_MAX_SEQS], block_s[CACHE_MAX_SEQS], bad;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) append_plan_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ int red[33], slot_s[THREADS], first_s[THREADS], block_s[THREADS], bad;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CacheView &c = a.c;
   const int b = threadIdx.x, in_page = (1 << c.page_shift) - 1;
@@ -135,13 +157,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const __grid_
   __syncthreads();
   int need = 0, cow = 0, old_page = -1;
   if (in && ok) {
+    bool wrong = false;  // all looked at: no load or compare waits for the one before
     if (a.slots)
-      for (int i = 0; i < b; ++i) ok = ok && slot_s[i] != slot;
+#pragma unroll 8
+      for (int i = 0; i < b; ++i) wrong |= slot_s[i] == slot;
     if (a.path)
-      for (int i = 0; i < n; ++i) {
-        const int r = a.path[(size_t)b * a.path_stride + i];
-        ok = ok && r >= 0 && r < have;
-      }
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) wrong |= (unsigned)a.path[(size_t)b * a.path_stride + i] >= (unsigned)have;
+    ok = !wrong;
     if (ok && n > 0) {
       need = pages_of(L + n, c.page_shift) - pages_of(L, c.page_shift);
       if (L & in_page) {
@@ -181,7 +204,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const __grid_
   }
   if (b == 0) *a.rows = rows;
   __syncthreads();
-  for (int k = b; k < total; k += PLAN_THREADS) {
+  for (int k = b; k < total; k += THREADS) {
     const int s = segment_of(first_s, a.B, k), page = a.pages[k];
     c.table[(size_t)slot_s[s] * c.max_pages + block_s[s] + (k - first_s[s])] = page;
     c.refs[page] = 1;
@@ -197,19 +220,23 @@ __global__ void __launch_bounds__(COPY_THREADS) append_copy_kernel(const __grid_
   for (int b = threadIdx.x; b < a.B; b += COPY_THREADS) start_s[b] = a.seg[b].start;
   __syncthreads();
   const long long warps = (long long)gridDim.x * (COPY_THREADS / 32);
+  const int jobs = (c.n_layers + a.per_job - 1) / a.per_job;  // of a row
+  const size_t pool = ((size_t)c.n_pages << c.page_shift) * c.row;  // values of a layer
   for (long long job = (long long)blockIdx.x * (COPY_THREADS / 32) + (threadIdx.x >> 5);
-       job < (long long)rows * c.n_layers; job += warps) {
-    const int layer = (int)(job / rows), r = (int)(job - (long long)layer * rows);
+       job < (long long)rows * jobs; job += warps) {
+    const int group = (int)(job / rows), r = (int)(job - (long long)group * rows);
+    const int layer = group * a.per_job, layers = min(a.per_job, c.n_layers - layer);
     const int b = segment_of(start_s, a.B, r);
     const AppendSeg g = a.seg[b];
     int i = r - g.start, at;
     const uint16_t *ks = a.k_new, *vs = a.v_new;
-    size_t src;
+    size_t src, from = (size_t)a.n_rows * c.row;
     if (i < g.cow) {
       at = (g.len & ~in_page) + i;
       src = ((size_t)layer * c.n_pages + g.old_page) * (in_page + 1) + i;
       ks = c.k;
       vs = c.v;
+      from = pool;
     } else {
       i -= g.cow;
       at = g.len + i;
@@ -218,7 +245,7 @@ __global__ void __launch_bounds__(COPY_THREADS) append_copy_kernel(const __grid_
     const int page = c.table[(size_t)g.slot * c.max_pages + (at >> c.page_shift)];
     if ((unsigned)page >= (unsigned)c.n_pages) continue;
     const size_t dst = ((size_t)layer * c.n_pages + page) * (in_page + 1) + (at & in_page);
-    copy_row(c.k + dst * c.row, c.v + dst * c.row, ks + src * c.row, vs + src * c.row, c.row);
+    copy_rows(c.k + dst * c.row, c.v + dst * c.row, ks + src * c.row, vs + src * c.row, c.row, layers, pool, from);
   }
 }
 
@@ -237,10 +264,12 @@ struct ForkArgs {
   int32_t *rows;  // [2] rows to copy, pages to share; 0 if the call changes nothing
   ForkSeg *seg;   // [n]
   int32_t *pages;
+  int per_job;    // layers a warp copies of a row
 };
 
-__global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const __grid_constant__ ForkArgs a) {
-  __shared__ int red[33], src_s[CACHE_MAX_SEQS], dst_s[CACHE_MAX_SEQS], bad;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) fork_plan_kernel(const __grid_constant__ ForkArgs a) {
+  __shared__ int red[33], src_s[THREADS], dst_s[THREADS], bad;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CacheView &c = a.c;
   const int i = threadIdx.x, in_page = (1 << c.page_shift) - 1;
@@ -259,7 +288,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) fork_plan_kernel(const __grid_co
   }
   __syncthreads();
   if (in && ok) {
-    for (int j = 0; j < a.n; ++j) ok = ok && src_s[j] != dst && (j >= i || dst_s[j] != dst);
+    bool wrong = false;
+#pragma unroll 8
+    for (int j = 0; j < a.n; ++j) wrong |= src_s[j] == dst || (j < i && dst_s[j] == dst);
+    ok = !wrong;
     if (ok && (L & in_page)) {
       old_page = table_page(c, src, L >> c.page_shift);
       ok = old_page >= 0;
@@ -315,13 +347,16 @@ __global__ void __launch_bounds__(COPY_THREADS) fork_copy_kernel(const __grid_co
     if (page >= 0) atomicAdd(&c.refs[page], 1);
   }
   const long long warps = (long long)gridDim.x * (COPY_THREADS / 32);
+  const int jobs = (c.n_layers + a.per_job - 1) / a.per_job;  // of a row
+  const size_t pool = ((size_t)c.n_pages << c.page_shift) * c.row;  // values of a layer
   for (long long job = (long long)blockIdx.x * (COPY_THREADS / 32) + (threadIdx.x >> 5);
-       job < (long long)rows * c.n_layers; job += warps) {
-    const int layer = (int)(job / rows), r = (int)(job - (long long)layer * rows);
+       job < (long long)rows * jobs; job += warps) {
+    const int group = (int)(job / rows), r = (int)(job - (long long)group * rows);
+    const int layer = group * a.per_job, layers = min(a.per_job, c.n_layers - layer);
     const ForkSeg g = a.seg[segment_of(start_s, a.n, r)];
     const size_t base = (size_t)layer * c.n_pages, i = r - g.start;
     const size_t src = ((base + g.old_page) << c.page_shift) + i, dst = ((base + g.new_page) << c.page_shift) + i;
-    copy_row(c.k + dst * c.row, c.v + dst * c.row, c.k + src * c.row, c.v + src * c.row, c.row);
+    copy_rows(c.k + dst * c.row, c.v + dst * c.row, c.k + src * c.row, c.v + src * c.row, c.row, layers, pool, pool);
   }
 }
 
@@ -359,9 +394,20 @@ size_t append_ws(const attn_cache *c, int B, int n_rows, size_t *pages_at) {
   return *pages_at + ((size_t)n_rows / c->page_size + 2 * (size_t)B) * 4;
 }
 
-int copy_grid(long long jobs) {  // one warp a job, at most eight CTAs for each of 152 SMs
+// Warps of a copy at most: eight CTAs for each of 152 SMs.
+constexpr int COPY_CTAS = 152 * 8, COPY_WARPS = COPY_CTAS * (COPY_THREADS / 32);
+
+// Layers a warp copies of a row: all of them where the rows alone fill the
+// GPU twice, so that a row's place is looked up once; else enough to.
+int layers_per_job(long long rows, int n_layers) {
+  const long long n = rows * n_layers / (2 * COPY_WARPS);
+  return (int)(n < 1 ? 1 : n > n_layers ? n_layers : n);
+}
+
+int copy_grid(long long rows, int n_layers, int per_job) {
+  const long long jobs = rows * ((n_layers + per_job - 1) / per_job);
   const long long g = (jobs + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32);
-  return (int)(g < 1 ? 1 : g > 152 * 8 ? 152 * 8 : g);
+  return (int)(g < 1 ? 1 : g > COPY_CTAS ? COPY_CTAS : g);
 }
 
 }  // namespace
@@ -431,13 +477,17 @@ extern "C" moe_status attn_cache_append(const attn_cache *c, const void *k_new_d
   a.rows = static_cast<int32_t *>(ws_d);
   a.seg = moe::ws_ptr<moe::AppendSeg>(ws_d, 64);
   a.pages = moe::ws_ptr<int32_t>(ws_d, pages_at);
+  a.per_job = moe::layers_per_job(n_rows, c->n_layers);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = moe::launch_dep(false, moe::append_plan_kernel, dim3(1), dim3(moe::PLAN_THREADS), 0, s, a);
+  cudaError_t e = B <= moe::PLAN_FEW
+                      ? moe::launch_dep(false, moe::append_plan_kernel<moe::PLAN_FEW>, dim3(1), dim3(moe::PLAN_FEW), 0, s, a)
+                      : moe::launch_dep(false, moe::append_plan_kernel<moe::PLAN_MANY>, dim3(1), dim3(moe::PLAN_MANY), 0,
+                                        s, a);
   if (e != cudaSuccess) return moe::note_cuda_error(e);
   const bool pdl = moe::prof_quiet(MOE_KERNEL_CACHE_COPY);
   moe::prof_before(MOE_KERNEL_CACHE_COPY, s);
   // rows of a copied page come on top of the kept ones; the grid strides over all
-  e = moe::launch_dep(pdl, moe::append_copy_kernel, dim3(moe::copy_grid((long long)(n_rows + B) * c->n_layers)),
+  e = moe::launch_dep(pdl, moe::append_copy_kernel, dim3(moe::copy_grid(n_rows + B, c->n_layers, a.per_job)),
                       dim3(moe::COPY_THREADS), 0, s, a);
   moe::prof_after(MOE_KERNEL_CACHE_COPY, s);
   return moe::note_cuda_error(e);
@@ -467,15 +517,18 @@ extern "C" moe_status attn_cache_fork(const attn_cache *c, const int32_t *src_d,
   a.rows = static_cast<int32_t *>(ws_d);
   a.seg = moe::ws_ptr<moe::ForkSeg>(ws_d, 64);
   a.pages = moe::ws_ptr<int32_t>(ws_d, 64 + (size_t)n * sizeof(moe::ForkSeg));
+  const long long rows = (long long)n * (c->page_size / 2);  // half a page a fork on average
+  a.per_job = moe::layers_per_job(rows, c->n_layers);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = moe::launch_dep(false, moe::fork_plan_kernel, dim3(1), dim3(moe::PLAN_THREADS), 0, s, a);
+  cudaError_t e = n <= moe::PLAN_FEW
+                      ? moe::launch_dep(false, moe::fork_plan_kernel<moe::PLAN_FEW>, dim3(1), dim3(moe::PLAN_FEW), 0, s, a)
+                      : moe::launch_dep(false, moe::fork_plan_kernel<moe::PLAN_MANY>, dim3(1), dim3(moe::PLAN_MANY), 0, s,
+                                        a);
   if (e != cudaSuccess) return moe::note_cuda_error(e);
   const bool pdl = moe::prof_quiet(MOE_KERNEL_CACHE_COPY);
   moe::prof_before(MOE_KERNEL_CACHE_COPY, s);
-  // half a page of rows a fork on average
-  e = moe::launch_dep(pdl, moe::fork_copy_kernel,
-                      dim3(moe::copy_grid((long long)n * (c->page_size / 2) * c->n_layers)), dim3(moe::COPY_THREADS),
-                      0, s, a);
+  e = moe::launch_dep(pdl, moe::fork_copy_kernel, dim3(moe::copy_grid(rows, c->n_layers, a.per_job)),
+                      dim3(moe::COPY_THREADS), 0, s, a);
   moe::prof_after(MOE_KERNEL_CACHE_COPY, s);
   return moe::note_cuda_error(e);
 }
