@@ -3,7 +3,7 @@
 // The query heads of a KV head and the nodes of a tree together make the rows
 // of one matrix (row = node * G + head), so that a K or V tile read once
 // serves all of them: per tile of 64 positions
-//   S[128 rows x 64]  = Q . K^T     tcgen05, Q and K in shared memory
+//   S[128 rows x 64]  = Q . K^T     tcgen05, K in shared memory
 //   P = 2^(S - m)                   one thread a row, running maximum m and sum l
 //   O[128 rows x D]  += P . V       tcgen05, P in tensor memory, V in shared memory
 // A unit is (sequence, KV head, up to 128 rows); its tiles are the cached
@@ -34,36 +34,41 @@ namespace {
 
 constexpr int TR_MAXN = 256;      // nodes of a tree
 constexpr int TR_ROWS = 128;      // rows of a unit (MMA M)
-constexpr int TR_TILE = 64;       // positions of a tile
 constexpr int TR_MAX_SMS = 160;   // SMs used at most (the workspace is sized for them)
 constexpr float TR_SLACK = 8.f;   // growth of the maximum (log2) that O is not rescaled for
 constexpr unsigned long long TR_TIMEOUT_NS = 1000000000ull;
 
-template <int D>
+// D: head size.  WIDE (D = 256 only): tiles of 128 positions, for units of
+// many rows; the rule is at tree_wide().
+template <int D, bool WIDE>
 struct Cfg {
+  static_assert(!WIDE || D == 256, "wide tiles are for D = 256");
+  static constexpr int TILE = WIDE ? 128 : 64;      // positions of a tile
   static constexpr int CHUNKS = D / 64;             // 128-byte columns of a row
   static constexpr int CTAS = D == 256 ? 1 : 2;     // per SM
-  // one thread issues an MMA every 50 cycles or so: the scores' MMAs (N = 64,
-  // 32 cycles each) have a warp of their own where one CTA has the SM
+  // one thread issues an MMA every 50 cycles or so: the scores' MMAs have a
+  // warp of their own where one CTA has the SM
   static constexpr int ISSUERS = D == 256 ? 2 : 1;
-  // threads of a row, each with 64 / HALVES columns of S and D / HALVES of O
+  // threads of a row, each with TILE / HALVES columns of S and D / HALVES of O
   // (two CTAs have no registers for more than one)
   static constexpr int HALVES = D == 256 ? 2 : 1;
   static constexpr int ROW_WARPS = 4 * HALVES, LOADER = ROW_WARPS, WARPS = ROW_WARPS + 1 + ISSUERS;
   static constexpr int THREADS = WARPS * 32;
   // what a unit costs besides its tiles (its start and its result), in tiles
-  static constexpr int OVERHEAD = D == 256 ? 2 : 1;
-  static constexpr int Q_CHUNK = TR_ROWS * 128;     // bytes of one column of Q
-  static constexpr int KV_CHUNK = TR_TILE * 128;    // of a K or V tile
-  static constexpr int SLOT = CHUNKS * KV_CHUNK;    // one K or V tile
+  static constexpr int OVERHEAD = D == 256 && !WIDE ? 2 : 1;
+  // A tile of K or V takes PARTS ring slots: K by columns (CHUNKS / PARTS of
+  // them, TILE rows each), V by rows (64, all columns).
+  static constexpr int PARTS = WIDE ? 2 : 1;
+  static constexpr int SLOT = 64 * D * 2, Q_CHUNK = TR_ROWS * 128, V_CHUNK = 64 * 128, K_CHUNK = TILE * 128;
+  static constexpr int K_CHUNKS = CHUNKS / PARTS;   // columns of a K slot
   // Q is the MMA's A operand in tensor memory where there is room for it
-  // (D = 256: it goes through two ring slots first), else in shared memory.
-  // From shared memory the 64-wide score MMAs would read Q anew for every
-  // tile, as much again as K, V and their copies in together: a tile of 128
-  // rows then takes 1,500 cycles instead of 1,200.
-  static constexpr bool Q_TMEM = D == 256;
+  // (D = 256 but for wide tiles: it goes through two ring slots first), else
+  // in shared memory.  From there a score MMA of 64 positions reads more of Q
+  // than of K: a 64-wide tile of 128 rows then takes 1,900 cycles instead of 1,750.
+  static constexpr bool Q_TMEM = D == 256 && !WIDE;
   static constexpr int Q_SLOTS = Q_TMEM ? 2 : 0;
-  static constexpr int NS = D == 256 ? 7 : D == 128 ? 4 : 10;  // ring slots: what fits in 227 KB, or half of that
+  // ring slots: what fits in 227 KB, or half of that
+  static constexpr int NS = D == 256 ? (WIDE ? 5 : 7) : D == 128 ? 4 : 10;
   static constexpr int OFF_RING = Q_TMEM ? 0 : CHUNKS * Q_CHUNK;
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
   static constexpr int SMEM = OFF_MISC + 3 * 1024;
@@ -71,13 +76,13 @@ struct Cfg {
   // tensor memory columns: O, Q, two S tiles, each turned into P in place
   static constexpr uint32_t Q_COL = D, S_COL = Q_COL + (Q_TMEM ? D / 2 : 0);
   static constexpr uint32_t TMEM = D == 256 ? 512 : 256;
-  static_assert(S_COL + 2 * TR_TILE <= TMEM, "tensor memory");
+  static_assert(S_COL + 2 * TILE <= TMEM, "tensor memory");
 };
 
 struct TreeMaps {
   CUtensorMap q;             // {64, Hq, nodes, chunks}, boxes of G heads x nt nodes
-  CUtensorMap k, v;          // {64, pool rows, chunks}
-  CUtensorMap k_new, v_new;  // {64, nodes, chunks}
+  CUtensorMap k, v;          // {64, pool rows, chunks}: boxes of one page's rows of a slot
+  CUtensorMap k_new, v_new;  // {64, nodes, chunks}: boxes of a slot
 };
 
 // A CTA's split unit that starts with it, for the joining kernel.
@@ -97,7 +102,7 @@ struct TreeArgs {
   int B, n_nodes, max_nodes, Hq, Hkv, G;
   int nt;           // nodes of a unit
   int rows_cap;     // nt * G
-  int page_box;     // positions of one page-table entry that a tile takes (min(page, 64))
+  int page_box;     // rows of a box (min(page, 64))
   float scale_log2;
 };
 
@@ -134,12 +139,15 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
   return s;
 }
 
-__device__ __forceinline__ int tiles_of(int n) { return (n + TR_TILE - 1) / TR_TILE; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int n) {
+  return (n + TILE - 1) / TILE;
+}
 
-template <int OVH>
+template <typename C>
 __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
   if (s.n == 0) return 0;
-  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (OVH + tiles_of(s.L) + tiles_of(s.n));
+  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (C::OVERHEAD + tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n));
 }
 
 // x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
@@ -150,8 +158,9 @@ __device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
 
 // A CTA's walk over the units of its run.  A unit counts OVH + its tiles, the
 // overhead first, so that a CTA with more units has fewer tiles.
-template <int OVH>
+template <typename C>
 struct Walk {
+  static constexpr int OVH = C::OVERHEAD;
   const TreeArgs &a;
   int b;
   long long left;  // of the run, still to come
@@ -163,7 +172,7 @@ struct Walk {
 
   __device__ Walk(const TreeArgs &a_, int b0, const Seq &s0, long long off0, long long count)
       : a(a_), b(b0), left(count), s(s0), fresh(true) {
-    nt_all = tiles_of(s.L) + tiles_of(s.n);
+    nt_all = tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n);
     const int rts = (s.n + a.nt - 1) / a.nt, u = (int)mul_div(off0, 1, OVH + nt_all);
     g = u / rts;
     rt = u - g * rts;
@@ -182,7 +191,7 @@ struct Walk {
               s = load_seq(a, ++b);
             } while (s.n == 0 && b + 1 < a.B);
             if (s.n == 0) return false;
-            nt_all = tiles_of(s.L) + tiles_of(s.n);
+            nt_all = tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n);
           }
         }
       }
@@ -255,20 +264,20 @@ template <bool FP16>
 constexpr uint32_t EXP_MASK = FP16 ? 0x7C00u : 0x7F80u;  // all ones: infinity or NaN
 
 // Position of K(j) / V(j) of a unit of n tiles in the ring's load order
-// [Q Q] K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-template <int D>
+// [Q Q] K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), PARTS slots each.
+template <typename C>
 __device__ __forceinline__ uint32_t k_pos(int j) {
-  return Cfg<D>::Q_SLOTS + (j == 0 ? 0u : 2u * j - 1u);
+  return C::Q_SLOTS + C::PARTS * (j == 0 ? 0u : 2u * j - 1u);
 }
-template <int D>
+template <typename C>
 __device__ __forceinline__ uint32_t v_pos(int j, int n) {
-  return Cfg<D>::Q_SLOTS + (j == n - 1 ? 2u * n - 1u : 2u * j + 2u);
+  return C::Q_SLOTS + C::PARTS * (j == n - 1 ? 2u * n - 1u : 2u * j + 2u);
 }
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
+template <int D, bool FP16, bool WIDE>
+__global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, WIDE>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
   Misc *m = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   long long mine = 0;
   for (int b = sb; b < se; ++b) {
     seq = load_seq(a, b);
-    mine += seq_tiles<C::OVERHEAD>(a, seq);
+    mine += seq_tiles<C>(a, seq);
   }
   if (tid >= 32 && tid < 32 + C::NS) {
     ptx::mbar_init(&m->full[tid - 32], 1);
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     if (per > 1)
       for (;; ++b) {
         seq = load_seq(a, b);
-        const long long t = seq_tiles<C::OVERHEAD>(a, seq);
+        const long long t = seq_tiles<C>(a, seq);
         if (first < at + t) break;
         at += t;
       }
@@ -364,52 +373,84 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     m->off0 = first - at;
   }
   __syncthreads();
-  Walk<C::OVERHEAD> w(a, m->b0, m->s0, m->off0, end - first);
+  Walk<C> w(a, m->b0, m->s0, m->off0, end - first);
   uint8_t *ring = smem + C::OFF_RING;
   int32_t *status = a.c.status;
 
   if (warp == C::LOADER) {
     // ---------------------------------------------------------------- loads
-    const int pool_rows = a.c.n_pages << a.c.page_shift;
-    const int boxes = TR_TILE / a.page_box;  // table entries of a tile
-    const int my_page = boxes == 1 ? 0 : lane / C::CHUNKS, my_chunk = boxes == 1 ? 0 : lane % C::CHUNKS;
-    const bool issues = boxes == 1 ? lane == 0 : lane < boxes * C::CHUNKS;
-    const uint32_t box_bytes = (uint32_t)a.page_box * 128;
+    const int pool_rows = a.c.n_pages << a.c.page_shift, in_page = (1 << a.c.page_shift) - 1;
+    // boxes of a slot: this lane's rows and column of it.  A K slot of one
+    // column span and a V slot go in one box where a page holds all of its rows.
+    const int v_boxes = 64 / a.page_box, k_boxes = C::TILE / a.page_box;
+    const bool whole = v_boxes == 1;
+    const int v_box = whole ? 0 : lane / C::CHUNKS, v_chunk = whole ? 0 : lane % C::CHUNKS;
+    const bool v_issues = whole ? lane == 0 : lane < v_boxes * C::CHUNKS;
+    const int k_box = WIDE ? lane / C::K_CHUNKS : v_box, k_chunk = WIDE ? lane % C::K_CHUNKS : v_chunk;
+    const bool k_issues = WIDE ? lane < k_boxes * C::K_CHUNKS : v_issues;
+    const int box_bytes = a.page_box * 128;
     uint32_t ld = 0, units = 0;
     bool ok = true;
     while (ok && w.next()) {
-      const int L = w.s.L, n_old = tiles_of(L), x = w.g * C::CHUNKS, blocks = pages_of(L, a.c.page_shift);
+      const int L = w.s.L, n_old = tiles_of<C::TILE>(L), x = w.g * C::CHUNKS, blocks = pages_of(L, a.c.page_shift);
       const int32_t *table = a.c.table + (size_t)w.s.slot * a.c.max_pages;
-      int eb = -32, ent = 0;  // 32 table entries from block eb on, one a lane
-      // the pool row of this lane's box of tile t (past the pool, read as zeros, where there is none)
-      auto locate = [&](int t) {
-        const int blk0 = (t * TR_TILE) >> a.c.page_shift;
-        if (blk0 < eb || blk0 + boxes > eb + 32) {
-          eb = blk0;
+      int eb = -64, ent = 0;  // 32 table entries from block eb on, one a lane
+      // the pool row of position `pos`, lane by lane, all of them in the tile
+      // that begins at `base` (past the pool, read as zeros, where there is none)
+      auto locate = [&](int base, int pos) {
+        constexpr int SPAN = C::TILE / 16;  // blocks of a tile at most; the tile before stays in view
+        const int blk0 = base >> a.c.page_shift;
+        if (blk0 < eb || blk0 + SPAN > eb + 32) {
+          eb = max(0, blk0 - SPAN);
           ent = eb + lane < blocks ? table[eb + lane] : -1;
           if (eb + lane < blocks && (unsigned)ent >= (unsigned)a.c.n_pages) {
             set_status(status, MOE_ERR_DEVICE_BOUNDS);
             ent = -1;
           }
         }
-        const int p = __shfl_sync(0xffffffffu, ent, blk0 - eb + my_page % boxes);
-        return p < 0 ? pool_rows : (p << a.c.page_shift) + ((t * TR_TILE) & ((1 << a.c.page_shift) - 1));
+        const int p = __shfl_sync(0xffffffffu, ent, ((pos >> a.c.page_shift) - eb) & 31);
+        return p < 0 ? pool_rows : (p << a.c.page_shift) + (pos & in_page);
       };
-      auto load = [&](bool value_tile, int t, int row) {
+      // the next ring slot, its bytes announced; null if the wait gave up
+      auto take_slot = [&]() -> uint8_t * {
         const uint32_t slot = ld % C::NS;
-        if (!tr_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status)) return false;
+        if (!tr_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status)) return nullptr;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&m->full[slot], C::SLOT);
         __syncwarp();
-        uint8_t *dst = ring + slot * C::SLOT;
-        if (t >= n_old) {
-          if (lane == 0)
-            ptx::tma_load_3d(dst, value_tile ? &maps.v_new : &maps.k_new, &m->full[slot], 0,
-                             w.s.lo + (t - n_old) * TR_TILE, x);
-        } else if (issues) {
-          ptx::tma_load_3d(dst + my_chunk * C::KV_CHUNK + my_page * box_bytes, value_tile ? &maps.v : &maps.k,
-                           &m->full[slot], 0, row, x + my_chunk);
+        return ring + slot * C::SLOT;
+      };
+      auto load_k = [&](int t) {
+        for (int part = 0; part < C::PARTS; ++part) {
+          uint8_t *dst = take_slot();
+          if (!dst) return false;
+          uint64_t *bar = &m->full[ld % C::NS];
+          const int col = x + part * C::K_CHUNKS;
+          if (t >= n_old) {
+            if (lane == 0) ptx::tma_load_3d(dst, &maps.k_new, bar, 0, w.s.lo + (t - n_old) * C::TILE, col);
+          } else {
+            const int row = locate(t * C::TILE, t * C::TILE + k_box * a.page_box);
+            if (k_issues)
+              ptx::tma_load_3d(dst + k_chunk * C::K_CHUNK + k_box * box_bytes, &maps.k, bar, 0, row, col + k_chunk);
+          }
+          ++ld;
         }
-        ++ld;
+        return true;
+      };
+      auto load_v = [&](int t) {
+        for (int part = 0; part < C::PARTS; ++part) {
+          uint8_t *dst = take_slot();
+          if (!dst) return false;
+          uint64_t *bar = &m->full[ld % C::NS];
+          if (t >= n_old) {
+            if (lane == 0)
+              ptx::tma_load_3d(dst, &maps.v_new, bar, 0, w.s.lo + (t - n_old) * C::TILE + part * 64, x);
+          } else {
+            const int row = locate(t * C::TILE, t * C::TILE + part * 64 + v_box * a.page_box);
+            if (v_issues)
+              ptx::tma_load_3d(dst + v_chunk * C::V_CHUNK + v_box * box_bytes, &maps.v, bar, 0, row, x + v_chunk);
+          }
+          ++ld;
+        }
         return true;
       };
       if constexpr (C::Q_TMEM) {  // the unit's queries through the ring, two columns a slot
@@ -434,17 +475,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         }
       }
       ++units;
-      int row = w.t0 < n_old ? locate(w.t0) : 0;
-      ok = load(false, w.t0, row);
+      ok = load_k(w.t0);
       for (int j = 0; ok && j < w.n; ++j) {
-        const int t = w.t0 + j;
-        int next_row = 0;
-        if (j + 1 < w.n) {
-          if (t + 1 < n_old) next_row = locate(t + 1);
-          ok = load(false, t + 1, next_row);
-        }
-        ok = ok && load(true, t, row);
-        row = next_row;
+        if (j + 1 < w.n) ok = load_k(w.t0 + j + 1);
+        ok = ok && load_v(w.t0 + j);
       }
     }
     if (!ok && lane == 0) {  // loads of the last slots may still be in flight
@@ -455,52 +489,59 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   } else if (warp > C::LOADER) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::LOADER + 1, does_o = C::ISSUERS == 1 || !does_s;
-    const uint32_t id_s = ptx::idesc_f16(TR_TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
+    const uint32_t id_s = ptx::idesc_f16(C::TILE, FP16, false), id_o = ptx::idesc_f16(D, FP16, true);
     const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
     uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
     auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
-      const uint32_t slot = pos % C::NS;
       // the P tile in its place has been used up
       if (t >= 2 && !tr_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-      if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
-      ptx::tc_fence_after();
-      const uint64_t kd = ptx::sdesc_sw128(ptx::smem_u32(ring + slot * C::SLOT));
-      const uint32_t s_col = tmem + C::S_COL + (t & 1) * TR_TILE;
-      if (ptx::elect_one()) {
+      const uint32_t s_col = tmem + C::S_COL + (t & 1) * C::TILE;
 #pragma unroll
-        for (int ch = 0; ch < C::CHUNKS; ++ch)
+      for (int part = 0; part < C::PARTS; ++part, ++pos) {
+        const uint32_t slot = pos % C::NS;
+        if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+        ptx::tc_fence_after();
+        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_u32(ring + slot * C::SLOT));
+        if (ptx::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if constexpr (C::Q_TMEM)
-              ptx::mma_ts(s_col, tmem + C::Q_COL + 8 * (4 * ch + i), kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s,
-                          (ch | i) != 0);
-            else
-              ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, kd + (ch * C::KV_CHUNK + i * 32) / 16, id_s,
-                          (ch | i) != 0);
-        ptx::mma_commit(&m->empty[slot]);
-        ptx::mma_commit(&m->s_full[t & 1]);
+          for (int c = 0; c < C::K_CHUNKS; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int ch = part * C::K_CHUNKS + c;
+              const uint64_t b = kd + (c * C::K_CHUNK + i * 32) / 16;
+              if constexpr (C::Q_TMEM)
+                ptx::mma_ts(s_col, tmem + C::Q_COL + 8 * (4 * ch + i), b, id_s, (ch | i) != 0);
+              else
+                ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, b, id_s, (ch | i) != 0);
+            }
+          ptx::mma_commit(&m->empty[slot]);
+          if (part == C::PARTS - 1) ptx::mma_commit(&m->s_full[t & 1]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
     auto values = [&](uint32_t pos, uint32_t t, bool first) {  // O += P V of running tile t
-      const uint32_t slot = pos % C::NS;
       if (!tr_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
-          !tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status) ||
           (first && units > 0 && !tr_wait_warp(&m->o_free, (units - 1) & 1u, m, status)))
         return false;
-      ptx::tc_fence_after();
-      const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::KV_CHUNK);
-      const uint32_t p_col = tmem + C::S_COL + (t & 1) * TR_TILE;
-      if (ptx::elect_one()) {
+      const uint32_t p_col = tmem + C::S_COL + (t & 1) * C::TILE;
 #pragma unroll
-        for (int i = 0; i < TR_TILE / 16; ++i)
-          ptx::mma_ts(tmem, p_col + 8 * i, vd + i * 2048 / 16, id_o, !first || i > 0);
-        ptx::mma_commit(&m->empty[slot]);
-        ptx::mma_commit(&m->pv_done[t & 1]);
+      for (int part = 0; part < C::PARTS; ++part, ++pos) {
+        const uint32_t slot = pos % C::NS;
+        if (!tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+        ptx::tc_fence_after();
+        const uint64_t vd = ptx::sdesc_sw128_mn(ptx::smem_u32(ring + slot * C::SLOT), C::V_CHUNK);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ptx::mma_ts(tmem, p_col + 8 * (4 * part + i), vd + i * 2048 / 16, id_o, !first || part > 0 || i > 0);
+          ptx::mma_commit(&m->empty[slot]);
+          if (part == C::PARTS - 1) ptx::mma_commit(&m->pv_done[t & 1]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
     while (ok && w.next()) {
@@ -509,18 +550,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
         if (ok && C::Q_TMEM && ptx::elect_one())  // the rows have copied Q out of its slots
           for (int h = 0; h < C::Q_SLOTS; ++h) ptx::mbar_arrive(&m->empty[(ld + h) % C::NS]);
         __syncwarp();
-        ok = ok && scores(ld + k_pos<D>(0), jj);
+        ok = ok && scores(ld + k_pos<C>(0), jj);
       }
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
         if (does_s) {
-          if (j + 1 < w.n) ok = scores(ld + k_pos<D>(j + 1), jj + 1);
+          if (j + 1 < w.n) ok = scores(ld + k_pos<C>(j + 1), jj + 1);
           // the unit's last scores are under way
           if (ok && !C::Q_TMEM && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
           __syncwarp();
         }
-        if (ok && does_o) ok = values(ld + v_pos<D>(j, w.n), jj, j == 0);
+        if (ok && does_o) ok = values(ld + v_pos<C>(j, w.n), jj, j == 0);
       }
-      ld += C::Q_SLOTS + 2 * w.n;
+      ld += C::Q_SLOTS + 2 * C::PARTS * w.n;
       ++units;
     }
     __syncwarp();
@@ -529,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     tr_drain(&m->final_bar, 0);
   } else {
     // ----------------------------------------------------------------- rows
-    constexpr int COLS = TR_TILE / C::HALVES, OCOLS = D / C::HALVES;  // this thread's columns of S and of O
+    constexpr int COLS = C::TILE / C::HALVES, OCOLS = D / C::HALVES;  // this thread's columns of S and of O
     const int r = tid & (TR_ROWS - 1), half = tid / TR_ROWS;
     const int my_node = r / a.G, my_head = r - my_node * a.G;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -562,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     } un{};
     float mx = -INFINITY, sum = 0.f;
     bool in = false, real = false;
-    unsigned long long sees[TR_MAXN / TR_TILE] = {};
+    unsigned long long sees[TR_MAXN / 64] = {};
     auto finish = [&]() {
       if (!tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
@@ -591,8 +632,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           if (!in) continue;
           if (fix && real) {
             for (int i = 0; i < un.nodes; ++i) {
-              const int t = un.n_old + i / TR_TILE;
-              if (t < un.t0 || t >= un.t0 + un.n || !(sees[i / TR_TILE] >> (i % TR_TILE) & 1)) continue;
+              const int t = un.n_old + i / C::TILE;
+              if (t < un.t0 || t >= un.t0 + un.n || !(sees[i / 64] >> (i % 64) & 1)) continue;
               const uint16_t *src = a.v_new + (size_t)(un.lo + i) * a.c.row + un.g * D + d;
 #pragma unroll
               for (int q = 0; q < 32; ++q) {
@@ -664,19 +705,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       }
       if (un.n > 0) ok = finish();
       if (!more || !ok) break;
-      const int L = w.s.L, n_old = tiles_of(L);
+      const int L = w.s.L, n_old = tiles_of<C::TILE>(L);
       un = Unit{w.s.lo, w.s.n, w.node0(), w.nodes() * a.G, w.g, n_old, w.t0, w.n, w.nt_all, end - w.left};
       in = r < un.rows;
       real = in && own >= -1 && own < un.node0 + my_node;
       const bool active = (warp & 3) * 32 < un.rows;                     // the warp has rows
       const bool all_real = __all_sync(0xffffffffu, real || !in);  // none of them is padding
 #pragma unroll
-      for (int q = 0; q < TR_MAXN / TR_TILE; ++q) sees[q] = 0;
+      for (int q = 0; q < TR_MAXN / 64; ++q) sees[q] = 0;
       mx = -INFINITY;
       sum = 0.f;
       for (int j = 0; j < un.n; ++j, ++jj) {
         const int t = un.t0 + j;
-        const bool edge = t >= n_old || (t + 1) * TR_TILE > L;
+        const bool edge = t >= n_old || (t + 1) * C::TILE > L;
         if (t >= n_old && (j == 0 || t == n_old)) {
           // the first of the tree's own tiles: its parents, and what this row's node sees of each tile
           if (!(ok = rows_sync())) break;  // the last unit's readers are done
@@ -693,8 +734,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           if (!(ok = rows_sync())) break;
           for (int i = real ? un.node0 + my_node : -1; i >= 0; i = m->parent[i]) {
 #pragma unroll
-            for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
-              if (i / TR_TILE == q) sees[q] |= 1ull << (i % TR_TILE);
+            for (int q = 0; q < TR_MAXN / 64; ++q)
+              if (i / 64 == q) sees[q] |= 1ull << (i % 64);
           }
           __syncwarp();
         }
@@ -704,13 +745,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           // V rows that nobody may see become zeros (0 x NaN is NaN), and in the
           // tree's own tiles non-finite values as well: finish() adds them to
           // the rows that see them
-          const uint32_t pos = ld + v_pos<D>(j, un.n), slot = pos % C::NS;
-          if (!(ok = tr_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))) break;
-          uint8_t *v = ring + slot * C::SLOT;
-          for (int e = tid; e < TR_TILE * C::CHUNKS * 8; e += TR_ROWS * C::HALVES) {  // 16-byte pieces
-            const int ch = e / (TR_TILE * 8), q = (e / 8) % TR_TILE;
-            uint4 *piece = reinterpret_cast<uint4 *>(v + ch * C::KV_CHUNK + q * 128 + (e & 7) * 16);
-            const int at = t < n_old ? t * TR_TILE + q : (t - n_old) * TR_TILE + q;
+          const uint32_t pos = ld + v_pos<C>(j, un.n);
+          for (int part = 0; ok && part < C::PARTS; ++part)
+            ok = tr_wait_warp(&m->full[(pos + part) % C::NS], ((pos + part) / C::NS) & 1u, m, status);
+          if (!ok) break;
+          for (int e = tid; e < C::TILE * C::CHUNKS * 8; e += TR_ROWS * C::HALVES) {  // 16-byte pieces
+            const int part = e / (64 * C::CHUNKS * 8), ch = e / (64 * 8) % C::CHUNKS, q = (e / 8) % 64;
+            uint4 *piece = reinterpret_cast<uint4 *>(ring + (pos + part) % C::NS * C::SLOT + ch * C::V_CHUNK + q * 128 +
+                                                     (e & 7) * 16);
+            const int at = (t < n_old ? t : t - n_old) * C::TILE + part * 64 + q;
             const bool hold = t < n_old ? at < L : at < un.nodes && m->parent[at] != -2;
             if (!hold) {
               *piece = make_uint4(0u, 0u, 0u, 0u);
@@ -735,23 +778,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           uint32_t x[COLS / 32][32];
 #pragma unroll
           for (int h = 0; h < COLS / 32; ++h)
-            ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * TR_TILE + half * COLS + 32 * h, x[h]);
+            ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * C::TILE + half * COLS + 32 * h, x[h]);
           ptx::tmem_wait_ld();
           if (edge || !all_real) {
-            unsigned long long see = 0;
+            unsigned long long see = 0;  // of this thread's columns
             if (real) {
+              const int pos = (t < n_old ? t : t - n_old) * C::TILE + half * COLS;
               if (t < n_old) {
-                const int left = L - t * TR_TILE;
-                see = left >= TR_TILE ? ~0ull : (1ull << left) - 1;
+                const int left = L - pos;
+                see = left >= 64 ? ~0ull : left <= 0 ? 0 : (1ull << left) - 1;
               } else {
 #pragma unroll
-                for (int q = 0; q < TR_MAXN / TR_TILE; ++q)
-                  if (t - n_old == q) see = sees[q];
+                for (int q = 0; q < TR_MAXN / 64; ++q)
+                  if (pos / 64 == q) see = sees[q] >> (pos % 64);
               }
             }
 #pragma unroll
             for (int h = 0; h < COLS / 32; ++h) {
-              const uint32_t bits = (uint32_t)(see >> (half * COLS + 32 * h));
+              const uint32_t bits = (uint32_t)(see >> (32 * h));
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1)) x[h][i] = 0xFF800000u;  // -infinity
@@ -798,16 +842,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
             p[i / 2] = pack2<FP16>(p0, p1);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if constexpr (C::HALVES == 2)
-            ptx::tmem_st_x16(lanes + C::S_COL + (jj & 1) * TR_TILE + half * 16, p);
+          const uint32_t p_col = lanes + C::S_COL + (jj & 1) * C::TILE + half * (COLS / 2);
+          if constexpr (COLS == 32)
+            ptx::tmem_st_x16(p_col, p);
           else
-            ptx::tmem_st_x32(lanes + C::S_COL + (jj & 1) * TR_TILE, p);
+            ptx::tmem_st_x32(p_col, p);
           ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
       }
-      ld += C::Q_SLOTS + 2 * un.n;
+      ld += C::Q_SLOTS + 2 * C::PARTS * un.n;
     }
     if (tid == 0) a.desc[cta] = split;
   }
@@ -996,17 +1041,30 @@ size_t tree_ws(int D, int ctas, int rows_cap, size_t *ml_at, size_t *part_at) {
   return *part_at + (size_t)2 * ctas * rows_cap * D * 4;
 }
 
-template <int D, bool FP16>
+// Whether a unit's tiles are 128 positions wide instead of 64.
+bool tree_wide(int D, int rows_cap) { return D == 256 && rows_cap > 64; }
+
+template <int D, bool FP16, bool WIDE>
 cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
+  using C = Cfg<D, WIDE>;
   // per device and cheap: set on every call rather than remembered
-  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  cudaError_t e =
+      cudaFuncSetAttribute(tree_kernel<D, FP16, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   prof_before(MOE_KERNEL_ATTN_TREE, s);
   const bool quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
-  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(Cfg<D>::THREADS), Cfg<D>::SMEM, s, maps, a);
+  e = launch_dep(false, tree_kernel<D, FP16, WIDE>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
   return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_THREADS), 0, s, a, ctas);
+}
+
+template <bool FP16>
+cudaError_t launch_tree_d(int D, bool wide, const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
+  return D == 64    ? launch_tree<64, FP16, false>(maps, a, ctas, s)
+         : D == 128 ? launch_tree<128, FP16, false>(maps, a, ctas, s)
+         : wide     ? launch_tree<256, FP16, true>(maps, a, ctas, s)
+                    : launch_tree<256, FP16, false>(maps, a, ctas, s);
 }
 
 }  // namespace
@@ -1063,7 +1121,7 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.G = G;
   a.nt = moe::unit_nodes(G, max_nodes);
   a.rows_cap = a.nt * G;
-  a.page_box = c->page_size < moe::TR_TILE ? c->page_size : moe::TR_TILE;
+  a.page_box = c->page_size < 64 ? c->page_size : 64;
   a.scale_log2 = scale * 1.4426950408889634f;
   size_t ml_at, part_at;
   moe::tree_ws(D, ctas, a.rows_cap, &ml_at, &part_at);
@@ -1072,20 +1130,17 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.part = moe::ws_ptr<float>(ws_d, part_at);
   const int64_t pool_rows = (int64_t)c->n_pages * c->page_size;
   const uint16_t *k = a.c.k + (size_t)layer * pool_rows * a.c.row, *v = a.c.v + (size_t)layer * pool_rows * a.c.row;
-  const int chunks = a.page_box == moe::TR_TILE ? D / 64 : 1;
+  const bool wide = moe::tree_wide(D, a.rows_cap);
+  const int all = D / 64, boxed = a.page_box == 64 ? all : 1;  // columns of a slot, of a box
   moe::TreeMaps maps;
   if (!moe::query_map(&maps.q, q_d, n_nodes, Hq, D, G, a.nt) ||
-      !moe::row_map(&maps.k, k, pool_rows, a.c.row, D, a.page_box, chunks) ||
-      !moe::row_map(&maps.v, v, pool_rows, a.c.row, D, a.page_box, chunks) ||
-      !moe::row_map(&maps.k_new, k_new_d, n_nodes, a.c.row, D, moe::TR_TILE, D / 64) ||
-      !moe::row_map(&maps.v_new, v_new_d, n_nodes, a.c.row, D, moe::TR_TILE, D / 64))
+      !moe::row_map(&maps.k, k, pool_rows, a.c.row, D, a.page_box, wide ? 1 : boxed) ||
+      !moe::row_map(&maps.v, v, pool_rows, a.c.row, D, a.page_box, boxed) ||
+      !moe::row_map(&maps.k_new, k_new_d, n_nodes, a.c.row, D, wide ? 128 : 64, wide ? all / 2 : all) ||
+      !moe::row_map(&maps.v_new, v_new_d, n_nodes, a.c.row, D, 64, all))
     return moe::note_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp16 = c->dtype == MOE_FP16;
-  e = D == 64    ? (fp16 ? moe::launch_tree<64, true>(maps, a, ctas, s) : moe::launch_tree<64, false>(maps, a, ctas, s))
-      : D == 128 ? (fp16 ? moe::launch_tree<128, true>(maps, a, ctas, s)
-                         : moe::launch_tree<128, false>(maps, a, ctas, s))
-                 : (fp16 ? moe::launch_tree<256, true>(maps, a, ctas, s)
-                         : moe::launch_tree<256, false>(maps, a, ctas, s));
+  e = fp16 ? moe::launch_tree_d<true>(D, wide, maps, a, ctas, s) : moe::launch_tree_d<false>(D, wide, maps, a, ctas, s);
   return moe::note_cuda_error(e);
 }
