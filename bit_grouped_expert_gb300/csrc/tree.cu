@@ -38,44 +38,35 @@ constexpr int TR_MAX_SMS = 160;   // SMs used at most (the workspace is sized fo
 constexpr float TR_SLACK = 8.f;   // growth of the maximum (log2) that O is not rescaled for
 constexpr unsigned long long TR_TIMEOUT_NS = 1000000000ull;
 
-// D: head size.  WIDE (D = 256 only): tiles of 128 positions, for units of
-// many rows; the rule is at tree_wide().
-template <int D, bool WIDE>
+template <int D>
 struct Cfg {
-  static_assert(!WIDE || D == 256, "wide tiles are for D = 256");
-  static constexpr int TILE = WIDE ? 128 : 64;      // positions of a tile
+  static constexpr bool BIG = D == 256;             // one CTA has the SM; else two share it
+  static constexpr int CTAS = BIG ? 1 : 2;
+  // positions of a tile.  At D = 256 score MMAs of 64 positions would read
+  // more of Q than of K from shared memory, and one thread issues an MMA every 50
+  // cycles or so: 128-wide ones took 109 us where 64-wide ones took 117 (61
+  // nodes over 131,000 positions), and as long for few rows.
+  static constexpr int TILE = BIG ? 128 : 64;
   static constexpr int CHUNKS = D / 64;             // 128-byte columns of a row
-  static constexpr int CTAS = D == 256 ? 1 : 2;     // per SM
-  // one thread issues an MMA every 50 cycles or so: the scores' MMAs have a
-  // warp of their own where one CTA has the SM
-  static constexpr int ISSUERS = D == 256 ? 2 : 1;
+  static constexpr int ISSUERS = BIG ? 2 : 1;       // warps that issue MMAs (scores and output apart)
   // threads of a row, each with TILE / HALVES columns of S and D / HALVES of O
   // (two CTAs have no registers for more than one)
-  static constexpr int HALVES = D == 256 ? 2 : 1;
+  static constexpr int HALVES = BIG ? 2 : 1;
   static constexpr int ROW_WARPS = 4 * HALVES, LOADER = ROW_WARPS, WARPS = ROW_WARPS + 1 + ISSUERS;
   static constexpr int THREADS = WARPS * 32;
-  // what a unit costs besides its tiles (its start and its result), in tiles
-  static constexpr int OVERHEAD = D == 256 && !WIDE ? 2 : 1;
+  static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
   // A tile of K or V takes PARTS ring slots: K by columns (CHUNKS / PARTS of
   // them, TILE rows each), V by rows (64, all columns).
-  static constexpr int PARTS = WIDE ? 2 : 1;
+  static constexpr int PARTS = TILE / 64;
   static constexpr int SLOT = 64 * D * 2, Q_CHUNK = TR_ROWS * 128, V_CHUNK = 64 * 128, K_CHUNK = TILE * 128;
   static constexpr int K_CHUNKS = CHUNKS / PARTS;   // columns of a K slot
-  // Q is the MMA's A operand in tensor memory where there is room for it
-  // (D = 256 but for wide tiles: it goes through two ring slots first), else
-  // in shared memory.  From there a score MMA of 64 positions reads more of Q
-  // than of K: a 64-wide tile of 128 rows then takes 1,900 cycles instead of 1,750.
-  static constexpr bool Q_TMEM = D == 256 && !WIDE;
-  static constexpr int Q_SLOTS = Q_TMEM ? 2 : 0;
-  // ring slots: what fits in 227 KB, or half of that
-  static constexpr int NS = D == 256 ? (WIDE ? 5 : 7) : D == 128 ? 4 : 10;
-  static constexpr int OFF_RING = Q_TMEM ? 0 : CHUNKS * Q_CHUNK;
+  static constexpr int NS = D == 256 ? 5 : D == 128 ? 4 : 10;  // ring slots: what fits next to Q in 227 KB, or half of that
+  static constexpr int OFF_RING = CHUNKS * Q_CHUNK;
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
   static constexpr int SMEM = OFF_MISC + 3 * 1024;
   static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
-  // tensor memory columns: O, Q, two S tiles, each turned into P in place
-  static constexpr uint32_t Q_COL = D, S_COL = Q_COL + (Q_TMEM ? D / 2 : 0);
-  static constexpr uint32_t TMEM = D == 256 ? 512 : 256;
+  // tensor memory columns: O, then two S tiles, each turned into P in place
+  static constexpr uint32_t S_COL = D, TMEM = BIG ? 512 : 256;
   static_assert(S_COL + 2 * TILE <= TMEM, "tensor memory");
 };
 
@@ -87,8 +78,9 @@ struct TreeMaps {
 
 // A CTA's split unit that starts with it, for the joining kernel.
 struct SplitDesc {
-  int32_t parts;  // CTAs it spans (0: none)
-  int32_t rows, node0, head0;
+  int32_t parts;   // CTAs it spans (0: none)
+  int32_t stride;  // from one of them to the next
+  int32_t rows, node0, head0, pad[3];
 };
 
 struct TreeArgs {
@@ -110,16 +102,26 @@ struct Seq {
   int slot, L, lo, n;  // n == 0: nothing to do
 };
 
+struct Count {
+  long long team, alone;  // with one row tile of a (sequence, KV head), with all
+};
+
 struct Misc {
   uint64_t full[10], empty[10];
-  uint64_t q_full, q_free, q_ready, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, pair_bar[4], final_bar;
+  uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, pair_bar[4], final_bar;
   uint32_t tmem;
   int abort_flag, nonfinite;
   int b0;
   Seq s0;
-  long long off0, wsum[12];
+  long long off0;
   int16_t parent[TR_MAXN];
-  float row[2][2][TR_ROWS];  // what the two threads of a row exchange, [turn][half]
+  union {
+    struct {
+      Count wsum[12];
+      int wrts[12];
+    };
+    float row[2][2][TR_ROWS];  // later: what the two threads of a row exchange, [turn][half]
+  };
 };
 static_assert(sizeof(Misc) <= 3 * 1024, "misc area");
 
@@ -144,11 +146,12 @@ __device__ __forceinline__ int tiles_of(int n) {
   return (n + TILE - 1) / TILE;
 }
 
+// A sequence's count for one row tile of every KV head, and its row tiles.
 template <typename C>
 __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
-  if (s.n == 0) return 0;
-  return (long long)a.Hkv * ((s.n + a.nt - 1) / a.nt) * (C::OVERHEAD + tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n));
+  return s.n == 0 ? 0 : (long long)a.Hkv * (C::OVERHEAD + tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n));
 }
+__device__ __forceinline__ int row_tiles(const TreeArgs &a, const Seq &s) { return (s.n + a.nt - 1) / a.nt; }
 
 // x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
 __device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
@@ -157,7 +160,9 @@ __device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
 }
 
 // A CTA's walk over the units of its run.  A unit counts OVH + its tiles, the
-// overhead first, so that a CTA with more units has fewer tiles.
+// overhead first, so that a CTA with more units has fewer tiles.  Alone, CTAs
+// cut the row of all units (sequence, KV head, row tile); in teams, a team cuts
+// the row of all (sequence, KV head) and its member i has row tile i of each.
 template <typename C>
 struct Walk {
   static constexpr int OVH = C::OVERHEAD;
@@ -165,17 +170,18 @@ struct Walk {
   int b;
   long long left;  // of the run, still to come
   Seq s;
+  int member;      // the row tile of a team's member, -1 alone
   int g, rt, off;  // unit, and where in its count the run's part begins
   int nt_all;      // tiles of the unit
   int t0, n;       // this CTA's: the first, and how many
   bool fresh;
 
-  __device__ Walk(const TreeArgs &a_, int b0, const Seq &s0, long long off0, long long count)
-      : a(a_), b(b0), left(count), s(s0), fresh(true) {
+  __device__ Walk(const TreeArgs &a_, int b0, const Seq &s0, long long off0, long long count, int member_)
+      : a(a_), b(b0), left(count), s(s0), member(member_), fresh(true) {
     nt_all = tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n);
-    const int rts = (s.n + a.nt - 1) / a.nt, u = (int)mul_div(off0, 1, OVH + nt_all);
+    const int rts = member < 0 ? row_tiles(a, s) : 1, u = (int)mul_div(off0, 1, OVH + nt_all);
     g = u / rts;
-    rt = u - g * rts;
+    rt = member < 0 ? u - g * rts : member;
     off = (int)(off0 - (long long)u * (OVH + nt_all));
   }
   // the next unit with tiles for this CTA; false when the run is done
@@ -183,8 +189,8 @@ struct Walk {
     while (left > 0) {
       if (!fresh) {
         off = 0;
-        if (++rt * a.nt >= s.n) {
-          rt = 0;
+        if (member >= 0 || ++rt * a.nt >= s.n) {
+          rt = max(member, 0);
           if (++g >= a.Hkv) {
             g = 0;
             do {  // left > 0: a later sequence has tiles
@@ -200,7 +206,7 @@ struct Walk {
       left -= take;
       t0 = max(0, off - OVH);
       n = max(0, off + take - OVH) - t0;
-      if (n > 0) return true;
+      if (n > 0 && rt * a.nt < s.n) return true;  // a smaller tree has nothing for some members
     }
     return false;
   }
@@ -264,20 +270,20 @@ template <bool FP16>
 constexpr uint32_t EXP_MASK = FP16 ? 0x7C00u : 0x7F80u;  // all ones: infinity or NaN
 
 // Position of K(j) / V(j) of a unit of n tiles in the ring's load order
-// [Q Q] K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), PARTS slots each.
+// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), PARTS slots each.
 template <typename C>
 __device__ __forceinline__ uint32_t k_pos(int j) {
-  return C::Q_SLOTS + C::PARTS * (j == 0 ? 0u : 2u * j - 1u);
+  return C::PARTS * (j == 0 ? 0u : 2u * j - 1u);
 }
 template <typename C>
 __device__ __forceinline__ uint32_t v_pos(int j, int n) {
-  return C::Q_SLOTS + C::PARTS * (j == n - 1 ? 2u * n - 1u : 2u * j + 2u);
+  return C::PARTS * (j == n - 1 ? 2u * n - 1u : 2u * j + 2u);
 }
 
-template <int D, bool FP16, bool WIDE>
-__global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
+template <int D, bool FP16>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
-  using C = Cfg<D, WIDE>;
+  using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
   Misc *m = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -307,10 +313,14 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
   // down where that is.
   const int per = (a.B + C::THREADS - 1) / C::THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
   Seq seq{0, 0, 0, 0};
-  long long mine = 0;
+  Count mine{0, 0};
+  int rts = 0;  // most row tiles
   for (int b = sb; b < se; ++b) {
     seq = load_seq(a, b);
-    mine += seq_tiles<C>(a, seq);
+    const long long t = seq_tiles<C>(a, seq);
+    mine.team += t;
+    mine.alone += t * row_tiles(a, seq);
+    rts = max(rts, row_tiles(a, seq));
   }
   if (tid >= 32 && tid < 32 + C::NS) {
     ptx::mbar_init(&m->full[tid - 32], 1);
@@ -320,7 +330,6 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     m->abort_flag = 0;
     ptx::mbar_init(&m->q_full, 1);
     ptx::mbar_init(&m->q_free, 1);
-    ptx::mbar_init(&m->q_ready, C::ROW_WARPS);
     ptx::mbar_init(&m->final_bar, C::ISSUERS);
     ptx::fence_mbar_init();
   } else if (tid == 96) {
@@ -334,37 +343,57 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&m->pair_bar[i], C::HALVES);
     ptx::fence_mbar_init();
   }
-  long long inc = mine;
+  Count inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
+    const long long t = __shfl_up_sync(0xffffffffu, inc.team, o), u = __shfl_up_sync(0xffffffffu, inc.alone, o);
+    rts = max(rts, __shfl_xor_sync(0xffffffffu, rts, o));
+    if (lane >= o) {
+      inc.team += t;
+      inc.alone += u;
+    }
   }
-  if (lane == 31) m->wsum[warp] = inc;
+  if (lane == 31) {
+    m->wsum[warp] = inc;
+    m->wrts[warp] = rts;
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = m->tmem;
-  long long before = inc - mine, T = 0;
+  Count all{0, 0};
 #pragma unroll
   for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += m->wsum[w];
-    T += m->wsum[w];
+    all.team += m->wsum[w].team;
+    all.alone += m->wsum[w].alone;
+    rts = max(rts, m->wrts[w]);
   }
-  const int ctas = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x), cta = blockIdx.x;
-  if (cta >= ctas) {  // less to do than CTAs
+  // Teams of one CTA a row tile read a tile of K and V at the same time, so
+  // that it comes from DRAM once: 16 trees of 61 nodes over 8,000 positions each
+  // (268 MB, more than L2) took 192 us alone.  Not where trees of different
+  // sizes would leave a fifth of the members without work.
+  const int grid = gridDim.x, cta = blockIdx.x;
+  const bool teams = rts > 1 && rts <= grid && 4 * all.team * grid <= 5 * all.alone * (grid / rts);
+  const int size = teams ? rts : 1;
+  const long long T = teams ? all.team : all.alone;
+  long long before = 0;
+  for (int w = 0; w < warp; ++w) before += teams ? m->wsum[w].team : m->wsum[w].alone;
+  const long long held = teams ? mine.team : mine.alone;
+  before += (teams ? inc.team : inc.alone) - held;
+  const int runs = (int)(T < (long long)(grid / size) ? T : (long long)(grid / size)), run = cta / size;
+  if (run >= runs) {  // less to do than CTAs
     if (tid == 0) a.desc[cta].parts = 0;
     if (warp == C::LOADER + 1) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
-  const long long first = mul_div(T, cta, ctas), end = mul_div(T, cta + 1, ctas);
-  if (first >= before && first < before + mine) {
+  const long long first = mul_div(T, run, runs), end = mul_div(T, run + 1, runs);
+  if (first >= before && first < before + held) {
     long long at = before;
     int b = sb;
     if (per > 1)
       for (;; ++b) {
         seq = load_seq(a, b);
-        const long long t = seq_tiles<C>(a, seq);
+        const long long t = seq_tiles<C>(a, seq) * (teams ? 1 : row_tiles(a, seq));
         if (first < at + t) break;
         at += t;
       }
@@ -373,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     m->off0 = first - at;
   }
   __syncthreads();
-  Walk<C> w(a, m->b0, m->s0, m->off0, end - first);
+  Walk<C> w(a, m->b0, m->s0, m->off0, end - first, teams ? cta - run * size : -1);
   uint8_t *ring = smem + C::OFF_RING;
   int32_t *status = a.c.status;
 
@@ -386,8 +415,8 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     const bool whole = v_boxes == 1;
     const int v_box = whole ? 0 : lane / C::CHUNKS, v_chunk = whole ? 0 : lane % C::CHUNKS;
     const bool v_issues = whole ? lane == 0 : lane < v_boxes * C::CHUNKS;
-    const int k_box = WIDE ? lane / C::K_CHUNKS : v_box, k_chunk = WIDE ? lane % C::K_CHUNKS : v_chunk;
-    const bool k_issues = WIDE ? lane < k_boxes * C::K_CHUNKS : v_issues;
+    const int k_box = C::PARTS > 1 ? lane / C::K_CHUNKS : v_box, k_chunk = C::PARTS > 1 ? lane % C::K_CHUNKS : v_chunk;
+    const bool k_issues = C::PARTS > 1 ? lane < k_boxes * C::K_CHUNKS : v_issues;
     const int box_bytes = a.page_box * 128;
     uint32_t ld = 0, units = 0;
     bool ok = true;
@@ -453,26 +482,13 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
         }
         return true;
       };
-      if constexpr (C::Q_TMEM) {  // the unit's queries through the ring, two columns a slot
-        for (int h = 0; ok && h < C::Q_SLOTS; ++h, ++ld) {
-          const uint32_t slot = ld % C::NS;
-          ok = tr_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status);
-          if (ok && lane == 0) {
-            ptx::mbar_arrive_expect_tx(&m->full[slot], (uint32_t)(a.rows_cap * 256));
-            for (int i = 0; i < 2; ++i)
-              ptx::tma_load_4d(ring + slot * C::SLOT + i * C::Q_CHUNK, &maps.q, &m->full[slot], 0, w.g * a.G,
-                               w.s.lo + w.node0(), 2 * h + i);
-          }
-        }
-        if (!ok) break;
-      } else {  // in their own place, once the last unit's scores are done
-        ok = units == 0 || tr_wait_warp(&m->q_free, (units - 1) & 1u, m, status);
-        if (!ok) break;
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
-          for (int ch = 0; ch < C::CHUNKS; ++ch)
-            ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
-        }
+      // the unit's queries, once the last unit's scores are done
+      ok = units == 0 || tr_wait_warp(&m->q_free, (units - 1) & 1u, m, status);
+      if (!ok) break;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
+        for (int ch = 0; ch < C::CHUNKS; ++ch)
+          ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
       }
       ++units;
       ok = load_k(w.t0);
@@ -482,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
       }
     }
     if (!ok && lane == 0) {  // loads of the last slots may still be in flight
-      if (!C::Q_TMEM && units) tr_drain(&m->q_full, (units - 1) & 1u);
+      if (units) tr_drain(&m->q_full, (units - 1) & 1u);
       for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
         tr_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
     }
@@ -510,10 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
             for (int i = 0; i < 4; ++i) {
               const int ch = part * C::K_CHUNKS + c;
               const uint64_t b = kd + (c * C::K_CHUNK + i * 32) / 16;
-              if constexpr (C::Q_TMEM)
-                ptx::mma_ts(s_col, tmem + C::Q_COL + 8 * (4 * ch + i), b, id_s, (ch | i) != 0);
-              else
-                ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, b, id_s, (ch | i) != 0);
+              ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, b, id_s, (ch | i) != 0);
             }
           ptx::mma_commit(&m->empty[slot]);
           if (part == C::PARTS - 1) ptx::mma_commit(&m->s_full[t & 1]);
@@ -546,22 +559,18 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     };
     while (ok && w.next()) {
       if (does_s) {
-        ok = tr_wait_warp(C::Q_TMEM ? &m->q_ready : &m->q_full, units & 1u, m, status);
-        if (ok && C::Q_TMEM && ptx::elect_one())  // the rows have copied Q out of its slots
-          for (int h = 0; h < C::Q_SLOTS; ++h) ptx::mbar_arrive(&m->empty[(ld + h) % C::NS]);
-        __syncwarp();
-        ok = ok && scores(ld + k_pos<C>(0), jj);
+        ok = tr_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_pos<C>(0), jj);
       }
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
         if (does_s) {
           if (j + 1 < w.n) ok = scores(ld + k_pos<C>(j + 1), jj + 1);
           // the unit's last scores are under way
-          if (ok && !C::Q_TMEM && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
+          if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
           __syncwarp();
         }
         if (ok && does_o) ok = values(ld + v_pos<C>(j, w.n), jj, j == 0);
       }
-      ld += C::Q_SLOTS + 2 * C::PARTS * w.n;
+      ld += 2 * C::PARTS * w.n;
       ++units;
     }
     __syncwarp();
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t ld = 0, jj = 0, syncs = 0, pairs = 0;
     bool ok = true;
-    SplitDesc split{0, 0, 0, 0};
+    SplitDesc split{};
     // one arrival a warp, for all of its lanes
     auto arrive = [&](uint64_t *bar) {
       __syncwarp();
@@ -596,10 +605,10 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
       return m->row[turn][half ^ 1][r];
     };
     // The unit whose tiles were the last: its result is taken out of tensor
-    // memory only once the next unit's queries are in, so that its scores run meanwhile.
+    // memory while the next unit's first scores run.
     struct Unit {
       int lo, nodes, node0, rows, g, n_old, t0, n, nt_all;
-      long long done;  // where this CTA's part ends in the count of all units
+      long long done;  // where this CTA's part ends in the count of all
     } un{};
     float mx = -INFINITY, sum = 0.f;
     bool in = false, real = false;
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
-        split = SplitDesc{(int)mul_div(u1 * ctas + T - 1, 1, T) - cta, un.rows, un.lo + un.node0, un.g * a.G};
+        split = SplitDesc{(int)mul_div(u1 * runs + T - 1, 1, T) - run, size, un.rows, un.lo + un.node0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = un.t0 + un.n > un.n_old && *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
@@ -680,28 +689,6 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
 #pragma unroll
         for (int i = 0; i < UPS; ++i) up[i] = tid + i * TR_ROWS < w.s.n ? __ldg(parent + tid + i * TR_ROWS) : -2;
         if (my_node < w.nodes()) own = __ldg(parent + w.node0() + my_node);
-        if constexpr (C::Q_TMEM) {
-          // this row of Q from the ring into tensor memory (the last unit's
-          // scores, which read the one before, are done)
-#pragma unroll 1
-          for (int h = half; h < C::Q_SLOTS; h += C::HALVES) {
-            const uint32_t slot = (ld + h) % C::NS;
-            if (!(ok = tr_wait_warp(&m->full[slot], ((ld + h) / C::NS) & 1u, m, status))) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t x[32];
-              const uint8_t *src = ring + slot * C::SLOT + i * C::Q_CHUNK + r * 128;
-#pragma unroll
-              for (int p = 0; p < 8; ++p)  // 16-byte pieces, swizzled by the row
-                *reinterpret_cast<uint4 *>(x + 4 * p) = *reinterpret_cast<const uint4 *>(src + ((p ^ (r & 7)) * 16));
-              ptx::tmem_st_x32(lanes + C::Q_COL + (2 * h + i) * 32, x);
-            }
-          }
-          if (!ok) break;
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          arrive(&m->q_ready);
-        }
       }
       if (un.n > 0) ok = finish();
       if (!more || !ok) break;
@@ -852,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, WIDE>::THREADS, Cfg<D, WIDE>::CTAS)
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
       }
-      ld += C::Q_SLOTS + 2 * C::PARTS * un.n;
+      ld += 2 * C::PARTS * un.n;
     }
     if (tid == 0) a.desc[cta] = split;
   }
@@ -950,7 +937,7 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_cons
       M = mn;
     };
     if (in) {
-      // part i lies in CTA c0 + i's second slot if it starts the unit, else in its first
+      // part 0 lies in its CTA's second slot, the others in their CTAs' first
       for (int i0 = grp; i0 < ds.parts; i0 += 2 * groups) {
         float2 ml[2];
         float4 v[2][4];
@@ -959,7 +946,7 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_cons
           const int i = i0 + k * groups;
           ml[k] = make_float2(-INFINITY, 0.f);
           if (i < ds.parts) {
-            const size_t p = (size_t)2 * (c0 + i) + (i == 0 ? 1 : 0);
+            const size_t p = (size_t)2 * (c0 + i * ds.stride) + (i == 0 ? 1 : 0);
             ml[k] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
             const float4 *src = reinterpret_cast<const float4 *>(a.part) + (p * (D / 4) + c4) * a.rows_cap + r;
 #pragma unroll
@@ -1041,30 +1028,25 @@ size_t tree_ws(int D, int ctas, int rows_cap, size_t *ml_at, size_t *part_at) {
   return *part_at + (size_t)2 * ctas * rows_cap * D * 4;
 }
 
-// Whether a unit's tiles are 128 positions wide instead of 64.
-bool tree_wide(int D, int rows_cap) { return D == 256 && rows_cap > 64; }
-
-template <int D, bool FP16, bool WIDE>
+template <int D, bool FP16>
 cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
-  using C = Cfg<D, WIDE>;
+  using C = Cfg<D>;
   // per device and cheap: set on every call rather than remembered
-  cudaError_t e =
-      cudaFuncSetAttribute(tree_kernel<D, FP16, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   prof_before(MOE_KERNEL_ATTN_TREE, s);
   const bool quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
-  e = launch_dep(false, tree_kernel<D, FP16, WIDE>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
+  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
   return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_THREADS), 0, s, a, ctas);
 }
 
 template <bool FP16>
-cudaError_t launch_tree_d(int D, bool wide, const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
-  return D == 64    ? launch_tree<64, FP16, false>(maps, a, ctas, s)
-         : D == 128 ? launch_tree<128, FP16, false>(maps, a, ctas, s)
-         : wide     ? launch_tree<256, FP16, true>(maps, a, ctas, s)
-                    : launch_tree<256, FP16, false>(maps, a, ctas, s);
+cudaError_t launch_tree_d(int D, const TreeMaps &maps, const TreeArgs &a, int ctas, cudaStream_t s) {
+  return D == 64    ? launch_tree<64, FP16>(maps, a, ctas, s)
+         : D == 128 ? launch_tree<128, FP16>(maps, a, ctas, s)
+                    : launch_tree<256, FP16>(maps, a, ctas, s);
 }
 
 }  // namespace
@@ -1130,7 +1112,7 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.part = moe::ws_ptr<float>(ws_d, part_at);
   const int64_t pool_rows = (int64_t)c->n_pages * c->page_size;
   const uint16_t *k = a.c.k + (size_t)layer * pool_rows * a.c.row, *v = a.c.v + (size_t)layer * pool_rows * a.c.row;
-  const bool wide = moe::tree_wide(D, a.rows_cap);
+  const bool wide = D == 256;  // K tiles of two column spans
   const int all = D / 64, boxed = a.page_box == 64 ? all : 1;  // columns of a slot, of a box
   moe::TreeMaps maps;
   if (!moe::query_map(&maps.q, q_d, n_nodes, Hq, D, G, a.nt) ||
@@ -1141,6 +1123,6 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
     return moe::note_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp16 = c->dtype == MOE_FP16;
-  e = fp16 ? moe::launch_tree_d<true>(D, wide, maps, a, ctas, s) : moe::launch_tree_d<false>(D, wide, maps, a, ctas, s);
+  e = fp16 ? moe::launch_tree_d<true>(D, maps, a, ctas, s) : moe::launch_tree_d<false>(D, maps, a, ctas, s);
   return moe::note_cuda_error(e);
 }
