@@ -418,7 +418,7 @@ moe_status cache_view(const attn_cache *c, CacheView *out) {
     return MOE_ERR_INVALID_ARGUMENT;
   const int ps = c->page_size, D = c->head_dim;
   if ((ps & (ps - 1)) || ps < 16 || ps > 256 || (D != 64 && D != 128 && D != 256) || c->n_kv_heads > 256 ||
-      (int64_t)c->n_pages * ps > INT32_MAX || (int64_t)c->max_pages * ps > INT32_MAX ||
+      (int64_t)c->n_pages * ps > INT32_MAX || (int64_t)c->max_pages * ps > (1 << 30) ||
       (c->dtype != MOE_BF16 && c->dtype != MOE_FP16))
     return MOE_ERR_UNSUPPORTED;
   if (!aligned16(c->k_d) || !aligned16(c->v_d) || !aligned16(c->refs_d) || !aligned16(c->table_d) ||

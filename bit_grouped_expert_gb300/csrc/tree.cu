@@ -93,6 +93,7 @@ struct TreeArgs {
   float *part;      // [2 * grid][D / 4][rows_cap][4]
   int B, n_nodes, max_nodes, Hq, Hkv, G;
   int nt;           // nodes of a unit
+  int nt_mul, g_mul;  // 2^16 / nt + 1 and 2^16 / G + 1: x / nt = x nt_mul >> 16 for x < 2^9 (nt, G <= 128)
   int rows_cap;     // nt * G
   int page_box;     // rows of a box (min(page, 64))
   float scale_log2;
@@ -151,12 +152,16 @@ template <typename C>
 __device__ __forceinline__ long long seq_tiles(const TreeArgs &a, const Seq &s) {
   return s.n == 0 ? 0 : (long long)a.Hkv * (C::OVERHEAD + tiles_of<C::TILE>(s.L) + tiles_of<C::TILE>(s.n));
 }
-__device__ __forceinline__ int row_tiles(const TreeArgs &a, const Seq &s) { return (s.n + a.nt - 1) / a.nt; }
+__device__ __forceinline__ int row_tiles(const TreeArgs &a, const Seq &s) {
+  return (s.n + a.nt - 1) * a.nt_mul >> 16;
+}
 
 // x y / z, in 32 bits where that is enough (a 64-bit division takes hundreds of cycles).
+// (its many instructions apart: a CTA's start is mostly their fetching)
+__device__ __noinline__ long long div_long(long long p, long long z) { return p / z; }
 __device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
   const long long p = x * y;
-  return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
+  return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : div_long(p, z);
 }
 
 // A CTA's walk over the units of its run.  A unit counts OVH + its tiles, the
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     ptx::fence_mbar_init();
   }
   Count inc = mine;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, inc.team, o), u = __shfl_up_sync(0xffffffffu, inc.alone, o);
     rts = max(rts, __shfl_xor_sync(0xffffffffu, rts, o));
@@ -361,13 +366,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = m->tmem;
-  Count all{0, 0};
-#pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    all.team += m->wsum[w].team;
-    all.alone += m->wsum[w].alone;
-    rts = max(rts, m->wrts[w]);
+  // the warps' counts, a lane each
+  Count upto = lane < C::WARPS ? m->wsum[lane] : Count{0, 0};
+  rts = (int)__reduce_max_sync(0xffffffffu, lane < C::WARPS ? (unsigned)m->wrts[lane] : 0u);
+#pragma unroll 1
+  for (int o = 1; o < 16; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, upto.team, o), u = __shfl_up_sync(0xffffffffu, upto.alone, o);
+    if (lane >= o) {
+      upto.team += t;
+      upto.alone += u;
+    }
   }
+  static_assert(C::WARPS <= 16, "four steps");
+  const Count all{__shfl_sync(0xffffffffu, upto.team, 15), __shfl_sync(0xffffffffu, upto.alone, 15)};
   // Teams of one CTA a row tile read a tile of K and V at the same time, so
   // that it comes from DRAM once: 16 trees of 61 nodes over 8,000 positions each
   // (268 MB, more than L2) took 192 us alone.  Not where trees of different
@@ -376,8 +387,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   const bool teams = rts > 1 && rts <= grid && 4 * all.team * grid <= 5 * all.alone * (grid / rts);
   const int size = teams ? rts : 1;
   const long long T = teams ? all.team : all.alone;
-  long long before = 0;
-  for (int w = 0; w < warp; ++w) before += teams ? m->wsum[w].team : m->wsum[w].alone;
+  long long before = __shfl_sync(0xffffffffu, teams ? upto.team : upto.alone, max(warp - 1, 0));
+  if (warp == 0) before = 0;
   const long long held = teams ? mine.team : mine.alone;
   before += (teams ? inc.team : inc.alone) - held;
   const int runs = (int)(T < (long long)(grid / size) ? T : (long long)(grid / size)), run = cta / size;
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     // ----------------------------------------------------------------- rows
     constexpr int COLS = C::TILE / C::HALVES, OCOLS = D / C::HALVES;  // this thread's columns of S and of O
     const int r = tid & (TR_ROWS - 1), half = tid / TR_ROWS;
-    const int my_node = r / a.G, my_head = r - my_node * a.G;
+    const int my_node = r * a.g_mul >> 16, my_head = r - my_node * a.G;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t ld = 0, jj = 0, syncs = 0, pairs = 0;
     bool ok = true;
@@ -630,33 +641,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       const bool fix = un.t0 + un.n > un.n_old && *reinterpret_cast<volatile int *>(&m->nonfinite) != 0;
       const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
       const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      if ((warp & 3) * 32 < un.rows) {
-        uint16_t *out = a.o + ((size_t)(un.lo + un.node0 + my_node) * a.Hq + un.g * a.G + my_head) * D;
+      if (fix) {  // into O, apart from the usual way out
 #pragma unroll 1
         for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
           uint32_t v[32];
-          __syncwarp();
           ptx::tmem_ld_x32(lanes + d, v);
           ptx::tmem_wait_ld();
-          if (!in) continue;
-          if (fix && real) {
-            for (int i = 0; i < un.nodes; ++i) {
-              const int t = un.n_old + i / C::TILE;
-              if (t < un.t0 || t >= un.t0 + un.n || !(sees[i / 64] >> (i % 64) & 1)) continue;
-              const uint16_t *src = a.v_new + (size_t)(un.lo + i) * a.c.row + un.g * D + d;
+          for (int i = 0; i < un.nodes; ++i) {
+            const int t = un.n_old + i / C::TILE;
+            if (!real || t < un.t0 || t >= un.t0 + un.n || !(sees[i / 64] >> (i % 64) & 1)) continue;
+            const uint16_t *src = a.v_new + (size_t)(un.lo + i) * a.c.row + un.g * D + d;
 #pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                const uint32_t h = src[q];
-                if ((h & EXP_MASK<FP16>) == EXP_MASK<FP16>)
-                  v[q] = __float_as_uint(__uint_as_float(v[q]) + value<FP16>(h));
-              }
+            for (int q = 0; q < 32; ++q) {
+              const uint32_t h = src[q];
+              if ((h & EXP_MASK<FP16>) == EXP_MASK<FP16>)
+                v[q] = __float_as_uint(__uint_as_float(v[q]) + value<FP16>(h));
             }
           }
+          __syncwarp();
+          ptx::tmem_st_x32(lanes + d, v);
+        }
+        ptx::tmem_wait_st();
+      }
+      if ((warp & 3) * 32 < un.rows) {
+        uint16_t *out = a.o + ((size_t)(un.lo + un.node0 + my_node) * a.Hq + un.g * a.G + my_head) * D;
+        auto put = [&](int d, uint32_t (&v)[32]) {  // columns d .. d + 31 of this row
           if (whole) {
-            if (sum == 0.f) {  // a row that sees nothing
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
-            }
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint4 x;
@@ -664,6 +674,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               x.y = pack2<FP16>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
               x.z = pack2<FP16>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
               x.w = pack2<FP16>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+              if (sum == 0.f) x = make_uint4(0u, 0u, 0u, 0u);  // a row that sees nothing
               *reinterpret_cast<uint4 *>(out + d + i) = x;
             }
           } else {
@@ -671,6 +682,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        };
+#pragma unroll 1
+        for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 64) {
+          uint32_t v0[32], v1[32];
+          __syncwarp();
+          ptx::tmem_ld_x32(lanes + d, v0);
+          ptx::tmem_ld_x32(lanes + d + 32, v1);
+          ptx::tmem_wait_ld();
+          if (in) {
+            put(d, v0);
+            put(d + 32, v1);
           }
         }
         if (in && !whole && half == 0)
@@ -720,6 +743,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           if (tid == 0) m->nonfinite = 0;
           if (!(ok = rows_sync())) break;
           for (int i = real ? un.node0 + my_node : -1; i >= 0; i = m->parent[i]) {
+            if (m->parent[i] == -2) {  // padding has no children
+              set_status(status, MOE_ERR_DEVICE_BOUNDS);
+              break;
+            }
 #pragma unroll
             for (int q = 0; q < TR_MAXN / 64; ++q)
               if (i / 64 == q) sees[q] |= 1ull << (i % 64);
@@ -1103,6 +1130,8 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.G = G;
   a.nt = moe::unit_nodes(G, max_nodes);
   a.rows_cap = a.nt * G;
+  a.nt_mul = 65536 / a.nt + 1;
+  a.g_mul = 65536 / G + 1;
   a.page_box = c->page_size < 64 ? c->page_size : 64;
   a.scale_log2 = scale * 1.4426950408889634f;
   size_t ml_at, part_at;

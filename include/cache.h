@@ -32,7 +32,7 @@ enum { MOE_BF16 = 0, MOE_FP16 = 1 };  /* attn_cache.dtype */
 /* Host struct of device pointers; the caller owns every buffer.
  * Supported: page_size 16, 32, 64, 128 or 256, head_dim 64, 128 or 256,
  * 1 <= n_kv_heads <= 256, n_pages * page_size < 2^31, max_pages * page_size
- * < 2^31.  To start: refs_d, lens_d and status_d zero, table_d -1. */
+ * <= 2^30.  To start: refs_d, lens_d and status_d zero, table_d -1. */
 typedef struct attn_cache {
   void *k_d, *v_d;     /* [n_layers][n_pages][page_size][n_kv_heads][head_dim], bf16 or fp16 */
   int32_t *refs_d;     /* [n_pages]              holders of a page, 0 = free         */

@@ -9,7 +9,7 @@
  *
  * A tree is a range of nodes, offsets[b] .. offsets[b+1]-1 for sequence b, in
  * an order in which parents come first: parent[i] < i counted within the
- * tree, -1 for a root, -2 for a node that is padding.  One node per sequence
+ * tree, -1 for a root, -2 for a node that is padding (and has no children).  One node per sequence
  * is ordinary decoding, a chain the usual list of drafted tokens.
  */
 #ifndef TREE_H

@@ -95,6 +95,19 @@ def test_many_trees(B, most, seed, drafted):
     same(verify(p, q, tokens, [x for t in parents for x in t], off, ua, us, most), p, q, tokens, parents, off, ua, us)
 
 
+@pytest.mark.parametrize("B", [1, 20, 25, 34, 43, 60, 100, 152, 153, 400])
+def test_clusters_of_all_sizes(B):
+    # from 16 CTAs a tree down to one
+    r = np.random.default_rng(B)
+    V, n = 17000, 3
+    p, q = probs(r, n * B, V, 1.0), probs(r, n * B, V, 1.0)
+    tokens, parents = r.integers(0, V, n * B), [[-1, 0, 0]] * B
+    off = [n * b for b in range(B + 1)]
+    ua, us = (r.random(n * B, dtype=np.float32) + np.float32(0.5)) % np.float32(1), r.random(B, dtype=np.float32)
+    for d in (q, None):
+        same(verify(p, d, tokens, [-1, 0, 0] * B, off, ua, us, n), p, d, tokens, parents, off, ua, us)
+
+
 def test_long_chains_that_are_taken_whole():
     r = np.random.default_rng(5)
     n, V = 1024, 50

@@ -298,7 +298,8 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(c.o, w)
 
 
-@pytest.mark.parametrize("what", ["slot", "slot_low", "offset", "order", "max_nodes", "parent", "parent_self", "len", "page"])
+@pytest.mark.parametrize("what", ["slot", "slot_low", "offset", "order", "max_nodes", "parent", "parent_self", "padded_parent",
+                                  "len", "page"])
 def test_device_checks(what):
     c = Case(20, [100, 70], [[-1, 0, 1], [-1, 0]])
     c.slots_t = i32([0, 1])
@@ -316,6 +317,8 @@ def test_device_checks(what):
         c.par[1] = 2
     elif what == "parent_self":
         c.par[1] = -3
+    elif what == "padded_parent":
+        c.par[1] = -2  # and node 2 is its child
     elif what == "len":
         c.slot_lens[0] = 129
     elif what == "page":

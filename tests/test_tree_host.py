@@ -37,6 +37,7 @@ BAD_CACHES = [(dict(k_d=None), moe.MOE_ERR_INVALID_ARGUMENT), (dict(status_d=Non
               (dict(page_size=512), moe.MOE_ERR_UNSUPPORTED), (dict(head_dim=96), moe.MOE_ERR_UNSUPPORTED),
               (dict(dtype=2), moe.MOE_ERR_UNSUPPORTED), (dict(n_kv_heads=257), moe.MOE_ERR_UNSUPPORTED),
               (dict(n_pages=1 << 25), moe.MOE_ERR_UNSUPPORTED), (dict(max_pages=1 << 25), moe.MOE_ERR_UNSUPPORTED),
+              (dict(max_pages=(1 << 24) + 1), moe.MOE_ERR_UNSUPPORTED),
               (dict(v_d=A + 8), moe.MOE_ERR_MISALIGNED), (dict(table_d=A + 4), moe.MOE_ERR_MISALIGNED)]
 
 
