@@ -364,8 +364,9 @@ def _given(name, t, dtype, device, shape):
 def _here(name, device):
     """Refuse a call whose tensors are not on the current device (kernels launch there)."""
     import torch
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{name}: on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    current = torch._C._cuda_getDevice() if device >= 0 else None  # CUDA is up: a tensor lives there
+    if device != current:
+        raise ValueError(f"{name}: on {'the host' if device < 0 else f'cuda:{device}'}, not on the current device")
 
 
 def _raw_stream(stream, device):
