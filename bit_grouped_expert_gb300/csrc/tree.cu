@@ -13,10 +13,22 @@
 //
 // Roles: the first four warps own the rows (at D = 256 eight, two threads a
 // row), the next loads (TMA: pages by the table's numbers, K one tile ahead of
-// V, into a ring), the next issues the MMAs (S of the next tile before O of
-// this one; at D = 256 the last issues those of O).  Rescaling O on a new maximum
+// V, into a ring), the next issues the MMAs (S of the next tile during the
+// softmax of this one; at D = 256 the last issues those of O).  Rescaling O on a new maximum
 // is put off while the maximum grows by less than 2^8: P then stays within
 // 2^8 and the fp32 sums lose nothing.
+// Who waits on a barrier's parity must know that the phase before has passed:
+// the comments at the waits say from what.  (The whole protocol was run on
+// the CPU as a model, thousands of times with random delays, for overflows, stale
+// slots and deadlocks.)
+//
+// Bound: for few rows by HBM (24 sequences of 1,100 to 9,000 positions, 5 nodes
+// each, 260 MB: 58 us, 4.5 TB/s with the start, the results' way out and the join;
+// 5.9 TB/s in between).  For 128 rows by shared memory: a 128-wide tile of D = 256
+// moves Q 64, K 64 (both for the scores) and V 64 KB out of it and K and V in,
+// 2,560 cycles at 128 bytes each of the 3,050 a tile takes; its MMAs are 2,048
+// (61 nodes over 131,000 positions: 106 us, 1,240 TFLOP/s).
+//
 // Every wait is bounded: after one second the kernel records
 // MOE_ERR_DEVICE_TIMEOUT, drains its copies and MMAs, frees tensor memory
 // and exits.
@@ -65,9 +77,12 @@ struct Cfg {
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
   static constexpr int SMEM = OFF_MISC + 3 * 1024;
   static_assert(SMEM * CTAS <= 227 * 1024, "shared memory");
-  // tensor memory columns: O, then two S tiles, each turned into P in place
-  static constexpr uint32_t S_COL = D, TMEM = BIG ? 512 : 256;
-  static_assert(S_COL + 2 * TILE <= TMEM, "tensor memory");
+  // Tensor memory columns: O, one S tile, two P tiles.  The rows take a whole S
+  // tile into registers first thing, so that the next one's MMAs run during
+  // the softmax.  (Two S tiles turned into P in place, whose MMAs had to wait for
+  // the output's, took as long within 2 %: shared memory is the bound.)
+  static constexpr uint32_t S_COL = D, P_COL = D + TILE, TMEM = BIG ? 512 : 256;
+  static_assert(P_COL + TILE <= TMEM, "tensor memory");
 };
 
 struct TreeMaps {
@@ -109,7 +124,7 @@ struct Count {
 
 struct Misc {
   uint64_t full[10], empty[10];
-  uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done[2], o_free, rows_bar, pair_bar[4], final_bar;
+  uint64_t q_full, q_free, s_full, s_free, p_ready[2], pv_done[2], o_free, rows_bar, pair_bar[4], final_bar;
   uint32_t tmem;
   int abort_flag, nonfinite;
   int b0;
@@ -339,10 +354,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     ptx::fence_mbar_init();
   } else if (tid == 96) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&m->s_full[i], 1);
       ptx::mbar_init(&m->p_ready[i], C::ROW_WARPS);
       ptx::mbar_init(&m->pv_done[i], 1);
     }
+    ptx::mbar_init(&m->s_full, 1);
+    ptx::mbar_init(&m->s_free, C::ROW_WARPS);
     ptx::mbar_init(&m->o_free, C::ROW_WARPS);
     ptx::mbar_init(&m->rows_bar, C::ROW_WARPS);
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&m->pair_bar[i], C::HALVES);
@@ -520,10 +536,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     const uint64_t qd = ptx::sdesc_sw128(ptx::smem_u32(smem));
     uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
-    auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
-      // the P tile in its place has been used up
-      if (t >= 2 && !tr_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-      const uint32_t s_col = tmem + C::S_COL + (t & 1) * C::TILE;
+    auto scores = [&](uint32_t pos, uint32_t t, bool first) {  // S of running tile t from the K tile at load `pos`
+      if (t >= 1 && !tr_wait_warp(&m->s_free, (t - 1) & 1u, m, status)) return false;
+      // (a unit's first slots may follow the last unit's V of tile t - 2)
+      if (first && t >= 2 && !tr_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+      const uint32_t s_col = tmem + C::S_COL;
 #pragma unroll
       for (int part = 0; part < C::PARTS; ++part, ++pos) {
         const uint32_t slot = pos % C::NS;
@@ -540,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               ptx::mma_ss(s_col, qd + (ch * C::Q_CHUNK + i * 32) / 16, b, id_s, (ch | i) != 0);
             }
           ptx::mma_commit(&m->empty[slot]);
-          if (part == C::PARTS - 1) ptx::mma_commit(&m->s_full[t & 1]);
+          if (part == C::PARTS - 1) ptx::mma_commit(&m->s_full);
         }
         __syncwarp();
       }
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       if (!tr_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
           (first && units > 0 && !tr_wait_warp(&m->o_free, (units - 1) & 1u, m, status)))
         return false;
-      const uint32_t p_col = tmem + C::S_COL + (t & 1) * C::TILE;
+      const uint32_t p_col = tmem + C::P_COL + (t & 1) * (C::TILE / 2);
 #pragma unroll
       for (int part = 0; part < C::PARTS; ++part, ++pos) {
         const uint32_t slot = pos % C::NS;
@@ -570,11 +587,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     };
     while (ok && w.next()) {
       if (does_s) {
-        ok = tr_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_pos<C>(0), jj);
+        ok = tr_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_pos<C>(0), jj, true);
       }
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
         if (does_s) {
-          if (j + 1 < w.n) ok = scores(ld + k_pos<C>(j + 1), jj + 1);
+          if (j + 1 < w.n) ok = scores(ld + k_pos<C>(j + 1), jj + 1, false);
           // the unit's last scores are under way
           if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
           __syncwarp();
@@ -753,13 +770,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           }
           __syncwarp();
         }
-        if (!(ok = tr_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, m, status))) break;
+        if (!(ok = tr_wait_warp(&m->s_full, jj & 1u, m, status))) break;
+        // Every row warp, with rows or without, is at most two tiles ahead of O: the P
+        // tile of jj is free then, and no wait below or in the other roles can take
+        // a phase of its barrier for the one two before.
+        if (jj >= 2 && !(ok = tr_wait_warp(&m->pv_done[jj & 1], ((jj - 2) >> 1) & 1u, m, status))) break;
         ptx::tc_fence_after();
         if (edge) {
           // V rows that nobody may see become zeros (0 x NaN is NaN), and in the
           // tree's own tiles non-finite values as well: finish() adds them to
           // the rows that see them
           const uint32_t pos = ld + v_pos<C>(j, un.n);
+          // the slots' last loads have been used up (else their barriers could still be a phase behind)
+          if (jj >= 1) ok = tr_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
           for (int part = 0; ok && part < C::PARTS; ++part)
             ok = tr_wait_warp(&m->full[(pos + part) % C::NS], ((pos + part) / C::NS) & 1u, m, status);
           if (!ok) break;
@@ -792,8 +815,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           uint32_t x[COLS / 32][32];
 #pragma unroll
           for (int h = 0; h < COLS / 32; ++h)
-            ptx::tmem_ld_x32(lanes + C::S_COL + (jj & 1) * C::TILE + half * COLS + 32 * h, x[h]);
+            ptx::tmem_ld_x32(lanes + C::S_COL + half * COLS + 32 * h, x[h]);
           ptx::tmem_wait_ld();
+          ptx::tc_fence_before();
+          arrive(&m->s_free);
           if (edge || !all_real) {
             unsigned long long see = 0;  // of this thread's columns
             if (real) {
@@ -821,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
 #pragma unroll
             for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(x[h][i]));
           float tmax = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * a.scale_log2;
-          if constexpr (C::HALVES == 2) {  // also: both have read S before either writes P over it
+          if constexpr (C::HALVES == 2) {
             tmax = fmaxf(tmax, exchange(tmax, ok));
             if (!ok) break;
           }
@@ -856,12 +881,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
             p[i / 2] = pack2<FP16>(p0, p1);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          const uint32_t p_col = lanes + C::S_COL + (jj & 1) * C::TILE + half * (COLS / 2);
+          const uint32_t p_col = lanes + C::P_COL + (jj & 1) * (C::TILE / 2) + half * (COLS / 2);
           if constexpr (COLS == 32)
             ptx::tmem_st_x16(p_col, p);
           else
             ptx::tmem_st_x32(p_col, p);
           ptx::tmem_wait_st();
+        } else {
+          arrive(&m->s_free);
         }
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
