@@ -19,7 +19,7 @@
 // 2^8 and the fp32 sums lose nothing.
 // Who waits on a barrier's parity must know that the phase before has passed:
 // the comments at the waits say from what.  (The whole protocol was run on
-// the CPU as a model, thousands of times with random delays, for overflows, stale
+// the CPU as a model, tests/test_tree_protocol.py, for overflows, stale
 // slots and deadlocks.)
 //
 // Bound: for few rows by HBM (24 sequences of 1,100 to 9,000 positions, 5 nodes
@@ -1093,7 +1093,7 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
-  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(4 * TR_MAX_SMS), dim3(TJ_THREADS), 0, s, a, ctas);
+  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(ctas * 2 / C::CTAS), dim3(TJ_THREADS), 0, s, a, ctas);
 }
 
 template <bool FP16>
