@@ -45,6 +45,13 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t code) {
   atomicCAS(status, 0, code);
 }
 
+// The start of a kernel launched as a programmatic dependent: the next kernel
+// may be made ready from here on, and the one before has ended, its writes seen.
+__device__ __forceinline__ void start_dependent() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- numbers
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) {

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (ptx::smem_u32(smem) & 1023u) {  // not placed as declared: no kernel then, rather than wrong tiles
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
       set_status(a.c.status, MOE_ERR_UNSUPPORTED);
       a.desc[blockIdx.x].parts = 0;
@@ -328,6 +329,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
+  // what the kernel before writes (lengths, tables, rows, queries) from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // This CTA's run: every thread adds up some sequences' units, a scan gives
   // their places, and the thread whose sequences hold the run's start writes
   // down where that is.
@@ -1088,9 +1091,9 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   // per device and cheap: set on every call rather than remembered
   cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  const bool chain = prof_chain(MOE_KERNEL_ATTN_TREE), quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
   prof_before(MOE_KERNEL_ATTN_TREE, s);
-  const bool quiet = prof_quiet(MOE_KERNEL_ATTN_TREE);
-  e = launch_dep(false, tree_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
+  e = launch_dep(chain, tree_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
   return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(ctas * 2 / C::CTAS), dim3(TJ_THREADS), 0, s, a, ctas);
