@@ -369,6 +369,13 @@ def _here(name, device):
         raise ValueError(f"{name}: on {'the host' if device < 0 else f'cuda:{device}'}, not on the current device")
 
 
+def _scratch(ws, device):
+    """Address and bytes of a workspace tensor on the call's device."""
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on cuda:{device} wanted, got one on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
 def _raw_stream(stream, device):
     """As _stream, without making a Stream object for the current one."""
     if stream is None:
@@ -421,7 +428,7 @@ def attn_cache_append(cache: AttnCache, k_new, v_new, offsets, B: int, ws, slots
     [n_layers, n_rows, Hkv, D], offsets int32 [B + 1], slots int32 [B] or None
     (0 .. B-1), path int32 [B, stride] and n_keep int32 [B] as moe_draft_verify
     leaves them, or None (every row, in order)."""
-    dev, i32, n_rows = cache.device, cache.i32, k_new.shape[1]
+    dev, i32, n_rows, B = cache.device, cache.i32, k_new.shape[1], int(B)
     _here("cache", dev)
     shape, stride = (cache.layers, n_rows, cache.heads, cache.dim), 0 if path is None else path.shape[-1]
     _check("attn_cache_append", lib().attn_cache_append(
@@ -429,8 +436,8 @@ def attn_cache_append(cache: AttnCache, k_new, v_new, offsets, B: int, ws, slots
         None if slots is None else _given("slots", slots, i32, dev, (B,)),
         _given("offsets", offsets, i32, dev, (B + 1,)),
         None if n_keep is None else _given("n_keep", n_keep, i32, dev, (B,)),
-        None if path is None else _given("path", path, i32, dev, (B, stride)), stride, B, n_rows, _ptr(ws),
-        _nbytes(ws), _raw_stream(stream, dev)))
+        None if path is None else _given("path", path, i32, dev, (B, stride)), stride, B, n_rows, *_scratch(ws, dev),
+        _raw_stream(stream, dev)))
 
 
 def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
@@ -440,16 +447,16 @@ def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
 def attn_cache_fork(cache: AttnCache, src, dst, n: int, ws, stream=None):
     """Slot dst[i] (empty) becomes a copy of slot src[i]: full pages shared, the
     partly filled last page copied.  src, dst int32 [n]."""
-    dev = cache.device
+    dev, n = cache.device, int(n)
     _here("cache", dev)
     _check("attn_cache_fork", lib().attn_cache_fork(
-        cache.ref, _given("src", src, cache.i32, dev, (n,)), _given("dst", dst, cache.i32, dev, (n,)), n, _ptr(ws),
-        _nbytes(ws), _raw_stream(stream, dev)))
+        cache.ref, _given("src", src, cache.i32, dev, (n,)), _given("dst", dst, cache.i32, dev, (n,)), n,
+        *_scratch(ws, dev), _raw_stream(stream, dev)))
 
 
 def attn_cache_trim(cache: AttnCache, slots, new_lens, n: int, stream=None):
     """Cut n sequences to new_lens (0 frees one); slots int32 [n], or None for 0 .. n-1."""
-    dev = cache.device
+    dev, n = cache.device, int(n)
     _here("cache", dev)
     _check("attn_cache_trim", lib().attn_cache_trim(
         cache.ref, None if slots is None else _given("slots", slots, cache.i32, dev, (n,)),
@@ -469,12 +476,13 @@ def attn_tree(cache: AttnCache, layer: int, q, k_new, v_new, offsets, parent, B:
     dev, dt, i32 = cache.device, cache.dtype, cache.i32
     _here("cache", dev)
     n, Hq, _ = q.shape
+    layer, B, max_nodes = int(layer), int(B), int(max_nodes)
     rows, heads = (n, cache.heads, cache.dim), (n, Hq, cache.dim)
     _check("attn_tree", lib().attn_tree(
         cache.ref, layer, _given("q", q, dt, dev, heads), _given("k_new", k_new, dt, dev, rows),
         _given("v_new", v_new, dt, dev, rows), None if slots is None else _given("slots", slots, i32, dev, (B,)),
         _given("offsets", offsets, i32, dev, (B + 1,)), _given("parent", parent, i32, dev, (n,)), B, n, max_nodes, Hq,
-        scale, _ptr(ws), _nbytes(ws), _given("o", o, dt, dev, heads), _raw_stream(stream, dev)))
+        scale, *_scratch(ws, dev), _given("o", o, dt, dev, heads), _raw_stream(stream, dev)))
 
 
 def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, path, n_path, next_token, status,
@@ -487,7 +495,7 @@ def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, 
     f32, i32, dev = torch.float32, torch.int32, p.get_device()
     _here("p", dev)
     n, V = p.shape
-    stride = path.shape[-1]
+    B, stride = int(B), path.shape[-1]
     _check("moe_draft_verify", lib().moe_draft_verify(
         _given("p", p, f32, dev, (n, V)), None if q is None else _given("q", q, f32, dev, (n, V)),
         _given("tokens", tokens, i32, dev, (n,)), _given("parent", parent, i32, dev, (n,)),

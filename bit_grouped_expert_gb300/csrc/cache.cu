@@ -469,6 +469,11 @@ extern "C" moe_status attn_cache_append(const attn_cache *c, const void *k_new_d
   if (!aligned16(k_new_d) || !aligned16(v_new_d) || !aligned16(slots_d) || !aligned16(offsets_d) ||
       !aligned16(n_keep_d) || !aligned16(path_d) || !aligned16(ws_d))
     return MOE_ERR_MISALIGNED;
+  const size_t nn = (size_t)c->n_layers * n_rows * a.c.row * 2;
+  const size_t np = (size_t)c->n_layers * c->n_pages * c->page_size * a.c.row * 2;
+  if (moe::ranges_meet(k_new_d, nn, c->k_d, np) || moe::ranges_meet(k_new_d, nn, c->v_d, np) ||
+      moe::ranges_meet(v_new_d, nn, c->k_d, np) || moe::ranges_meet(v_new_d, nn, c->v_d, np))
+    return MOE_ERR_INVALID_ARGUMENT;
   size_t pages_at;
   if (ws_bytes < moe::append_ws(c, B, n_rows, &pages_at)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.k_new = static_cast<const uint16_t *>(k_new_d);

@@ -161,6 +161,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Host-side helpers shared by the .cu files.
 namespace moe {
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// [p, p + np) and [q, q + nq) share a byte.
+inline bool ranges_meet(const void *p, size_t np, const void *q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return np && nq && a < b + nq && b < a + np;
+}
 template <typename T>
 inline T *ws_ptr(void *ws, size_t off) {
   return reinterpret_cast<T *>(static_cast<char *>(ws) + off);

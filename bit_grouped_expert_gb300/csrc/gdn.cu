@@ -193,11 +193,6 @@ __global__ void __launch_bounds__(GDN_THREADS) gdn_scan_kernel(const __grid_cons
   for (int i = 0; i < GDN_ROWS; ++i) st[(size_t)i * a.dv] = S[i];
 }
 
-bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return np && nq && a < b + nq && b < a + np;
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -214,9 +209,9 @@ extern "C" moe_status gdn_scan(const void *q_d, const void *k_d, const void *v_d
     return MOE_ERR_MISALIGNED;
   const size_t nqk = (size_t)T * Hk * dk * 2, nv = (size_t)T * Hv * dv * 2, nab = (size_t)T * Hv * 4,
                ns = (size_t)Hv * dk * dv * 4, no = nv;
-  if (moe::overlaps(o_d, no, q_d, nqk) || moe::overlaps(o_d, no, k_d, nqk) || moe::overlaps(o_d, no, v_d, nv) ||
-      moe::overlaps(o_d, no, alpha_d, nab) || moe::overlaps(o_d, no, beta_d, nab) ||
-      moe::overlaps(o_d, no, state_d, ns))
+  if (moe::ranges_meet(o_d, no, q_d, nqk) || moe::ranges_meet(o_d, no, k_d, nqk) || moe::ranges_meet(o_d, no, v_d, nv) ||
+      moe::ranges_meet(o_d, no, alpha_d, nab) || moe::ranges_meet(o_d, no, beta_d, nab) ||
+      moe::ranges_meet(o_d, no, state_d, ns))
     return MOE_ERR_INVALID_ARGUMENT;
   moe::GdnArgs a;
   a.q = static_cast<const uint16_t *>(q_d);

@@ -1140,6 +1140,12 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   if (!aligned16(q_d) || !aligned16(k_new_d) || !aligned16(v_new_d) || !aligned16(slots_d) ||
       !aligned16(offsets_d) || !aligned16(parent_d) || !aligned16(ws_d) || !aligned16(o_d))
     return MOE_ERR_MISALIGNED;
+  const size_t no = (size_t)n_nodes * Hq * D * 2, nn = (size_t)n_nodes * a.c.row * 2;
+  const size_t np = (size_t)c->n_layers * c->n_pages * c->page_size * a.c.row * 2;
+  if (moe::ranges_meet(o_d, no, q_d, no) || moe::ranges_meet(o_d, no, k_new_d, nn) ||
+      moe::ranges_meet(o_d, no, v_new_d, nn) || moe::ranges_meet(o_d, no, c->k_d, np) ||
+      moe::ranges_meet(o_d, no, c->v_d, np))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (ws_bytes < attn_tree_workspace_bytes(c, B, n_nodes, max_nodes, Hq)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -61,7 +61,8 @@ typedef struct attn_cache {
  * Device checks: slots in range and distinct, offsets ascending within
  * n_rows, kept rows within the sequence's rows, room in its table.
  * Errors: MOE_ERR_INVALID_ARGUMENT (null pointers, negative sizes, path_d
- * without n_keep_d, path_stride < 1 with path_d), MOE_ERR_UNSUPPORTED (the cache's
+ * without n_keep_d, path_stride < 1 with path_d, rows that lie in the pool),
+ * MOE_ERR_UNSUPPORTED (the cache's
  * dimensions, B > 1024), MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL,
  * MOE_ERR_CUDA. */
 size_t attn_cache_append_workspace_bytes(const attn_cache *c, int32_t B, int32_t n_rows);

@@ -42,7 +42,7 @@ extern "C" {
  * query heads per KV head, B <= 1024.  B == 0 or n_nodes == 0 returns MOE_OK
  * with nothing enqueued.  Device checks (slots, offsets, parents, lengths,
  * pages) set MOE_ERR_DEVICE_BOUNDS in the cache's status word; the output of
- * that tree is then not valid.  MOE_ERR_DEVICE_TIMEOUT there: a wait for a
+ * that tree is then not valid.  o_d overlaps no input.  MOE_ERR_DEVICE_TIMEOUT there: a wait for a
  * copy gave up.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED,
  * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */

@@ -112,6 +112,19 @@ def test_a_life_of_a_cache(page, heads, dim, dtype):
     assert int(t.refs.abs().sum()) == 0 and (t.table == -1).all()
 
 
+@pytest.mark.parametrize("pages", [37, 61, 2050])
+def test_pools_of_odd_sizes_are_used_to_the_last_page(pages):
+    t = Twin(pages=pages, slots=2, max_pages=pages, layers=1, heads=1)
+    t.append([16 * pages - 5])
+    t.trim([(0, 16 * pages - 40)])
+    t.append([20], slots=[1])
+    t.check()
+    t.append([17], slots=[0], model=False)
+    t.check(moe.MOE_ERR_OUT_OF_PAGES)
+    t.append([3])
+    t.check()
+
+
 def test_random_calls():
     rng = np.random.default_rng(3)
     t = Twin(pages=300, slots=24, max_pages=20, layers=1, heads=1, page=16)
@@ -200,6 +213,21 @@ def test_trim_device_checks_are_per_sequence():
     t.trim([(2, 10), (2, 0)], model=False)  # named twice: the first counts
     t.model.trim(2, 10)
     t.check(moe.MOE_ERR_DEVICE_BOUNDS)
+
+
+def test_binding_refusals():
+    t = Twin()
+    kn, vn = t.rows(3)
+    ws = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    for bad in (dict(k=kn.float()), dict(k=kn[:1]), dict(off=i32([0, 3]).long()), dict(ws=ws.cpu()), dict(off=i32([0, 1, 3]))):
+        a = {**dict(k=kn, off=i32([0, 3]), ws=ws), **bad}
+        with pytest.raises(ValueError):
+            moe.attn_cache_append(t.cache, a["k"], vn, a["off"], 1, a["ws"])
+    with pytest.raises(ValueError):
+        moe.attn_cache_trim(t.cache, i32([0]), i32([0, 1]), 1)
+    with pytest.raises(ValueError):
+        moe.make_attn_cache(t.k, t.v, t.refs[:-1], t.table, t.lens, t.status)
+    t.check()
 
 
 def test_calls_with_nothing_to_do():

@@ -175,6 +175,33 @@ def test_padding_empty_trees_and_empty_sequences():
     assert (o[2] == 0).all() and (o[4:7] == 0).all()  # padding rows are zeros
 
 
+def test_a_row_tile_of_padding_only():
+    # 16 nodes a row tile: the second one is padding
+    c = Case(22, [150], [tree_of(np.random.default_rng(4), 16) + [-2] * 16 + [15] * 8])
+    o = c.run()
+    c.check(o)
+    assert (o[16:32] == 0).all()
+
+
+def test_no_nodes_at_all():
+    c = Case(23, [150, 0], [[], []])
+    c.check(c.run())
+
+
+def test_many_kv_heads():
+    c = Case(24, [70, 5], [[-1, 0], [-1]], Hq=128, Hkv=64, D=64, page=32)
+    c.check(c.run())
+
+
+def test_trees_of_uneven_sizes_and_long_caches():
+    # teams of row tiles that some trees leave empty, and the same work cut alone
+    rng = np.random.default_rng(5)
+    c = Case(25, [4000, 3500, 3000, 3900], [tree_of(rng, n) for n in (60, 50, 64, 33)], page=128)
+    c.check(c.run())
+    c = Case(26, [4000, 3500, 3000, 3900], [tree_of(rng, n) for n in (64, 1, 2, 1)], page=128)
+    c.check(c.run())
+
+
 def test_several_roots_see_only_their_own_tree():
     c = Case(5, [20], [[-1, -1, 0, 1, -1, 4]], D=128, Hq=8)
     c.check(c.run())
@@ -338,5 +365,9 @@ def test_binding_refusals():
                       c.ws, c.o)
     with pytest.raises(ValueError, match="offsets"):
         moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets.cpu(), c.par, 1, 2, c.ws, c.o)
+    with pytest.raises(ValueError, match="ws"):
+        moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets, c.par, 1, 2, c.ws.cpu(), c.o)
+    with pytest.raises(moe.MoeError, match="workspace too small"):
+        moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets, c.par, 1, 2, c.ws[:64], c.o)
     with pytest.raises(ValueError, match="parent"):
         moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets, c.par[:2], 1, 2, c.ws, c.o)

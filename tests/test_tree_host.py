@@ -73,6 +73,9 @@ def test_append_host_checks(lib):
     assert _append(lib, B=1025, ws=1 << 30) == moe.MOE_ERR_UNSUPPORTED
     assert _append(lib, v=A + 2) == moe.MOE_ERR_MISALIGNED
     assert _append(lib, path=A + 4) == moe.MOE_ERR_MISALIGNED
+    pool = 2 * 100 * 64 * 512 * 2  # bytes of K
+    assert _append(lib, k=A + pool - 16) == moe.MOE_ERR_INVALID_ARGUMENT  # rows inside the pool
+    assert _append(lib, v=2 * A) == moe.MOE_ERR_INVALID_ARGUMENT
     need = lib.attn_cache_append_workspace_bytes(_ref(_cache()), 3, 30)
     assert need > 0 and _append(lib, ws=need - 1) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
 
@@ -123,7 +126,10 @@ def test_tree_host_checks(lib):
     assert call(Hq=258, nb=1 << 30) == moe.MOE_ERR_UNSUPPORTED  # 129 query heads per KV head
     assert call(mx=257, nb=1 << 30) == moe.MOE_ERR_UNSUPPORTED
     assert call(B=1025, nb=1 << 30) == moe.MOE_ERR_UNSUPPORTED
-    assert call(q=A + 2) == moe.MOE_ERR_MISALIGNED
+    assert call(q=7 * A + 2) == moe.MOE_ERR_MISALIGNED
+    for x in (7, 8, 9):  # the output over an input, or inside the pool
+        assert call(o=x * A + 16) == moe.MOE_ERR_INVALID_ARGUMENT
+    assert call(o=A + 4096) == moe.MOE_ERR_INVALID_ARGUMENT
     assert call(slots=A + 4) == moe.MOE_ERR_MISALIGNED
     need = lib.attn_tree_workspace_bytes(_ref(_cache()), 2, 10, 8, 16)
     assert need > 0 and call(nb=need - 1) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
