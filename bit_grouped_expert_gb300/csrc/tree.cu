@@ -980,8 +980,11 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_cons
     const bool in = e < cells && r < ds.rows;
     float M = -INFINITY, den = 0.f;
     float4 acc[4] = {};
+    // A part in which the row saw nothing has the sum 0.  Its maximum does not
+    // tell: that is -infinity as well where every score is NaN (a maximum passes
+    // over NaN), and such a part, whose sum is NaN, makes the row NaN.
     auto add = [&](float2 ml, const float4 (&v)[4]) {
-      if (ml.x == -INFINITY) return;  // the row saw nothing there
+      if (ml.y == 0.f) return;
       const float mn = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : ex2(M - mn), h = ex2(ml.x - mn);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

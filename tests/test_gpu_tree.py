@@ -371,3 +371,48 @@ def test_binding_refusals():
         moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets, c.par, 1, 2, c.ws[:64], c.o)
     with pytest.raises(ValueError, match="parent"):
         moe.attn_tree(c.cache, 0, c.q, c.kn, c.vn, c.offsets, c.par[:2], 1, 2, c.ws, c.o)
+
+
+SPLITS = [([0], "whole"), ([64], "two CTAs"), ([3000], "many CTAs"), ([100] * 200, "more units than CTAs"),
+          ([20000, 5, 700], "uneven")]
+
+
+@pytest.mark.parametrize("lens", [s[0] for s in SPLITS], ids=[s[1] for s in SPLITS])
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "fp16"), (256, "bf16")])
+def test_a_query_that_is_not_a_number_gives_none_however_the_work_is_cut(lens, D, dtype):
+    c = Case(27, lens, [[-1, 0]] * len(lens), Hq=8, D=D, dtype=dtype)
+    good = c.run().clone()
+    rows = [(0, 3), (1, 6)]  # (node, head)
+    for i, h in rows:
+        c.q[i, h, D // 2] = float("nan")
+    o = c.run()
+    hit = torch.zeros(o.shape[:2], dtype=torch.bool, device=DEV)
+    for i, h in rows:
+        hit[i, h] = True
+    assert torch.isnan(o[hit].float()).all()
+    assert torch.equal(o[~hit], good[~hit])
+
+
+@pytest.mark.parametrize("L,lo,hi", [(64, 0, 64), (300, 128, 256), (3000, 1024, 1280), (3000, 0, 3000), (3000, 1500, 1501),
+                                     (20000, 4096, 9000)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_cached_keys_that_are_not_numbers_show_however_the_work_is_cut(L, lo, hi, D):
+    # a whole CTA's part of them, several, all, or one position
+    c = Case(28, [L, 130], [[-1, 0], [-1]], Hq=8, Hkv=2, D=D)
+    good = c.run().clone()
+    pos = torch.arange(lo, hi, device=DEV)
+    c.k[0, c.table[0].long()[pos // 64], pos % 64, 1] = float("nan")
+    o = c.run()
+    assert torch.isnan(o[:2, 4:].float()).all()
+    assert torch.equal(o[:2, :4], good[:2, :4]) and torch.equal(o[2:], good[2:])
+
+
+@pytest.mark.parametrize("L", [64, 3000])
+def test_cached_values_that_are_not_numbers_show_in_their_columns(L):
+    c = Case(29, [L], [[-1, 0]], Hq=8, Hkv=2, D=128)
+    good = c.run().clone()
+    c.v[0, int(c.table[0, 0]), 7, 0, 5] = float("nan")
+    o = c.run()
+    assert torch.isnan(o[:2, :4, 5].float()).all()
+    o[:2, :4, 5] = good[:2, :4, 5]
+    assert torch.equal(o, good)
