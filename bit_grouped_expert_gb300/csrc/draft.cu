@@ -80,11 +80,12 @@ __device__ __forceinline__ Pair scan_lanes(Pair a) {
   return a;
 }
 
-// max(r - s q, 0)
+// max(r - s q, 0).  NaN stays NaN, so that the sum shows it; an infinite q
+// leaves 0 (the product's error is NaN then, and the difference with it).
 __device__ __forceinline__ Pair drop(Pair r, Pair s, float q) {
   const float ph = __fmul_rn(s.h, q), pl = __fmaf_rn(s.l, q, __fmaf_rn(s.h, q, -ph));
   const Pair d = add(r, Pair{-ph, -pl});
-  return d.h > 0.f ? d : Pair{0.f, 0.f};
+  return d.h <= 0.f || ph == INFINITY ? Pair{0.f, 0.f} : d;
 }
 
 enum { CMD_END = 0, CMD_PASS = 1, CMD_DRAW = 2 };
@@ -205,7 +206,7 @@ __device__ __forceinline__ void residual(const Shared &s, int rounds, int t, flo
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         r[i] = two_sum(p[i], -q[i]);
-        if (!(r[i].h > 0.f)) r[i] = Pair{0.f, 0.f};
+        if (r[i].h <= 0.f) r[i] = Pair{0.f, 0.f};  // (NaN stays)
       }
     }
     for (int k = 1; k < rounds; ++k) {
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
           c.node = lo + cur;
           c.rounds = rounds;
           summed = true;
-        } else if (total.h > 0.f && total.h < INFINITY) {
+        } else if (total.h > 0.f && total.h < INFINITY && S.h == S.h) {  // (S: NaN among the refused tokens' R too)
           // draw: the first CTA whose sum takes the running sum past the
           // threshold; where rounding leaves none, the last with any mass
           const Pair want = scaled(total, u_sample), mine = lane < ctas ? s.cta_sum[lane] : zero;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
           const Pair before = shfl(upto, max(c.target - 1, 0));
           c.threshold = !past ? none : c.target ? add(want, minus(before)) : want;
           if (lane == 0) a.n_path[b] = count;
-        } else if (rounds > 0) {  // no residual mass: draw from p itself
+        } else if (rounds > 0 && total.h <= 0.f && S.h == S.h) {  // no residual mass: draw from p itself
           rounds = 0;
           c.op = CMD_PASS;
           c.node = lo + cur;

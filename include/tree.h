@@ -72,7 +72,8 @@ moe_status attn_tree(const attn_cache *c, int32_t layer, const void *q_d, const 
  *   n_path_d     int32 [B] (written) nodes on the path, >= 1 (0 for a tree with no nodes)
  *   next_d       int32 [B] (written) the next token (-1 for a tree with no nodes)
  *   status_d     int32, set to MOE_ERR_DEVICE_BOUNDS (offsets, parents, a token outside
- *                [0, V)) or MOE_ERR_NONFINITE (no finite positive mass to draw from);
+ *                [0, V)) or MOE_ERR_NONFINITE (the mass to draw from is not finite and positive:
+ *                NaN or infinity left in R or, of a child not taken, in R[x]; or p[c] zero everywhere);
  *                that tree then has n_path 0 and next -1
  * Supported: 1 <= V <= 2^20, B <= 65535.  B == 0 returns MOE_OK with nothing enqueued.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED, MOE_ERR_CUDA. */

@@ -259,3 +259,64 @@ def test_a_speculative_decoding_run():
         np.testing.assert_array_equal(f(k), model.k)
         np.testing.assert_array_equal(f(v), model.v)
     assert taken > 0 and int(status[0]) == 0
+
+
+def refusals(B, V, kids):
+    """B trees of a root with `kids` children that are all refused (u = 0.999 and p below q at their tokens),
+    p and q everywhere positive and finite."""
+    r = np.random.default_rng(31)
+    n = kids + 1
+    p, q = probs(r, B * n, V, 1.0), probs(r, B * n, V, 1.0)
+    tokens = np.zeros(B * n, np.int64)
+    for b in range(B):
+        tokens[b * n + 1:(b + 1) * n] = np.argsort(p[b * n] / q[b * n])[:kids]
+    return p, q, tokens, [-1] + [0] * kids, [n * b for b in range(B + 1)], np.full(B * n, 0.999, np.float32)
+
+
+# the residual kept in shared memory (one CTA, and a cluster), and rebuilt in every pass (one CTA a tree, a long row)
+RESIDUALS = [(3, 500), (3, 20000), (160, 12000)]
+
+
+@pytest.mark.parametrize("B,V", RESIDUALS)
+@pytest.mark.parametrize("kids", [1, 2, 4])
+@pytest.mark.parametrize("where,value", [("p", float("nan")), ("p", float("inf")), ("q", float("nan"))])
+def test_no_draw_from_a_residual_that_is_not_a_number(B, V, kids, where, value):
+    p, q, tokens, tree, off, ua = refusals(B, V, kids)
+    us = np.full(B, 0.5, np.float32)
+    same(verify(p, q, tokens, tree * B, off, ua, us, kids + 1), p, q, tokens, [tree] * B, off, ua, us)
+    at = [t for t in range(V) if t not in tokens[off[1] + 1:off[2]]][3]
+    (p if where == "p" else q)[off[1], at] = value  # the second tree's root, at no child's token
+    path, n, nxt, status = verify(p, q, tokens, tree * B, off, ua, us, kids + 1)
+    assert status == moe.MOE_ERR_NONFINITE and n[1] == 0 and nxt[1] == -1 and (path[1] == -1).all()
+    for b in [x for x in range(B) if x != 1][:20]:
+        s = slice(off[b], off[b + 1])
+        assert nxt[b] == verify_drafts(p[s], q[s], tokens[s], tree, ua[s], us[b])[1] and n[b] == 1
+
+
+@pytest.mark.parametrize("B,V", RESIDUALS)
+def test_a_draft_of_nothing_but_nan_is_not_read_as_no_residual(B, V):
+    p, q, tokens, tree, off, ua = refusals(B, V, 2)
+    q[0] = np.nan
+    path, n, nxt, status = verify(p, q, tokens, tree * B, off, ua, np.full(B, 0.5, np.float32), 3)
+    assert status == moe.MOE_ERR_NONFINITE and n[0] == 0 and nxt[0] == -1 and n[1] == 1
+
+
+@pytest.mark.parametrize("B,V", RESIDUALS)
+@pytest.mark.parametrize("kids", [1, 2, 4])
+def test_an_infinite_draft_probability_leaves_its_token_nothing(B, V, kids):
+    # max(R - S inf, 0) = 0, in every round
+    p, q, tokens, tree, off, ua = refusals(B, V, kids)
+    us = np.full(B, 0.5, np.float32)
+    q[0, :V // 2:2] = np.inf
+    same(verify(p, q, tokens, tree * B, off, ua, us, kids + 1), p, q, tokens, [tree] * B, off, ua, us)
+
+
+@pytest.mark.parametrize("B,V", RESIDUALS)
+def test_a_child_of_probability_nan_is_reported_without_draft_probabilities_too(B, V):
+    p, _, tokens, tree, off, ua = refusals(B, V, 3)
+    p[0, tokens[2]] = np.nan
+    path, n, nxt, status = verify(p, None, tokens, tree * B, off, ua, np.full(B, 0.5, np.float32), 4)
+    assert status == moe.MOE_ERR_NONFINITE and n[0] == 0 and nxt[0] == -1 and (path[0] == -1).all()
+    s = slice(off[1], off[2])
+    want, token = verify_drafts(p[s], None, tokens[s], tree, ua[s], 0.5)
+    assert path[1, :n[1]].tolist() == want and nxt[1] == token
