@@ -30,6 +30,7 @@ namespace {
 constexpr int DV_THREADS = 512, DV_WARPS = DV_THREADS / 32;
 constexpr int DV_MAXN = 1024;     // nodes of a tree
 constexpr int DV_MAX_CTAS = 16;   // CTAs of a cluster
+constexpr int DV_MAX_CACHE = 80 * 1024;  // bytes of the residual kept by a CTA at most: two CTAs an SM
 
 struct VerifyArgs {
   const float *p, *q;
@@ -552,7 +553,7 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   // the residual's cache: a CTA's quads (a row begins up to three tokens into
   // its first), if two CTAs an SM have room for it
   int cache_quads = (V / 4 + 2 + ctas * moe::DV_WARPS - 1) / (ctas * moe::DV_WARPS) * moe::DV_WARPS;
-  if (!q_d || cache_quads * 32 > 80 * 1024) cache_quads = 0;
+  if (!q_d || cache_quads * 32 > moe::DV_MAX_CACHE) cache_quads = 0;
   cfg.dynamicSmemBytes = (size_t)cache_quads * 32;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -563,11 +564,14 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = moe::prof_chain(MOE_KERNEL_DRAFT_VERIFY) ? 2 : 1;
   auto kernel = q_d ? moe::verify_kernel<true> : moe::verify_kernel<false>;
-  // clusters above eight CTAs want leave; per device and cheap: asked on every call rather than remembered
+  // clusters above eight CTAs want leave, and so does much shared memory; per device
+  // and cheap: asked on every call rather than remembered.  Both are the kernel's, not
+  // the call's, so every call asks for the same: a thread with a smaller row
+  // must not take back what another's launch is about to need.
   cudaError_t e = cudaSuccess;
   if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && cache_quads)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, moe::DV_MAX_CACHE);
   if (e != cudaSuccess) return moe::note_cuda_error(e);
   moe::prof_before(MOE_KERNEL_DRAFT_VERIFY, s);
   e = cudaLaunchKernelEx(&cfg, kernel, a, ctas, cache_quads);

@@ -320,3 +320,39 @@ def test_a_child_of_probability_nan_is_reported_without_draft_probabilities_too(
     s = slice(off[1], off[2])
     want, token = verify_drafts(p[s], None, tokens[s], tree, ua[s], 0.5)
     assert path[1, :n[1]].tolist() == want and nxt[1] == token
+
+
+def test_host_threads_with_vocabularies_of_their_own():
+    """Each thread's calls want another amount of shared memory for the residual: none may be refused because of another's."""
+    import ctypes
+    import threading
+    r = np.random.default_rng(34)
+    jobs, failed = [], []
+    for V in (900, 130000, 9000, 70000):
+        n = 3
+        p, q = (torch.from_numpy(probs(r, n, V, 1.0)).to(DEV) for _ in range(2))
+        ins = p, q, i32([0, 1, 2]), i32([-1, 0, 0]), i32([0, n]), torch.full((n,), 0.999, device=DEV), \
+            torch.full((1,), 0.3, device=DEV)
+        outs = torch.zeros(1, n, dtype=torch.int32, device=DEV), i32([0]), i32([0]), i32([0, 0, 0, 0])
+        want = verify_drafts(p.cpu().numpy(), q.cpu().numpy(), [0, 1, 2], [-1, 0, 0], ins[5].tolist(), float(ins[6]))
+        jobs.append((V, ins, outs, torch.cuda.Stream(), want))
+    torch.cuda.synchronize()
+    call = moe.lib().moe_draft_verify
+
+    def loop(V, ins, outs, stream, want):
+        a = [ctypes.c_void_p(t.data_ptr()) for t in ins]
+        o = [ctypes.c_void_p(t.data_ptr()) for t in outs]
+        args = (*a, 1, 3, V, o[0], 3, *o[1:], ctypes.c_void_p(stream.cuda_stream))
+        codes = [call(*args) for _ in range(20000)]
+        failed.extend((V, c) for c in codes if c != moe.MOE_OK)
+
+    threads = [threading.Thread(target=loop, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, f"{len(failed)} of 80000 calls refused, the first {failed[0]}"
+    for V, ins, outs, stream, want in jobs:
+        path, cnt, nxt, st = (t.flatten().tolist() for t in outs)
+        assert st[0] == 0 and path[:cnt[0]] == want[0] and nxt[0] == want[1]
