@@ -344,9 +344,11 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
           summed = true;
         } else if (total.h > 0.f && total.h < INFINITY && S.h == S.h) {  // (S: NaN among the refused tokens' R too)
           // draw: the first CTA whose sum takes the running sum past the
-          // threshold; where rounding leaves none, the last with any mass
+          // threshold; where rounding leaves none, the last with any mass.  (A CTA
+          // without mass takes it nowhere, but the scan adds in another order for
+          // each lane, and a threshold may lie between two roundings of one sum.)
           const Pair want = scaled(total, u_sample), mine = lane < ctas ? s.cta_sum[lane] : zero;
-          const unsigned past = __ballot_sync(0xffffffffu, lane < ctas && above(upto, want));
+          const unsigned past = __ballot_sync(0xffffffffu, lane < ctas && mine.h > 0.f && above(upto, want));
           const unsigned some = __ballot_sync(0xffffffffu, mine.h > 0.f);
           c.op = CMD_DRAW;
           c.node = lo + cur;
@@ -448,10 +450,10 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
       continue;
     }
     if (rank == (uint32_t)c.target) {
-      // the warp run, then the token: the first past the threshold, or the
-      // last with any mass where rounding leaves none
+      // the warp run (one with mass, as above), then the token: the first past
+      // the threshold, or the last with any mass where rounding leaves none
       const Pair mine_w = lane < DV_WARPS ? s.warp_sum[lane] : zero, upto = scan_lanes(mine_w);
-      const unsigned past = __ballot_sync(0xffffffffu, lane < DV_WARPS && above(upto, c.threshold));
+      const unsigned past = __ballot_sync(0xffffffffu, lane < DV_WARPS && mine_w.h > 0.f && above(upto, c.threshold));
       const unsigned some = __ballot_sync(0xffffffffu, mine_w.h > 0.f);
       const int w = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
       const Pair want = past ? c.threshold : none;

@@ -356,3 +356,22 @@ def test_host_threads_with_vocabularies_of_their_own():
     for V, ins, outs, stream, want in jobs:
         path, cnt, nxt, st = (t.flatten().tolist() for t in outs)
         assert st[0] == 0 and path[:cnt[0]] == want[0] and nxt[0] == want[1]
+
+
+@pytest.mark.parametrize("B,run", [(300, 128), (19, 1024)])
+def test_a_threshold_between_two_halves_never_picks_a_run_without_mass(B, run):
+    """Runs 0 .. 6 hold values of many sizes, runs 7 and 8 nothing, runs 9 .. 15 the values of the first in
+    another order: with u = 1/2 the threshold is the sum of the first half, and sums of another order differ from it in
+    their last bits.  (A run is a warp's part of the row with one CTA a tree, a CTA's with sixteen.)"""
+    r = np.random.default_rng(33)
+    V = 16 * run
+    p = np.zeros((B, V), np.float32)
+    for b in range(B):
+        half = (r.random(7 * run) * 2.0 ** -r.uniform(10, 40, 7 * run)).astype(np.float32)
+        p[b, :7 * run], p[b, 9 * run:] = half, r.permutation(half)
+    path, n, nxt, status = verify(p, None, [0] * B, [-1] * B, range(B + 1), np.zeros(B), np.full(B, 0.5), 1)
+    assert status == 0 and n == [1] * B
+    for b, t in enumerate(nxt):
+        assert t >= 0 and p[b, t] > 0
+        sums, half = np.cumsum(p[b].astype(np.float64)), p[b, :7 * run].astype(np.float64).sum()
+        assert sums[t] > half * (1 - 2.0 ** -40) and sums[t] - p[b, t] < half * (1 + 2.0 ** -40)
