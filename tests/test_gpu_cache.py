@@ -260,3 +260,39 @@ def test_an_append_replays_from_a_graph():
         t.model.append([(0, kf[:, new_path[0]], vf[:, new_path[0]]),
                         (1, kf[:, [3 + new_path[1][0]]], vf[:, [3 + new_path[1][0]]])])
         t.check()
+
+
+def corrupt(t, slot, block, page):
+    t.table[slot, block] = page
+    t.model.table[slot, block] = page
+
+
+@pytest.mark.parametrize("page", [-1, -7, 40, 2 ** 31 - 1])
+@pytest.mark.parametrize("block", [0, 1, 70])
+def test_a_fork_of_a_table_with_a_bad_entry_changes_nothing(page, block):
+    # blocks 0, 1 and 70 are full pages: shared, not copied
+    t = Twin(pages=40 if block < 70 else 100, max_pages=90)
+    if page == 40:
+        page = t.k.shape[1]
+    t.append([20, 16 * 71 + 3 if block == 70 else 40])
+    t.fork([(0, 4)])
+    corrupt(t, 1, block, page)
+    t.fork([(0, 2), (1, 3)], model=False)
+    t.check(moe.MOE_ERR_DEVICE_BOUNDS)
+    t.fork([(1, 3)], model=False)
+    t.check(moe.MOE_ERR_DEVICE_BOUNDS)
+    t.fork([(0, 2)])
+    t.check()
+
+
+def test_a_fork_of_many_long_sequences():
+    # every source's table is gone over by the whole plan, however the entries fall
+    t = Twin(pages=3000, slots=400, max_pages=130, layers=1, heads=1)
+    lens = [16 * 128 + 5, 0, 16, 1, 16 * 97, 400]
+    t.append(lens)
+    t.fork([(i % 6, 6 + i) for i in range(390)])
+    t.check()
+    corrupt(t, 4, 96, 3000)
+    t.trim([(s, 0) for s in range(6, 396)])
+    t.fork([(i % 6, 6 + i) for i in range(390)], model=False)
+    t.check(moe.MOE_ERR_DEVICE_BOUNDS)
