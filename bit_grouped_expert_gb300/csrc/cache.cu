@@ -400,8 +400,10 @@ __global__ void __launch_bounds__(COPY_THREADS) fork_copy_kernel(const __grid_co
 
 // ------------------------------------------------------------------ trim
 
-// One CTA per sequence.  A page leaves the table by an exchange, so that it
-// loses exactly one holder whatever else reads the entry.
+// One CTA per sequence.  All of its pages are looked at before any leaves the
+// table, so that a sequence with a bad entry, or a page that nobody holds, stays
+// as it was.  A thread keeps the first four it looks at; those of more than 512
+// are read again.
 __global__ void __launch_bounds__(128) trim_kernel(const __grid_constant__ CacheView c, const int32_t *slots,
                                                    const int32_t *new_lens) {
   start_dependent();
@@ -411,19 +413,31 @@ __global__ void __launch_bounds__(128) trim_kernel(const __grid_constant__ Cache
   ok = ok && want >= 0 && want <= L;
   if (ok && slots)  // a slot named twice: only the first counts
     for (int i = threadIdx.x; i < b; i += 128) ok = ok && slots[i] != slot;
+  constexpr int KEPT = 4;
+  int32_t *table = c.table + (size_t)(ok ? slot : 0) * c.max_pages;
+  const int j0 = pages_of(want, c.page_shift) + threadIdx.x, j1 = ok ? pages_of(L, c.page_shift) : 0;
+  auto held = [&](int page) { return (unsigned)page < (unsigned)c.n_pages && c.refs[page] > 0; };
+  int page[KEPT];
+#pragma unroll
+  for (int u = 0; u < KEPT; ++u) page[u] = j0 + u * 128 < j1 ? table[j0 + u * 128] : 0;
+#pragma unroll
+  for (int u = 0; u < KEPT; ++u) ok = (j0 + u * 128 >= j1 || held(page[u])) && ok;
+  for (int j = j0 + KEPT * 128; j < j1; j += 128) ok = held(table[j]) && ok;
   if (!__syncthreads_and(ok)) {
     if (threadIdx.x == 0) set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
-  for (int j = pages_of(want, c.page_shift) + threadIdx.x; j < pages_of(L, c.page_shift); j += 128) {
-    const int page = atomicExch(&c.table[(size_t)slot * c.max_pages + j], -1);
-    if ((unsigned)page >= (unsigned)c.n_pages)
-      set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
-    else if (atomicSub(&c.refs[page], 1) <= 0) {
-      atomicAdd(&c.refs[page], 1);
+  auto release = [&](int j, int p) {
+    table[j] = -1;
+    if (atomicSub(&c.refs[p], 1) <= 0) {  // named by more tables of the call than it has holders
+      atomicAdd(&c.refs[p], 1);
       set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
     }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < KEPT; ++u)
+    if (j0 + u * 128 < j1) release(j0 + u * 128, page[u]);
+  for (int j = j0 + KEPT * 128; j < j1; j += 128) release(j, table[j]);
   if (threadIdx.x == 0) c.lens[slot] = want;
 }
 

@@ -77,7 +77,8 @@ moe_status attn_cache_append(const attn_cache *c, const void *k_new_d, const voi
  * times; a dst is named once and is no src of the call.  n <= 1024; n == 0
  * returns MOE_OK with nothing enqueued.
  *   src_d, dst_d  int32 [n];  ws_d  attn_cache_fork_workspace_bytes(c, n), scratch
- * Device checks and errors as for attn_cache_append. */
+ * Device checks: slots in range, each dst empty, named once and no src, every
+ * position block of a src's length in its table.  Errors as for attn_cache_append. */
 size_t attn_cache_fork_workspace_bytes(const attn_cache *c, int32_t n);
 moe_status attn_cache_fork(const attn_cache *c, const int32_t *src_d, const int32_t *dst_d, int32_t n, void *ws_d,
                            size_t ws_bytes, void *stream);
@@ -87,7 +88,11 @@ moe_status attn_cache_fork(const attn_cache *c, const int32_t *src_d, const int3
  *   slots_d     int32 [n], distinct, or NULL: 0 .. n-1
  *   new_lens_d  int32 [n], 0 <= new <= the sequence's length
  * n <= 1024; n == 0 returns MOE_OK with nothing enqueued.  Device checks per
- * sequence: one that fails is left as it was. */
+ * sequence: the slot in range (of one named twice the first counts), the new
+ * length, and every page to be given up in the table and with a holder.  One
+ * that fails is left as it was.  (Holders that are too few for several
+ * sequences of one call may be found when these are cut already: the status
+ * word is set, the count stays 0.) */
 moe_status attn_cache_trim(const attn_cache *c, const int32_t *slots_d, const int32_t *new_lens_d, int32_t n,
                            void *stream);
 

@@ -296,3 +296,29 @@ def test_a_fork_of_many_long_sequences():
     t.trim([(s, 0) for s in range(6, 396)])
     t.fork([(i % 6, 6 + i) for i in range(390)], model=False)
     t.check(moe.MOE_ERR_DEVICE_BOUNDS)
+
+
+@pytest.mark.parametrize("page", [-1, -7, 40, 2 ** 31 - 1])
+@pytest.mark.parametrize("block", [1, 2, 140])
+def test_a_trim_over_a_bad_entry_leaves_that_sequence_as_it_was(page, block):
+    t = Twin(pages=40 if block < 140 else 400, max_pages=150)
+    if page == 40:
+        page = t.k.shape[1]
+    t.append([50, 60, 16 * 143 if block == 140 else 55])
+    corrupt(t, 2, block, page)
+    t.trim([(0, 5), (2, 3), (1, 0)], model=False)
+    t.model.trim(0, 5)
+    t.model.trim(1, 0)
+    t.check(moe.MOE_ERR_DEVICE_BOUNDS)
+    t.trim([(2, 16 * block + 16)])  # behind the bad entry: nothing wrong there
+    t.check()
+
+
+def test_a_trim_of_a_page_that_nobody_holds_leaves_the_sequence_as_it_was():
+    t = Twin()
+    t.append([50, 40])
+    t.refs[t.table[0, 2].long()] = 0
+    t.model.refs[t.model.table[0, 2]] = 0
+    t.trim([(0, 3), (1, 20)], model=False)
+    t.model.trim(1, 20)
+    t.check(moe.MOE_ERR_DEVICE_BOUNDS)
