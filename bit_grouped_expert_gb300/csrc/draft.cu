@@ -160,8 +160,8 @@ struct Row {
   // a whole quad (zeros where !in)
   __device__ __forceinline__ void load(int k, bool in, float4 &pv, float4 &qv) const {
     const int t = 4 * k - a;
-    pv = in ? __ldg(reinterpret_cast<const float4 *>(p + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (Q) qv = in ? __ldg(reinterpret_cast<const float4 *>(q + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    pv = in ? *reinterpret_cast<const float4 *>(p + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (Q) qv = in ? *reinterpret_cast<const float4 *>(q + t) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   // any quad, the row's ends among them (zeros outside the row)
   __device__ __forceinline__ void load_any(int k, float4 &pv, float4 &qv) const {
@@ -171,8 +171,8 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool in = t + i >= 0 && t + i < V;
-      x[i] = in ? __ldg(p + t + i) : 0.f;
-      y[i] = Q && in ? __ldg(q + t + i) : 0.f;
+      x[i] = in ? p[t + i] : 0.f;
+      y[i] = Q && in ? q[t + i] : 0.f;
     }
     pv = make_float4(x[0], x[1], x[2], x[3]);
     qv = make_float4(y[0], y[1], y[2], y[3]);
@@ -234,8 +234,10 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / ctas;
-  // a dependent of the kernel before (its own dependents wait for its end: let
-  // in early, they took the clusters' places, 28 us a call of 96 trees instead of 20)
+  // A dependent of the kernel before, whose results are read by ordinary loads
+  // only: a read-only one may look at what was there before.  (Its own dependents
+  // wait for its end: let in early, they took the clusters' places, 28 us a call
+  // of 96 trees instead of 20.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   cluster_arrive();  // no CTA's memory is written to before all have started (waited for below)
   int lo = 0, n = 0;
@@ -253,8 +255,8 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
           ok = false;
         else if (par >= 0) {
           const size_t at = (size_t)(lo + par) * a.V + x;
-          s.p_at[i] = __ldg(a.p + at);
-          s.q_at[i] = Q ? __ldg(a.q + at) : 1.f;
+          s.p_at[i] = a.p[at];
+          s.q_at[i] = Q ? a.q[at] : 1.f;
           s.u[i] = a.u_accept[lo + i];
           s.token[i] = x;
         }
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
 
   cluster_wait();
 
-  const float u_sample = rank == 0 ? __ldg(a.u_sample + b) : 0.f;
+  const float u_sample = rank == 0 ? a.u_sample[b] : 0.f;
   // the walker's state
   int32_t *path = a.path + (size_t)b * a.path_stride;
   int cur = 0, at = 0, count = 1, rounds = 0;  // at: the last node looked at

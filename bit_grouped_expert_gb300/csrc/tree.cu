@@ -144,9 +144,9 @@ static_assert(sizeof(Misc) <= 3 * 1024, "misc area");
 __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
   // the loads first: none of them waits for another's check
   Seq s;
-  s.slot = a.slots ? __ldg(a.slots + b) : b;
-  s.lo = __ldg(a.offsets + b);
-  const int hi = __ldg(a.offsets + b + 1);
+  s.slot = a.slots ? a.slots[b] : b;
+  s.lo = a.offsets[b];
+  const int hi = a.offsets[b + 1];
   const bool in = s.slot >= 0 && s.slot < a.c.n_slots;
   s.L = in ? slot_len(a.c, s.slot) : -1;
   s.n = hi - s.lo;
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
-  // what the kernel before writes (lengths, tables, rows, queries) from here on
+  // what the kernel before writes (lengths, tables, rows, queries) from here on,
+  // by ordinary loads: a read-only one may look at what was there before
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // This CTA's run: every thread adds up some sequences' units, a scan gives
   // their places, and the thread whose sequences hold the run's start writes
@@ -730,8 +731,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       if (more) {
         const int32_t *parent = a.parent + w.s.lo;
 #pragma unroll
-        for (int i = 0; i < UPS; ++i) up[i] = tid + i * TR_ROWS < w.s.n ? __ldg(parent + tid + i * TR_ROWS) : -2;
-        if (my_node < w.nodes()) own = __ldg(parent + w.node0() + my_node);
+        for (int i = 0; i < UPS; ++i) up[i] = tid + i * TR_ROWS < w.s.n ? parent[tid + i * TR_ROWS] : -2;
+        if (my_node < w.nodes()) own = parent[w.node0() + my_node];
       }
       if (un.n > 0) ok = finish();
       if (!more || !ok) break;

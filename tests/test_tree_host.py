@@ -158,3 +158,14 @@ def test_verify_host_checks(lib):
 
 def test_status_text():
     assert moe.status_str(moe.MOE_ERR_OUT_OF_PAGES) == "too few free cache pages"
+
+
+@pytest.mark.parametrize("name", ["tree.cu", "draft.cu", "cache.cu", "cache.cuh"])
+def test_early_kernels_read_by_ordinary_loads(name):
+    # a kernel that starts before the one ahead has ended reads data that changes while it runs: none of it
+    # may go the read-only way, which __ldg and __restrict__ pointers to const ask for
+    import os
+    src = os.path.join(os.path.dirname(moe.__file__), "csrc", name)
+    text = open(src).read()
+    for word in ("__ldg", "ld.global.nc", "__restrict__"):
+        assert word not in text, f"{name}: {word}"
