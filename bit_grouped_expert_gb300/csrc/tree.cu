@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   } else {
     // ----------------------------------------------------------------- rows
     constexpr int COLS = C::TILE / C::HALVES, OCOLS = D / C::HALVES;  // this thread's columns of S and of O
+    static_assert(COLS == 64, "a thread's columns of S are one word of sees[], and its P one store");
     const int r = tid & (TR_ROWS - 1), half = tid / TR_ROWS;
     const int my_node = r * a.g_mul >> 16, my_head = r - my_node * a.G;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               } else {
 #pragma unroll
                 for (int q = 0; q < TR_MAXN / 64; ++q)
-                  if (pos / 64 == q) see = sees[q] >> (pos % 64);
+                  if (pos / 64 == q) see = sees[q];
               }
             }
 #pragma unroll
@@ -886,10 +887,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
           const uint32_t p_col = lanes + C::P_COL + (jj & 1) * (C::TILE / 2) + half * (COLS / 2);
-          if constexpr (COLS == 32)
-            ptx::tmem_st_x16(p_col, p);
-          else
-            ptx::tmem_st_x32(p_col, p);
+          ptx::tmem_st_x32(p_col, p);
           ptx::tmem_wait_st();
         } else {
           arrive(&m->s_free);
