@@ -375,3 +375,94 @@ def test_a_threshold_between_two_halves_never_picks_a_run_without_mass(B, run):
         assert t >= 0 and p[b, t] > 0
         sums, half = np.cumsum(p[b].astype(np.float64)), p[b, :7 * run].astype(np.float64).sum()
         assert sums[t] > half * (1 - 2.0 ** -40) and sums[t] - p[b, t] < half * (1 + 2.0 ** -40)
+
+
+@pytest.mark.parametrize("V", [1 << 20, (1 << 20) - 1])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_the_largest_vocabularies(V, drafted):
+    r = np.random.default_rng(36)
+    p, q = probs(r, 4, V, 1.0), probs(r, 4, V, 1.0)
+    tokens, tree = [0, V - 1, 7, V // 2], [-1, 0, 0, 0]
+    ua, us = np.full(4, 0.9, np.float32), np.array([0.6], np.float32)
+    for u in (0.0, 0.6, float(np.nextafter(np.float32(1), np.float32(0)))):
+        us[0] = u
+        same(verify(p, q if drafted else None, tokens, tree, [0, 4], ua, us, 4), p, q if drafted else None,
+             np.array(tokens), [tree], [0, 4], ua, us)
+
+
+def test_the_most_trees():
+    r = np.random.default_rng(37)
+    B, V = 65535, 3
+    p, q = probs(r, B, V, 1.0), probs(r, B, V, 1.0)
+    us = r.random(B, dtype=np.float32)
+    path, n, nxt, status = verify(p, q, np.zeros(B, int), [-1] * B, range(B + 1), np.zeros(B), us, 1)
+    sums = np.cumsum(p.astype(np.float64), 1)
+    assert status == 0 and (path == 0).all() and n == [1] * B
+    np.testing.assert_array_equal(nxt, (sums <= us[:, None].astype(np.float64) * sums[:, -1:]).sum(1))
+
+
+def test_captures_with_copies_and_events_around_the_calls():
+    """A copy and a fill as graph nodes directly in front of every entry point, and a call on a forked branch of the
+    capture: what a dependent launch waits for is then no kernel, or several nodes."""
+    r = np.random.default_rng(35)
+    Hq, Hkv, D, V, n = 8, 2, 64, 3000, 4
+    k, v = (torch.from_numpy(r.normal(size=(1, 16, 16, Hkv, D)).astype(np.float32)).to(DEV).bfloat16() for _ in range(2))
+    refs, table, lens, st = i32([1, 1] + [0] * 14), i32([[0, 1, -1, -1], [-1] * 4, [-1] * 4]), i32([20, 0, 0]), i32([0] * 4)
+    cache = moe.make_attn_cache(k, v, refs, table, lens, st)
+    first = [t.clone() for t in (k, v, refs, table, lens)]
+    kn, vn, q = (torch.from_numpy(r.normal(size=s).astype(np.float32)).to(DEV).bfloat16()
+                 for s in ((1, n, Hkv, D), (1, n, Hkv, D), (n, Hq, D)))
+    parent, off = [-1, 0, 0, 1], i32([0, n])
+    p, d = probs(r, n, V), probs(r, n, V)
+    tok, ua, us = [0, 5, 9, 2], r.random(n, dtype=np.float32), np.array([0.4], np.float32)
+    pg, dg, uag, usg = (torch.from_numpy(x).to(DEV) for x in (p, d, ua, us))
+    hq, hp, par, tokg = q.clone(), pg.clone(), i32(parent), i32(tok)
+    path, cnt, nxt = i32([[0] * n]), i32([0]), i32([0])
+    o, o2 = torch.empty_like(q), torch.empty_like(q)
+    ws = [torch.empty(max(moe.attn_tree_workspace_bytes(cache, 1, n, n, Hq), moe.attn_cache_append_workspace_bytes(cache, 1, n),
+                          moe.attn_cache_fork_workspace_bytes(cache, 1)), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    src, dst, zero, one = i32([0]), i32([2]), i32([0]), i32([2])
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        q.copy_(hq)
+        o.zero_()
+        moe.attn_tree(cache, 0, q, kn[0], vn[0], off, par, 1, n, ws[0], o)
+        o2.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            moe.attn_tree(cache, 0, q, kn[0], vn[0], off, par, 1, n, ws[1], o2)
+        pg.copy_(hp)
+        path.zero_()
+        moe.moe_draft_verify(pg, dg, tokg, par, off, uag, usg, 1, path, cnt, nxt, st)
+        torch.cuda.current_stream().wait_stream(side)
+        moe.attn_cache_append(cache, kn, vn, off, 1, ws[0], path=path, n_keep=cnt)
+        src.copy_(zero)
+        moe.attn_cache_fork(cache, src, dst, 1, ws[0])
+        dst.copy_(one)
+        moe.attn_cache_trim(cache, dst, zero, 1)
+
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    for _ in range(3):
+        for t, old in zip((k, v, refs, table, lens), first):
+            t.copy_(old)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        model = Pages(*[x.float().cpu().numpy() for x in first[:2]], *[x.cpu().numpy().copy() for x in first[2:]])
+        ref = tree_attention(f(q), *model.rows(0), f(kn[0]), f(vn[0]), parent)[0]
+        assert np.linalg.norm(f(o) - ref) <= 2 * 2.0 ** -8 * np.linalg.norm(ref) and torch.equal(o, o2)
+        want, token = verify_drafts(p, d, tok, parent, ua, us[0])
+        assert path[0, :int(cnt)].tolist() == want and int(nxt) == token
+        model.append([(0, f(kn)[:, want], f(vn)[:, want])])
+        model.fork([(0, 2)])
+        model.trim(2, 0)
+        for a, m in ((refs, model.refs), (table, model.table), (lens, model.lens)):
+            np.testing.assert_array_equal(a.cpu().numpy(), m)
+        np.testing.assert_array_equal(f(k), model.k)
+        assert st.tolist() == [0] * 4

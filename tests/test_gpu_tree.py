@@ -416,3 +416,11 @@ def test_cached_values_that_are_not_numbers_show_in_their_columns(L):
     assert torch.isnan(o[:2, :4, 5].float()).all()
     o[:2, :4, 5] = good[:2, :4, 5]
     assert torch.equal(o, good)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,n", [(5, 1, 64, "bf16", 40), (14, 2, 128, "fp16", 19), (127, 1, 64, "bf16", 3),
+                                              (66, 2, 256, "bf16", 9), (128, 1, 64, "fp16", 256)])
+def test_groups_of_odd_sizes_and_the_most_row_tiles(Hq, Hkv, D, dtype, n):
+    # the last: 256 row tiles of one node, more than a team can have CTAs
+    c = Case(32, [200, 0], [tree_of(np.random.default_rng(n), n), [-1]], Hq=Hq, Hkv=Hkv, D=D, page=32, dtype=dtype)
+    c.check(c.run())
