@@ -18,7 +18,10 @@ namespace moe {
 namespace {
 
 // Threads of a planning CTA: one a sequence, and 128 where that is enough (its
-// barriers and scans are most of a small call).
+// barriers and scans are most of a small call: with 512, four rows of one sequence
+// 6.9 us for 6.8, one fork into four 9.1 for 8.8, 8 x 64 rows 11.7 for 11.5).  A large
+// pool wants more: it is gone over from page 0 on, 2,048 pages a round at 128
+// threads, and four rows take 126 us where 280,000 of 312,000 pages are held.
 constexpr int PLAN_FEW = 128, PLAN_MANY = CACHE_MAX_SEQS;
 constexpr int COPY_THREADS = 256;
 
@@ -451,7 +454,10 @@ size_t append_ws(const attn_cache *c, int B, int n_rows, size_t *pages_at) {
 constexpr int COPY_CTAS = 152 * 8, COPY_WARPS = COPY_CTAS * (COPY_THREADS / 32);
 
 // Layers a warp copies of a row: all of them where the rows alone fill the
-// GPU twice, so that a row's place is looked up once; else enough to.
+// GPU twice, so that a row's place is looked up once; else enough to.  One layer
+// always, this rule, all always, us: 24 prompts of up to 500 rows, 10 layers, 89.8,
+// 71.2, 71.2; 24 forks into 96 54.1, 46.6, 44.1; four rows 6.8, 6.8, 8.8; one fork
+// into four 8.8, 8.8, 12.1.  (Between the two all would be better: 64 x 64 rows 38.0, 38.0, 30.4.)
 int layers_per_job(long long rows, int n_layers) {
   const long long n = rows * n_layers / (2 * COPY_WARPS);
   return (int)(n < 1 ? 1 : n > n_layers ? n_layers : n);
@@ -545,7 +551,8 @@ extern "C" moe_status attn_cache_append(const attn_cache *c, const void *k_new_d
   if (e != cudaSuccess) return moe::note_cuda_error(e);
   const bool pdl = moe::prof_quiet(MOE_KERNEL_CACHE_COPY);
   moe::prof_before(MOE_KERNEL_CACHE_COPY, s);
-  // rows of a copied page come on top of the kept ones; the grid strides over all
+  // Rows of a copied page come on top of the kept ones; the grid, which does not
+  // count them (only the device knows them), strides over all.
   e = moe::launch_dep(pdl, moe::append_copy_kernel, dim3(moe::copy_grid(n_rows + B, c->n_layers, a.per_job)),
                       dim3(moe::COPY_THREADS), 0, s, a);
   moe::prof_after(MOE_KERNEL_CACHE_COPY, s);

@@ -12,7 +12,8 @@
 // The sampled token is a whole number that sums in another order must not
 // change, but an SM does two fp64 operations a cycle: residuals and sums are
 // pairs of fp32 (value and error, some 45 bits; T. J. Dekker, "A floating-point
-// technique for extending the available precision", 1971).  With fp64 for the
+// technique for extending the available precision", 1971; the sum with its error
+// without a comparison is D. E. Knuth's, "The Art of Computer Programming" 2, 4.2.2).  With fp64 for the
 // sums of warps and CTAs and for the draw's prefixes alone, one tree over 32,000
 // tokens took 37.6 us, most of it there.
 //
@@ -236,8 +237,8 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
   const int b = blockIdx.x / ctas;
   // A dependent of the kernel before, whose results are read by ordinary loads
   // only: a read-only one may look at what was there before.  (Its own dependents
-  // wait for its end: let in early, they took the clusters' places, 28 us a call
-  // of 96 trees instead of 20.)
+  // wait for its end: let in early, they took the clusters' places, 24 us a call
+  // of 96 trees over 100,003 tokens instead of 16.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   cluster_arrive();  // no CTA's memory is written to before all have started (waited for below)
   int lo = 0, n = 0;
@@ -508,7 +509,14 @@ __global__ void __launch_bounds__(DV_THREADS, 2) verify_kernel(const __grid_cons
 }
 
 // CTAs of a tree's cluster: as many as run at once for B trees, two an SM, up
-// to 16 and down to 1024 tokens a CTA.
+// to 16 and down to 1024 tokens a CTA.  With at least 512, 1024, 2048 or 4096, us:
+//   1 tree of 8,192 tokens, 7 refusals with q    31, 30, 29, 32
+//   1 tree of 32,000                             31, 31, 33, 36
+//   16 trees of 16,384                           63, 63, 35, 33
+//   16 trees of 32,000                           63, 63, 68, 45
+//   16 trees of 131,072 (16 CTAs in any case)    85, 84, 84, 84
+// One tree, which waits for its passes, is served best by 1024.  Sixteen clusters
+// of sixteen CTAs do not all run at once, it seems: there fewer would be better.
 int cluster_ctas(int B, int V) {
   const int n = std::min({DV_MAX_CTAS, 2 * 152 / B, V / 1024});
   return n < 1 ? 1 : n;
@@ -555,7 +563,9 @@ extern "C" moe_status moe_draft_verify(const float *p_d, const float *q_d, const
   cfg.blockDim = dim3(moe::DV_THREADS);
   cfg.stream = s;
   // the residual's cache: a CTA's quads (a row begins up to three tokens into
-  // its first), if two CTAs an SM have room for it
+  // its first), if two CTAs an SM have room for it.  Seven refusals, with it and
+  // without: 1 tree of 32,000 tokens 31 and 38 us, 48 trees 76 and 118, 20 trees of
+  // 131,072 102 and 162; 24 of those have no room and take 187.
   int cache_quads = (V / 4 + 2 + ctas * moe::DV_WARPS - 1) / (ctas * moe::DV_WARPS) * moe::DV_WARPS;
   if (!q_d || cache_quads * 32 > moe::DV_MAX_CACHE) cache_quads = 0;
   cfg.dynamicSmemBytes = (size_t)cache_quads * 32;

@@ -401,8 +401,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   const Count all{__shfl_sync(0xffffffffu, upto.team, 15), __shfl_sync(0xffffffffu, upto.alone, 15)};
   // Teams of one CTA a row tile read a tile of K and V at the same time, so
   // that it comes from DRAM once: 16 trees of 61 nodes over 8,000 positions each
-  // (268 MB, more than L2) took 192 us alone.  Not where trees of different
-  // sizes would leave a fifth of the members without work.
+  // (268 MB, more than L2) take 182 us alone and 108 in teams.  Not where trees of
+  // different sizes would leave a fifth of the members without work.  Alone and
+  // in teams, by the share of the members with work: eight trees of 61 nodes and
+  // eight of 40 (7/8) 149 and 107 us, of 30 (3/4) 142 and 105, of 10 (5/8) 84 and
+  // 104; over 2,000 positions, which L2 holds, 51 and 50 us (all), 49 and 48 (7/8),
+  // 45.8 and 47.3 (3/4).
   const int grid = gridDim.x, cta = blockIdx.x;
   const bool teams = rts > 1 && rts <= grid && 4 * all.team * grid <= 5 * all.alone * (grid / rts);
   const int size = teams ? rts : 1;
@@ -441,7 +445,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     // ---------------------------------------------------------------- loads
     const int pool_rows = a.c.n_pages << a.c.page_shift, in_page = (1 << a.c.page_shift) - 1;
     // boxes of a slot: this lane's rows and column of it.  A K slot of one
-    // column span and a V slot go in one box where a page holds all of its rows.
+    // column span and a V slot go in one box where a page holds all of its rows
+    // (one box a column: 61 nodes over 131,000 positions 108 us for 102, few rows the same).
     const int v_boxes = 64 / a.page_box, k_boxes = C::TILE / a.page_box;
     const bool whole = v_boxes == 1;
     const int v_box = whole ? 0 : lane / C::CHUNKS, v_chunk = whole ? 0 : lane % C::CHUNKS;
@@ -874,6 +879,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               }
             }
           }
+          // The weights are rounded to the cache's type: a tcgen05.mma takes both factors in
+          // one type, and V is the cache's.  Their sum stays in fp32, unrounded.  Each
+          // weight is off by half a step at most, so o by half a step of sum p|v|:
+          // against 64 bits 0.0022-0.0024 (bf16) and 0.00029 (fp16) of the output's norm, with
+          // fp32 weights 0.0017 and 0.00021 from the output's own rounding alone.  (Two products, of
+          // the weights' upper and lower halves, would keep them at twice the MMAs for V.)
           const float base = mx == -INFINITY ? 0.f : -mx;
           uint32_t p[COLS / 2];
           float acc[4] = {};
@@ -915,6 +926,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
 // split over as few as two CTAs and as many as all of them).
 constexpr int TJ_THREADS = 256;
 
+// (One group always, this rule, eight always, whole calls in us: 1 node over 3,000
+// positions 17.4, 14.8, 14.4; 4 x 5 over 9,000 29.8, 25.0, 24.3; 24 x 5 over 6,000
+// 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.)
 __device__ __forceinline__ int part_groups(int parts) { return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8; }
 
 template <int D, bool FP16>

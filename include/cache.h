@@ -17,7 +17,8 @@
  * first error stays until the caller zeroes it) and the call it belongs to
  * changes nothing: attn_cache_append and attn_cache_fork take all of their
  * sequences or none, attn_cache_trim each sequence by itself.
- * Calls on one cache must not overlap (one stream, or ordered by events).
+ * Calls on one cache must not overlap (one stream, or ordered by events).  A
+ * workspace overlaps nothing else.
  */
 #ifndef CACHE_H
 #define CACHE_H

@@ -38,12 +38,12 @@ extern "C" {
  * Arithmetic: scores and softmax in fp32, the weights rounded to the cache's
  * type for the product with V (fp32 sums), o rounded once.  What a row does
  * not see cannot change it, whatever its bits (rows behind a length, other
- * branches, padding).  Supported: Hq a multiple of n_kv_heads, at most 128
+ * branches, padding); a NaN among its scores makes it NaN.  Supported: Hq a multiple of n_kv_heads, at most 128
  * query heads per KV head, B <= 1024.  B == 0 or n_nodes == 0 returns MOE_OK
  * with nothing enqueued.  Device checks (slots, offsets, parents, lengths,
  * pages) set MOE_ERR_DEVICE_BOUNDS in the cache's status word; the output of
- * that tree is then not valid.  o_d overlaps no input.  MOE_ERR_DEVICE_TIMEOUT there: a wait for a
- * copy gave up.
+ * that tree is then not valid.  MOE_ERR_DEVICE_TIMEOUT there: a wait for a
+ * copy gave up.  o_d overlaps no input, ws_d nothing else.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED,
  * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
 size_t attn_tree_workspace_bytes(const attn_cache *c, int32_t B, int32_t n_nodes, int32_t max_nodes, int32_t Hq);
@@ -75,6 +75,7 @@ moe_status attn_tree(const attn_cache *c, int32_t layer, const void *q_d, const 
  *                [0, V)) or MOE_ERR_NONFINITE (the mass to draw from is not finite and positive:
  *                NaN or infinity left in R or, of a child not taken, in R[x]; or p[c] zero everywhere);
  *                that tree then has n_path 0 and next -1
+ * The written arrays overlap nothing else.
  * Supported: 1 <= V <= 2^20, B <= 65535.  B == 0 returns MOE_OK with nothing enqueued.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED, MOE_ERR_CUDA. */
 moe_status moe_draft_verify(const float *p_d, const float *q_d, const int32_t *tokens_d, const int32_t *parent_d,
