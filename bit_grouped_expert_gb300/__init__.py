@@ -48,7 +48,10 @@ EXPORTS = ("moe_plan", "moe_plan_destroy", "moe_workspace_bytes", "moe_workspace
            "moe_last_cuda_error",
            "moe_decode_static", "moe_decode_stack", "gdn_scan", "attn_decode_workspace_bytes", "attn_decode",
            "attn_cache_append_workspace_bytes", "attn_cache_append", "attn_cache_fork_workspace_bytes",
-           "attn_cache_fork", "attn_cache_trim", "attn_tree_workspace_bytes", "attn_tree", "moe_draft_verify")
+           "attn_cache_fork", "attn_cache_trim", "attn_tree_workspace_bytes", "attn_tree", "moe_draft_verify",
+           "attn_rotary_plan", "attn_rotary", "attn_cache_append_rotary", "attn_qcache_append_workspace_bytes",
+           "attn_qcache_append", "attn_qcache_fork_workspace_bytes", "attn_qcache_fork", "attn_qcache_trim",
+           "attn_qcache_attend_workspace_bytes", "attn_qcache_attend")
 
 MOE_DECODE_STATIC_SCRATCH_BYTES = 65536
 
@@ -99,6 +102,24 @@ class attn_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_d", "v_d", "refs_d", "table_d", "lens_d", "status_d")] + \
                [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_slots",
                                               "max_pages", "dtype")]
+
+
+class attn_qcache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_d", "v_d", "k_scale_d", "v_scale_d", "refs_d", "table_d", "lens_d",
+                                               "status_d")] + \
+               [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_slots",
+                                              "max_pages", "reserved")]
+
+
+class attn_rotary_config(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)] + \
+               [(n, ctypes.c_double) for n in ("base", "stretch", "low_turns", "high_turns", "original_len")] + \
+               [("factor", ctypes.c_float)]
+
+
+class attn_rotary_table(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 128), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -181,6 +202,27 @@ def lib():
         L.attn_tree.argtypes = [cache, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, sz, vp, vp]
         L.moe_draft_verify.restype = i32
         L.moe_draft_verify.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp]
+        table, qcache, i64 = ctypes.POINTER(attn_rotary_table), ctypes.POINTER(attn_qcache), ctypes.c_int64
+        L.attn_rotary_plan.restype = i32
+        L.attn_rotary_plan.argtypes = [ctypes.POINTER(attn_rotary_config), table]
+        L.attn_rotary.restype = i32
+        L.attn_rotary.argtypes = [table, vp, i64, i32, vp, i32, i32, i32, vp, i64, vp]
+        L.attn_cache_append_rotary.restype = i32
+        L.attn_cache_append_rotary.argtypes = [cache, table, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
+        L.attn_qcache_append_workspace_bytes.restype = sz
+        L.attn_qcache_append_workspace_bytes.argtypes = [qcache, i32, i32]
+        L.attn_qcache_append.restype = i32
+        L.attn_qcache_append.argtypes = [qcache, table, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
+        L.attn_qcache_fork_workspace_bytes.restype = sz
+        L.attn_qcache_fork_workspace_bytes.argtypes = [qcache, i32]
+        L.attn_qcache_fork.restype = i32
+        L.attn_qcache_fork.argtypes = [qcache, vp, vp, i32, vp, sz, vp]
+        L.attn_qcache_trim.restype = i32
+        L.attn_qcache_trim.argtypes = [qcache, vp, vp, i32, vp]
+        L.attn_qcache_attend_workspace_bytes.restype = sz
+        L.attn_qcache_attend_workspace_bytes.argtypes = [qcache, i32, i32, i32, i32]
+        L.attn_qcache_attend.restype = i32
+        L.attn_qcache_attend.argtypes = [qcache, i32, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, sz, vp, vp]
         _lib = L
     return _lib
 
@@ -384,6 +426,64 @@ def _raw_stream(stream, device):
     return _stream(stream)
 
 
+class Rotary:
+    """The rates of rotary positions (rotary.h): an attn_rotary_table on the host."""
+
+    def __init__(self, struct: attn_rotary_table):
+        self.struct = struct
+        self.ref = ctypes.byref(struct)
+
+
+def make_rotary(dim: int, base: float = 10000.0, interleaved: bool = False, stretch: float = 1.0,
+                low_turns: float = 0.0, high_turns: float = 0.0, original_len: float = 0.0,
+                factor: float = 1.0) -> Rotary:
+    """The rates of the first ``dim`` values of a head: base^(-2i/dim), slowed
+    by ``stretch`` for pairs that turn less than ``high_turns`` times over
+    ``original_len`` positions (fully below ``low_turns``; with both 0 all of them)."""
+    cfg = attn_rotary_config(int(dim), int(interleaved), base, stretch, low_turns, high_turns, original_len, factor)
+    table = attn_rotary_table()
+    _check("attn_rotary_plan", lib().attn_rotary_plan(ctypes.byref(cfg), ctypes.byref(table)))
+    return Rotary(table)
+
+
+def _kind(name, dtype):
+    """MOE_BF16 or MOE_FP16 of a torch type."""
+    import torch
+    if dtype is torch.bfloat16:
+        return MOE_BF16
+    if dtype is torch.float16:
+        return MOE_FP16
+    raise ValueError(f"{name}: bf16 or fp16 wanted, got {dtype}")
+
+
+def _rows_given(name, t, dtype, device, shape):
+    """Address and row stride of rows [n, H, D] whose heads lie one after another."""
+    n, H, D = shape
+    strides = t.stride() if t.dim() == 3 else ()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or (t.numel() and (
+            strides[2] != 1 or (H > 1 and strides[1] != D))):
+        raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} on cuda:{device} wanted, each row's heads one "
+                         f"after another, got {t.dtype} {tuple(t.shape)} with strides {strides} on {t.device}")
+    return t.data_ptr(), strides[0] if n > 1 else H * D
+
+
+def attn_rotary(rotary: Rotary, x, positions, o, stream=None):
+    """Rows turned by their positions (rotary.h): x, o [n, H, D] bf16 or fp16
+    (rows may lie apart; o may be x), positions int32 [n]."""
+    import torch
+    dev, shape = x.get_device(), x.shape
+    _here("x", dev)
+    if len(shape) != 3:
+        raise ValueError(f"x: [n, H, D] wanted, got {tuple(shape)}")
+    n, H, D = shape
+    kind = _kind("x", x.dtype)
+    x_at, x_stride = _rows_given("x", x, x.dtype, dev, shape)
+    o_at, o_stride = _rows_given("o", o, x.dtype, dev, shape)
+    _check("attn_rotary", lib().attn_rotary(
+        rotary.ref, x_at, x_stride, kind, _given("positions", positions, torch.int32, dev, (n,)), n, H, D, o_at, o_stride,
+        _raw_stream(stream, dev)))
+
+
 class AttnCache:
     """A paged KV cache (cache.h): the attn_cache struct and the tensors behind it."""
 
@@ -422,22 +522,35 @@ def attn_cache_append_workspace_bytes(cache: AttnCache, B: int, n_rows: int) -> 
     return int(lib().attn_cache_append_workspace_bytes(cache.ref, int(B), int(n_rows)))
 
 
+def _append_given(cache, dtype, k_new, v_new, offsets, B, ws, slots, path, n_keep):
+    """The arguments that every append shares, in the entry points' order, up to the stream."""
+    dev, i32, n_rows = cache.device, cache.i32, k_new.shape[1]
+    _here("cache", dev)
+    shape, stride = (cache.layers, n_rows, cache.heads, cache.dim), 0 if path is None else path.shape[-1]
+    return ((_given("k_new", k_new, dtype, dev, shape), _given("v_new", v_new, dtype, dev, shape)),
+            (None if slots is None else _given("slots", slots, i32, dev, (B,)),
+             _given("offsets", offsets, i32, dev, (B + 1,)),
+             None if n_keep is None else _given("n_keep", n_keep, i32, dev, (B,)),
+             None if path is None else _given("path", path, i32, dev, (B, stride)), stride, B, n_rows,
+             *_scratch(ws, dev)))
+
+
 def attn_cache_append(cache: AttnCache, k_new, v_new, offsets, B: int, ws, slots=None, path=None, n_keep=None,
                       stream=None):
     """Append the kept rows of B sequences, in all layers: k_new, v_new
     [n_layers, n_rows, Hkv, D], offsets int32 [B + 1], slots int32 [B] or None
     (0 .. B-1), path int32 [B, stride] and n_keep int32 [B] as moe_draft_verify
     leaves them, or None (every row, in order)."""
-    dev, i32, n_rows, B = cache.device, cache.i32, k_new.shape[1], int(B)
-    _here("cache", dev)
-    shape, stride = (cache.layers, n_rows, cache.heads, cache.dim), 0 if path is None else path.shape[-1]
-    _check("attn_cache_append", lib().attn_cache_append(
-        cache.ref, _given("k_new", k_new, cache.dtype, dev, shape), _given("v_new", v_new, cache.dtype, dev, shape),
-        None if slots is None else _given("slots", slots, i32, dev, (B,)),
-        _given("offsets", offsets, i32, dev, (B + 1,)),
-        None if n_keep is None else _given("n_keep", n_keep, i32, dev, (B,)),
-        None if path is None else _given("path", path, i32, dev, (B, stride)), stride, B, n_rows, *_scratch(ws, dev),
-        _raw_stream(stream, dev)))
+    rows, rest = _append_given(cache, cache.dtype, k_new, v_new, offsets, int(B), ws, slots, path, n_keep)
+    _check("attn_cache_append", lib().attn_cache_append(cache.ref, *rows, *rest, _raw_stream(stream, cache.device)))
+
+
+def attn_cache_append_rotary(cache: AttnCache, rotary: Rotary, k_new, v_new, offsets, B: int, ws, slots=None, path=None,
+                             n_keep=None, stream=None):
+    """As attn_cache_append, every K row turned by the position it is stored at (rotary.h)."""
+    rows, rest = _append_given(cache, cache.dtype, k_new, v_new, offsets, int(B), ws, slots, path, n_keep)
+    _check("attn_cache_append_rotary", lib().attn_cache_append_rotary(cache.ref, rotary.ref, *rows, *rest,
+                                                                      _raw_stream(stream, cache.device)))
 
 
 def attn_cache_fork_workspace_bytes(cache: AttnCache, n: int) -> int:
@@ -503,6 +616,98 @@ def moe_draft_verify(p, q, tokens, parent, offsets, u_accept, u_sample, B: int, 
         _given("u_sample", u_sample, f32, dev, (B,)), B, n, V, _given("path", path, i32, dev, (B, stride)), stride,
         _given("n_path", n_path, i32, dev, (B,)), _given("next_token", next_token, i32, dev, (B,)),
         _given("status", status, i32, dev, status.shape), _raw_stream(stream, dev)))
+
+
+class AttnQCache:
+    """An 8-bit paged KV cache (qcache.h): the attn_qcache struct and the tensors behind it."""
+
+    def __init__(self, struct: attn_qcache, tensors: dict):
+        import torch
+        self.struct = struct
+        self.ref = ctypes.byref(struct)
+        self.tensors = tensors
+        self.i32 = torch.int32
+        self.device = tensors["k"].get_device()
+        self.layers, self.heads, self.dim = struct.n_layers, struct.n_kv_heads, struct.head_dim
+
+
+def make_attn_qcache(k, v, k_scale, v_scale, refs, table, lens, status) -> AttnQCache:
+    """The cache over the caller's tensors: k, v float8_e4m3fn [n_layers,
+    n_pages, page_size, Hkv, D], k_scale, v_scale fp32 [n_layers, n_pages, Hkv], the
+    others as for make_attn_cache.  A new cache starts with refs, lens and
+    status zero and table -1."""
+    import torch
+    if k.dtype is not torch.float8_e4m3fn or k.dim() != 5 or table.dim() != 2 or lens.dim() != 1 or status.dim() != 1:
+        raise ValueError(f"k: float8_e4m3fn [layers, pages, page_size, heads, dim], table of 2, lens and status of 1 "
+                         f"dimensions wanted, got k {k.dtype} {tuple(k.shape)}")
+    layers, pages, page, heads, dim = k.shape
+    dev, ints, scales = k.get_device(), torch.int32, (layers, pages, heads)
+    st = attn_qcache(_given("k", k, k.dtype, dev, k.shape), _given("v", v, k.dtype, dev, k.shape),
+                     _given("k_scale", k_scale, torch.float32, dev, scales),
+                     _given("v_scale", v_scale, torch.float32, dev, scales),
+                     _given("refs", refs, ints, dev, (pages,)),
+                     _given("table", table, ints, dev, (lens.shape[0], table.shape[1])),
+                     _given("lens", lens, ints, dev, lens.shape), _given("status", status, ints, dev, status.shape),
+                     layers, pages, page, heads, dim, lens.shape[0], table.shape[1], 0)
+    return AttnQCache(st, dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, refs=refs, table=table, lens=lens,
+                               status=status))
+
+
+def attn_qcache_append_workspace_bytes(cache: AttnQCache, B: int, n_rows: int) -> int:
+    return int(lib().attn_qcache_append_workspace_bytes(cache.ref, int(B), int(n_rows)))
+
+
+def attn_qcache_append(cache: AttnQCache, rotary, k_new, v_new, offsets, B: int, ws, slots=None, path=None, n_keep=None,
+                       stream=None):
+    """As attn_cache_append, into e4m3 codes (qcache.h); k_new, v_new bf16 or fp16.
+    ``rotary``: K rows are turned by the position they are stored at; None: not."""
+    kind = _kind("k_new", k_new.dtype)
+    rows, rest = _append_given(cache, k_new.dtype, k_new, v_new, offsets, int(B), ws, slots, path, n_keep)
+    _check("attn_qcache_append", lib().attn_qcache_append(cache.ref, None if rotary is None else rotary.ref, *rows, kind,
+                                                          *rest, _raw_stream(stream, cache.device)))
+
+
+def attn_qcache_fork_workspace_bytes(cache: AttnQCache, n: int) -> int:
+    return int(lib().attn_qcache_fork_workspace_bytes(cache.ref, int(n)))
+
+
+def attn_qcache_fork(cache: AttnQCache, src, dst, n: int, ws, stream=None):
+    """As attn_cache_fork; a copied page brings its scales."""
+    dev, n = cache.device, int(n)
+    _here("cache", dev)
+    _check("attn_qcache_fork", lib().attn_qcache_fork(
+        cache.ref, _given("src", src, cache.i32, dev, (n,)), _given("dst", dst, cache.i32, dev, (n,)), n,
+        *_scratch(ws, dev), _raw_stream(stream, dev)))
+
+
+def attn_qcache_trim(cache: AttnQCache, slots, new_lens, n: int, stream=None):
+    """As attn_cache_trim."""
+    dev, n = cache.device, int(n)
+    _here("cache", dev)
+    _check("attn_qcache_trim", lib().attn_qcache_trim(
+        cache.ref, None if slots is None else _given("slots", slots, cache.i32, dev, (n,)),
+        _given("new_lens", new_lens, cache.i32, dev, (n,)), n, _raw_stream(stream, dev)))
+
+
+def attn_qcache_attend_workspace_bytes(cache: AttnQCache, B: int, n_rows: int, max_rows: int, Hq: int) -> int:
+    return int(lib().attn_qcache_attend_workspace_bytes(cache.ref, int(B), int(n_rows), int(max_rows), int(Hq)))
+
+
+def attn_qcache_attend(cache: AttnQCache, layer: int, q, offsets, B: int, max_rows: int, ws, o, slots=None,
+                       scale: float = 0.0, stream=None):
+    """Attention of the last rows of B sequences over the 8-bit cache's layer
+    (qcache.h): q, o [n_rows, Hq, D] bf16 or fp16, offsets int32 [B + 1], slots
+    int32 [B] or None (0 .. B-1), ws a uint8 device tensor of
+    attn_qcache_attend_workspace_bytes bytes or more."""
+    dev, i32 = cache.device, cache.i32
+    _here("cache", dev)
+    n, Hq, _ = q.shape
+    layer, B, max_rows, shape = int(layer), int(B), int(max_rows), (n, Hq, cache.dim)
+    kind = _kind("q", q.dtype)
+    _check("attn_qcache_attend", lib().attn_qcache_attend(
+        cache.ref, layer, _given("q", q, q.dtype, dev, shape), kind,
+        None if slots is None else _given("slots", slots, i32, dev, (B,)), _given("offsets", offsets, i32, dev, (B + 1,)),
+        B, n, max_rows, Hq, scale, *_scratch(ws, dev), _given("o", o, q.dtype, dev, shape), _raw_stream(stream, dev)))
 
 
 def moe_route_view(plan: Plan, ws, T: int) -> moe_route_ptrs:

@@ -23,7 +23,6 @@ namespace {
 // pool wants more: it is gone over from page 0 on, 2,048 pages a round at 128
 // threads, and four rows take 126 us where 280,000 of 312,000 pages are held.
 constexpr int PLAN_FEW = 128, PLAN_MANY = CACHE_MAX_SEQS;
-constexpr int COPY_THREADS = 256;
 
 // Exclusive prefix sum of one int per thread over the CTA; *total gets the
 // sum.  Every thread calls it; red: 33 ints of shared memory.
@@ -79,64 +78,7 @@ __device__ __forceinline__ int find_free(const CacheView &c, int want, int *red,
   return found;
 }
 
-// The last i in [0, n) with start[i] <= v (start ascending, start[0] <= v).
-__device__ __forceinline__ int segment_of(const int *start, int n, int v) {
-  int s = 0;
-#pragma unroll
-  for (int step = CACHE_MAX_SEQS / 2; step; step >>= 1)
-    if (s + step < n && start[s + step] <= v) s += step;
-  return s;
-}
-
-// One row (a multiple of 64 values) of K and V in `layers` layers, by one
-// warp; strides in values from layer to layer.  Two layers at a time, so that
-// eight 16-byte loads a lane are on their way before the first store.
-__device__ __forceinline__ void copy_rows(uint16_t *kd, uint16_t *vd, const uint16_t *ks, const uint16_t *vs, int row,
-                                          int layers, size_t to, size_t from) {
-  const int lane = threadIdx.x & 31;
-  auto at = [](const uint16_t *p, size_t i) { return reinterpret_cast<const uint4 *>(p) + i; };
-  auto put = [](uint16_t *p, size_t i, uint4 x) { reinterpret_cast<uint4 *>(p)[i] = x; };
-  int l = 0;
-  for (; l + 2 <= layers; l += 2) {
-#pragma unroll 2
-    for (int i = lane; i < row / 8; i += 32) {
-      const uint4 k0 = *at(ks, i), v0 = *at(vs, i), k1 = *at(ks + from, i), v1 = *at(vs + from, i);
-      put(kd, i, k0);
-      put(vd, i, v0);
-      put(kd + to, i, k1);
-      put(vd + to, i, v1);
-    }
-    kd += 2 * to, vd += 2 * to, ks += 2 * from, vs += 2 * from;
-  }
-  if (l < layers)
-#pragma unroll 2
-    for (int i = lane; i < row / 8; i += 32) {
-      const uint4 k0 = *at(ks, i), v0 = *at(vs, i);
-      put(kd, i, k0);
-      put(vd, i, v0);
-    }
-}
-
 // ---------------------------------------------------------------- append
-
-// A sequence's part of an append, written by the plan and read by the copies.
-struct AppendSeg {
-  int32_t start;     // its first row in the call's count: copied page rows, then kept rows
-  int32_t cow;       // rows to copy from old_page to a page of the sequence's own
-  int32_t old_page;
-  int32_t slot, len, src;  // len: before the append; src: its first row of k_new
-};
-
-struct AppendArgs {
-  CacheView c;
-  const uint16_t *k_new, *v_new;
-  const int32_t *slots, *offsets, *n_keep, *path;
-  int path_stride, B, n_rows;
-  int32_t *rows;   // [1] rows to copy, 0 if the call changes nothing
-  AppendSeg *seg;  // [B]
-  int32_t *pages;  // the pages found
-  int per_job;     // layers a warp copies of a row
-};
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) append_plan_kernel(const __grid_constant__ AppendArgs a) {
@@ -273,6 +215,8 @@ struct ForkArgs {
   ForkSeg *seg;   // [n]
   int32_t *pages;
   int per_job;    // layers a warp copies of a row
+  float *ks, *vs; // scales [layers][pages][heads] that a copied page brings along, or null
+  int heads;
 };
 
 template <int THREADS>
@@ -387,6 +331,16 @@ __global__ void __launch_bounds__(COPY_THREADS) fork_copy_kernel(const __grid_co
     c.table[(size_t)a.seg[s].dst * c.max_pages + j] = page;
     if (page >= 0) atomicAdd(&c.refs[page], 1);
   }
+  if (a.ks)
+    for (long long e = (long long)blockIdx.x * COPY_THREADS + threadIdx.x, each = (long long)c.n_layers * a.heads;
+         e < a.n * each; e += (long long)gridDim.x * COPY_THREADS) {
+      const ForkSeg g = a.seg[e / each];
+      if (g.new_page < 0) continue;
+      const int layer = (int)(e % each) / a.heads, head = (int)(e % each) % a.heads;
+      const size_t base = (size_t)layer * c.n_pages;
+      a.ks[(base + g.new_page) * a.heads + head] = a.ks[(base + g.old_page) * a.heads + head];
+      a.vs[(base + g.new_page) * a.heads + head] = a.vs[(base + g.old_page) * a.heads + head];
+    }
   const long long warps = (long long)gridDim.x * (COPY_THREADS / 32);
   const int jobs = (c.n_layers + a.per_job - 1) / a.per_job;  // of a row
   const size_t pool = ((size_t)c.n_pages << c.page_shift) * c.row;  // values of a layer
@@ -444,58 +398,88 @@ __global__ void __launch_bounds__(128) trim_kernel(const __grid_constant__ Cache
   if (threadIdx.x == 0) c.lens[slot] = want;
 }
 
-// Workspaces: a header of 64 bytes, the segments, the pages found.
-size_t append_ws(const attn_cache *c, int B, int n_rows, size_t *pages_at) {
-  *pages_at = 64 + (size_t)B * sizeof(AppendSeg);
-  return *pages_at + ((size_t)n_rows / c->page_size + 2 * (size_t)B) * 4;
-}
-
-// Warps of a copy at most: eight CTAs for each of 152 SMs.
-constexpr int COPY_CTAS = 152 * 8, COPY_WARPS = COPY_CTAS * (COPY_THREADS / 32);
-
-// Layers a warp copies of a row: all of them where the rows alone fill the
-// GPU twice, so that a row's place is looked up once; else enough to.  One layer
-// always, this rule, all always, us: 24 prompts of up to 500 rows, 10 layers, 89.8,
-// 71.2, 71.2; 24 forks into 96 54.1, 46.6, 44.1; four rows 6.8, 6.8, 8.8; one fork
-// into four 8.8, 8.8, 12.1.  (Between the two all would be better: 64 x 64 rows 38.0, 38.0, 30.4.)
-int layers_per_job(long long rows, int n_layers) {
-  const long long n = rows * n_layers / (2 * COPY_WARPS);
-  return (int)(n < 1 ? 1 : n > n_layers ? n_layers : n);
-}
-
-int copy_grid(long long rows, int n_layers, int per_job) {
-  const long long jobs = rows * ((n_layers + per_job - 1) / per_job);
-  const long long g = (jobs + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32);
-  return (int)(g < 1 ? 1 : g > COPY_CTAS ? COPY_CTAS : g);
-}
-
 }  // namespace
 
-moe_status cache_view(const attn_cache *c, CacheView *out) {
-  if (!c || !c->k_d || !c->v_d || !c->refs_d || !c->table_d || !c->lens_d || !c->status_d || c->n_layers < 1 ||
-      c->n_pages < 1 || c->n_slots < 1 || c->max_pages < 1 || c->n_kv_heads < 1 || c->page_size < 1)
+moe_status cache_view_any(const void *k, const void *v, int32_t *refs, int32_t *table, int32_t *lens, int32_t *status,
+                          int n_layers, int n_pages, int page_size, int n_kv_heads, int head_dim, int n_slots,
+                          int max_pages, int row_words, CacheView *out) {
+  if (!k || !v || !refs || !table || !lens || !status || n_layers < 1 || n_pages < 1 || n_slots < 1 || max_pages < 1 ||
+      n_kv_heads < 1 || page_size < 1)
     return MOE_ERR_INVALID_ARGUMENT;
-  const int ps = c->page_size, D = c->head_dim;
-  if ((ps & (ps - 1)) || ps < 16 || ps > 256 || (D != 64 && D != 128 && D != 256) || c->n_kv_heads > 256 ||
-      (int64_t)c->n_pages * ps > INT32_MAX || (int64_t)c->max_pages * ps > (1 << 30) ||
-      (c->dtype != MOE_BF16 && c->dtype != MOE_FP16))
+  const int ps = page_size, D = head_dim;
+  if ((ps & (ps - 1)) || ps < 16 || ps > 256 || (D != 64 && D != 128 && D != 256) || n_kv_heads > 256 ||
+      (int64_t)n_pages * ps > INT32_MAX || (int64_t)max_pages * ps > (1 << 30))
     return MOE_ERR_UNSUPPORTED;
-  if (!aligned16(c->k_d) || !aligned16(c->v_d) || !aligned16(c->refs_d) || !aligned16(c->table_d) ||
-      !aligned16(c->lens_d) || !aligned16(c->status_d))
+  if (!aligned16(k) || !aligned16(v) || !aligned16(refs) || !aligned16(table) || !aligned16(lens) || !aligned16(status))
     return MOE_ERR_MISALIGNED;
-  out->k = static_cast<uint16_t *>(c->k_d);
-  out->v = static_cast<uint16_t *>(c->v_d);
-  out->refs = c->refs_d;
-  out->table = c->table_d;
-  out->lens = c->lens_d;
-  out->status = c->status_d;
-  out->n_layers = c->n_layers;
-  out->n_pages = c->n_pages;
+  out->k = static_cast<uint16_t *>(const_cast<void *>(k));
+  out->v = static_cast<uint16_t *>(const_cast<void *>(v));
+  out->refs = refs;
+  out->table = table;
+  out->lens = lens;
+  out->status = status;
+  out->n_layers = n_layers;
+  out->n_pages = n_pages;
   out->page_shift = __builtin_ctz(ps);
-  out->row = c->n_kv_heads * D;
-  out->n_slots = c->n_slots;
-  out->max_pages = c->max_pages;
+  out->row = row_words;
+  out->n_slots = n_slots;
+  out->max_pages = max_pages;
   return MOE_OK;
+}
+
+moe_status cache_view(const attn_cache *c, CacheView *out) {
+  if (!c) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status st =
+      cache_view_any(c->k_d, c->v_d, c->refs_d, c->table_d, c->lens_d, c->status_d, c->n_layers, c->n_pages,
+                     c->page_size, c->n_kv_heads, c->head_dim, c->n_slots, c->max_pages,
+                     c->n_kv_heads * c->head_dim, out);
+  if (st == MOE_ERR_INVALID_ARGUMENT) return st;
+  return c->dtype != MOE_BF16 && c->dtype != MOE_FP16 ? MOE_ERR_UNSUPPORTED : st;
+}
+
+// Workspaces: a header of 64 bytes, the segments, the pages found.
+size_t append_ws(int page_size, int B, int n_rows, size_t *pages_at) {
+  *pages_at = 64 + (size_t)B * sizeof(AppendSeg);
+  return *pages_at + ((size_t)n_rows / page_size + 2 * (size_t)B) * 4;
+}
+
+moe_status append_args(const CacheView &c, const AppendCall &call, int new_words, AppendArgs *a) {
+  if (call.B < 0 || call.n_rows < 0 || (call.path && (!call.n_keep || call.path_stride < 1)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (call.B > CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
+  a->B = call.B;
+  if (call.B == 0) return MOE_OK;
+  if (!call.offsets || !call.ws || (call.n_rows > 0 && (!call.k_new || !call.v_new))) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(call.k_new) || !aligned16(call.v_new) || !aligned16(call.slots) || !aligned16(call.offsets) ||
+      !aligned16(call.n_keep) || !aligned16(call.path) || !aligned16(call.ws))
+    return MOE_ERR_MISALIGNED;
+  const size_t nn = (size_t)c.n_layers * call.n_rows * new_words * 2;
+  const size_t np = ((size_t)c.n_layers * c.n_pages << c.page_shift) * c.row * 2;
+  if (ranges_meet(call.k_new, nn, c.k, np) || ranges_meet(call.k_new, nn, c.v, np) ||
+      ranges_meet(call.v_new, nn, c.k, np) || ranges_meet(call.v_new, nn, c.v, np))
+    return MOE_ERR_INVALID_ARGUMENT;
+  size_t pages_at;
+  if (call.ws_bytes < append_ws(1 << c.page_shift, call.B, call.n_rows, &pages_at)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  a->c = c;
+  a->k_new = static_cast<const uint16_t *>(call.k_new);
+  a->v_new = static_cast<const uint16_t *>(call.v_new);
+  a->slots = call.slots;
+  a->offsets = call.offsets;
+  a->n_keep = call.n_keep;
+  a->path = call.path;
+  a->path_stride = call.path_stride;
+  a->n_rows = call.n_rows;
+  a->rows = static_cast<int32_t *>(call.ws);
+  a->seg = ws_ptr<AppendSeg>(call.ws, 64);
+  a->pages = ws_ptr<int32_t>(call.ws, pages_at);
+  a->per_job = layers_per_job(call.n_rows, c.n_layers);
+  return MOE_OK;
+}
+
+cudaError_t launch_append_plan(const AppendArgs &a, cudaStream_t s) {
+  const bool chain = prof_chain(0);
+  return a.B <= PLAN_FEW ? launch_dep(chain, append_plan_kernel<PLAN_FEW>, dim3(1), dim3(PLAN_FEW), 0, s, a)
+                         : launch_dep(chain, append_plan_kernel<PLAN_MANY>, dim3(1), dim3(PLAN_MANY), 0, s, a);
 }
 
 }  // namespace moe
@@ -504,50 +488,22 @@ extern "C" size_t attn_cache_append_workspace_bytes(const attn_cache *c, int32_t
   moe::CacheView v;
   if (moe::cache_view(c, &v) != MOE_OK || B < 1 || B > moe::CACHE_MAX_SEQS || n_rows < 0) return 0;
   size_t at;
-  return moe::append_ws(c, B, n_rows, &at);
+  return moe::append_ws(c->page_size, B, n_rows, &at);
 }
 
 extern "C" moe_status attn_cache_append(const attn_cache *c, const void *k_new_d, const void *v_new_d,
                                         const int32_t *slots_d, const int32_t *offsets_d, const int32_t *n_keep_d,
                                         const int32_t *path_d, int32_t path_stride, int32_t B, int32_t n_rows,
                                         void *ws_d, size_t ws_bytes, void *stream) {
-  using moe::aligned16;
+  moe::CacheView v;
   moe::AppendArgs a;
-  const moe_status st = moe::cache_view(c, &a.c);
+  moe_status st = moe::cache_view(c, &v);
   if (st != MOE_OK) return st;
-  if (B < 0 || n_rows < 0 || (path_d && (!n_keep_d || path_stride < 1))) return MOE_ERR_INVALID_ARGUMENT;
-  if (B > moe::CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
-  if (B == 0) return MOE_OK;
-  if (!offsets_d || !ws_d || (n_rows > 0 && (!k_new_d || !v_new_d))) return MOE_ERR_INVALID_ARGUMENT;
-  if (!aligned16(k_new_d) || !aligned16(v_new_d) || !aligned16(slots_d) || !aligned16(offsets_d) ||
-      !aligned16(n_keep_d) || !aligned16(path_d) || !aligned16(ws_d))
-    return MOE_ERR_MISALIGNED;
-  const size_t nn = (size_t)c->n_layers * n_rows * a.c.row * 2;
-  const size_t np = (size_t)c->n_layers * c->n_pages * c->page_size * a.c.row * 2;
-  if (moe::ranges_meet(k_new_d, nn, c->k_d, np) || moe::ranges_meet(k_new_d, nn, c->v_d, np) ||
-      moe::ranges_meet(v_new_d, nn, c->k_d, np) || moe::ranges_meet(v_new_d, nn, c->v_d, np))
-    return MOE_ERR_INVALID_ARGUMENT;
-  size_t pages_at;
-  if (ws_bytes < moe::append_ws(c, B, n_rows, &pages_at)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  a.k_new = static_cast<const uint16_t *>(k_new_d);
-  a.v_new = static_cast<const uint16_t *>(v_new_d);
-  a.slots = slots_d;
-  a.offsets = offsets_d;
-  a.n_keep = n_keep_d;
-  a.path = path_d;
-  a.path_stride = path_stride;
-  a.B = B;
-  a.n_rows = n_rows;
-  a.rows = static_cast<int32_t *>(ws_d);
-  a.seg = moe::ws_ptr<moe::AppendSeg>(ws_d, 64);
-  a.pages = moe::ws_ptr<int32_t>(ws_d, pages_at);
-  a.per_job = moe::layers_per_job(n_rows, c->n_layers);
+  st = moe::append_args(v, moe::AppendCall{k_new_d, v_new_d, slots_d, offsets_d, n_keep_d, path_d, path_stride, B, n_rows,
+                                           ws_d, ws_bytes}, v.row, &a);
+  if (st != MOE_OK || a.B == 0) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool chain = moe::prof_chain(0);
-  cudaError_t e = B <= moe::PLAN_FEW
-                      ? moe::launch_dep(chain, moe::append_plan_kernel<moe::PLAN_FEW>, dim3(1), dim3(moe::PLAN_FEW), 0, s, a)
-                      : moe::launch_dep(chain, moe::append_plan_kernel<moe::PLAN_MANY>, dim3(1), dim3(moe::PLAN_MANY), 0,
-                                        s, a);
+  cudaError_t e = moe::launch_append_plan(a, s);
   if (e != cudaSuccess) return moe::note_cuda_error(e);
   const bool pdl = moe::prof_quiet(MOE_KERNEL_CACHE_COPY);
   moe::prof_before(MOE_KERNEL_CACHE_COPY, s);
@@ -559,58 +515,71 @@ extern "C" moe_status attn_cache_append(const attn_cache *c, const void *k_new_d
   return moe::note_cuda_error(e);
 }
 
+namespace moe {
+
+size_t fork_ws(int n) { return n < 1 || n > CACHE_MAX_SEQS ? 0 : 64 + (size_t)n * (sizeof(ForkSeg) + 4); }
+
+moe_status fork_call(const CacheView &c, const int32_t *src, const int32_t *dst, int n, void *ws, size_t ws_bytes,
+                     float *ks, float *vs, int heads, cudaStream_t s) {
+  if (n < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (n > CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!src || !dst || !ws) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(src) || !aligned16(dst) || !aligned16(ws)) return MOE_ERR_MISALIGNED;
+  if (ws_bytes < fork_ws(n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  ForkArgs a;
+  a.c = c;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.rows = static_cast<int32_t *>(ws);
+  a.seg = ws_ptr<ForkSeg>(ws, 64);
+  a.pages = ws_ptr<int32_t>(ws, 64 + (size_t)n * sizeof(ForkSeg));
+  a.ks = ks;
+  a.vs = vs;
+  a.heads = heads;
+  const long long rows = (long long)n << c.page_shift >> 1;  // half a page a fork on average
+  a.per_job = layers_per_job(rows, c.n_layers);
+  const bool chain = prof_chain(0);
+  cudaError_t e = n <= PLAN_FEW
+                      ? launch_dep(chain, fork_plan_kernel<PLAN_FEW>, dim3(1), dim3(PLAN_FEW), 0, s, a)
+                      : launch_dep(chain, fork_plan_kernel<PLAN_MANY>, dim3(1), dim3(PLAN_MANY), 0, s, a);
+  if (e != cudaSuccess) return note_cuda_error(e);
+  const bool pdl = prof_quiet(MOE_KERNEL_CACHE_COPY);
+  prof_before(MOE_KERNEL_CACHE_COPY, s);
+  e = launch_dep(pdl, fork_copy_kernel, dim3(copy_grid(rows, c.n_layers, a.per_job)), dim3(COPY_THREADS), 0, s, a);
+  prof_after(MOE_KERNEL_CACHE_COPY, s);
+  return note_cuda_error(e);
+}
+
+moe_status trim_call(const CacheView &c, const int32_t *slots, const int32_t *new_lens, int n, cudaStream_t s) {
+  if (n < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (n > CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (!new_lens) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(slots) || !aligned16(new_lens)) return MOE_ERR_MISALIGNED;
+  return note_cuda_error(launch_dep(prof_chain(0), trim_kernel, dim3(n), dim3(128), 0, s, c, slots, new_lens));
+}
+
+}  // namespace moe
+
 extern "C" size_t attn_cache_fork_workspace_bytes(const attn_cache *c, int32_t n) {
   moe::CacheView v;
-  if (moe::cache_view(c, &v) != MOE_OK || n < 1 || n > moe::CACHE_MAX_SEQS) return 0;
-  return 64 + (size_t)n * (sizeof(moe::ForkSeg) + 4);
+  return moe::cache_view(c, &v) == MOE_OK ? moe::fork_ws(n) : 0;
 }
 
 extern "C" moe_status attn_cache_fork(const attn_cache *c, const int32_t *src_d, const int32_t *dst_d, int32_t n,
                                       void *ws_d, size_t ws_bytes, void *stream) {
-  using moe::aligned16;
-  moe::ForkArgs a;
-  const moe_status st = moe::cache_view(c, &a.c);
-  if (st != MOE_OK) return st;
-  if (n < 0) return MOE_ERR_INVALID_ARGUMENT;
-  if (n > moe::CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
-  if (n == 0) return MOE_OK;
-  if (!src_d || !dst_d || !ws_d) return MOE_ERR_INVALID_ARGUMENT;
-  if (!aligned16(src_d) || !aligned16(dst_d) || !aligned16(ws_d)) return MOE_ERR_MISALIGNED;
-  if (ws_bytes < attn_cache_fork_workspace_bytes(c, n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  a.src = src_d;
-  a.dst = dst_d;
-  a.n = n;
-  a.rows = static_cast<int32_t *>(ws_d);
-  a.seg = moe::ws_ptr<moe::ForkSeg>(ws_d, 64);
-  a.pages = moe::ws_ptr<int32_t>(ws_d, 64 + (size_t)n * sizeof(moe::ForkSeg));
-  const long long rows = (long long)n * (c->page_size / 2);  // half a page a fork on average
-  a.per_job = moe::layers_per_job(rows, c->n_layers);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool chain = moe::prof_chain(0);
-  cudaError_t e = n <= moe::PLAN_FEW
-                      ? moe::launch_dep(chain, moe::fork_plan_kernel<moe::PLAN_FEW>, dim3(1), dim3(moe::PLAN_FEW), 0, s, a)
-                      : moe::launch_dep(chain, moe::fork_plan_kernel<moe::PLAN_MANY>, dim3(1), dim3(moe::PLAN_MANY), 0, s,
-                                        a);
-  if (e != cudaSuccess) return moe::note_cuda_error(e);
-  const bool pdl = moe::prof_quiet(MOE_KERNEL_CACHE_COPY);
-  moe::prof_before(MOE_KERNEL_CACHE_COPY, s);
-  e = moe::launch_dep(pdl, moe::fork_copy_kernel, dim3(moe::copy_grid(rows, c->n_layers, a.per_job)),
-                      dim3(moe::COPY_THREADS), 0, s, a);
-  moe::prof_after(MOE_KERNEL_CACHE_COPY, s);
-  return moe::note_cuda_error(e);
+  moe::CacheView v;
+  const moe_status st = moe::cache_view(c, &v);
+  return st != MOE_OK ? st
+                      : moe::fork_call(v, src_d, dst_d, n, ws_d, ws_bytes, nullptr, nullptr, 0,
+                                       static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status attn_cache_trim(const attn_cache *c, const int32_t *slots_d, const int32_t *new_lens_d,
                                       int32_t n, void *stream) {
-  using moe::aligned16;
   moe::CacheView v;
   const moe_status st = moe::cache_view(c, &v);
-  if (st != MOE_OK) return st;
-  if (n < 0) return MOE_ERR_INVALID_ARGUMENT;
-  if (n > moe::CACHE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
-  if (n == 0) return MOE_OK;
-  if (!new_lens_d) return MOE_ERR_INVALID_ARGUMENT;
-  if (!aligned16(slots_d) || !aligned16(new_lens_d)) return MOE_ERR_MISALIGNED;
-  return moe::note_cuda_error(moe::launch_dep(moe::prof_chain(0), moe::trim_kernel, dim3(n), dim3(128), 0,
-                                              static_cast<cudaStream_t>(stream), v, slots_d, new_lens_d));
+  return st != MOE_OK ? st : moe::trim_call(v, slots_d, new_lens_d, n, static_cast<cudaStream_t>(stream));
 }

@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include "attn_join.cuh"
 #include "cache.cuh"
 #include "kernels.h"
 #include "tc.h"
@@ -46,7 +47,7 @@ namespace {
 
 constexpr int TR_MAXN = 256;      // nodes of a tree
 constexpr int TR_ROWS = 128;      // rows of a unit (MMA M)
-constexpr int TR_MAX_SMS = 160;   // SMs used at most (the workspace is sized for them)
+constexpr int TR_MAX_SMS = JOIN_MAX_CTAS / 2;  // SMs used at most (the workspace is sized for them)
 constexpr float TR_SLACK = 8.f;   // growth of the maximum (log2) that O is not rescaled for
 constexpr unsigned long long TR_TIMEOUT_NS = 1000000000ull;
 
@@ -91,25 +92,15 @@ struct TreeMaps {
   CUtensorMap k_new, v_new;  // {64, nodes, chunks}: boxes of a slot
 };
 
-// A CTA's split unit that starts with it, for the joining kernel.
-struct SplitDesc {
-  int32_t parts;   // CTAs it spans (0: none)
-  int32_t stride;  // from one of them to the next
-  int32_t rows, node0, head0, pad[3];
-};
-
 struct TreeArgs {
   CacheView c;
   const uint16_t *v_new;
   const int32_t *slots, *offsets, *parent;
   uint16_t *o;
-  SplitDesc *desc;  // [grid]
-  float *ml;        // [2 * grid][rows_cap][2]
-  float *part;      // [2 * grid][D / 4][rows_cap][4]
+  JoinArgs j;
   int B, n_nodes, max_nodes, Hq, Hkv, G;
   int nt;           // nodes of a unit
   int nt_mul, g_mul;  // 2^16 / nt + 1 and 2^16 / G + 1: x / nt = x nt_mul >> 16 for x < 2^9 (nt, G <= 128)
-  int rows_cap;     // nt * G
   int page_box;     // rows of a box (min(page, 64))
   float scale_log2;
 };
@@ -263,22 +254,6 @@ __device__ __forceinline__ void tr_drain(uint64_t *bar, uint32_t parity) {
     if (ptx::globaltimer() - t0 > TR_TIMEOUT_NS) return;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (FP16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-}
 template <bool FP16>
 __device__ __forceinline__ float value(uint32_t bits) {
   if constexpr (FP16)
@@ -314,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
       set_status(a.c.status, MOE_ERR_UNSUPPORTED);
-      a.desc[blockIdx.x].parts = 0;
+      a.j.desc[blockIdx.x].parts = 0;
     }
     return;
   }
@@ -417,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   before += (teams ? inc.team : inc.alone) - held;
   const int runs = (int)(T < (long long)(grid / size) ? T : (long long)(grid / size)), run = cta / size;
   if (run >= runs) {  // less to do than CTAs
-    if (tid == 0) a.desc[cta].parts = 0;
+    if (tid == 0) a.j.desc[cta].parts = 0;
     if (warp == C::LOADER + 1) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
@@ -522,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       ok = units == 0 || tr_wait_warp(&m->q_free, (units - 1) & 1u, m, status);
       if (!ok) break;
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.rows_cap * 128 * C::CHUNKS));
+        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.j.rows_cap * 128 * C::CHUNKS));
         for (int ch = 0; ch < C::CHUNKS; ++ch)
           ptx::tma_load_4d(smem + ch * C::Q_CHUNK, &maps.q, &m->q_full, 0, w.g * a.G, w.s.lo + w.node0(), ch);
       }
@@ -705,10 +680,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
               *reinterpret_cast<uint4 *>(out + d + i) = x;
             }
           } else {
-            uint4 *part = reinterpret_cast<uint4 *>(a.part) + (pslot * (D / 4) + d / 4) * a.rows_cap + r;
+            uint4 *part = reinterpret_cast<uint4 *>(a.j.part) + (pslot * (D / 4) + d / 4) * a.j.rows_cap + r;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              part[i * a.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              part[i * a.j.rows_cap] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         };
 #pragma unroll 1
@@ -724,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
           }
         }
         if (in && !whole && half == 0)
-          *reinterpret_cast<float2 *>(a.ml + (pslot * a.rows_cap + r) * 2) = make_float2(mx, sum);
+          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r) * 2) = make_float2(mx, sum);
       }
       ptx::tc_fence_before();
       arrive(&m->o_free);
@@ -908,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
       }
       ld += 2 * C::PARTS * un.n;
     }
-    if (tid == 0) a.desc[cta] = split;
+    if (tid == 0) a.j.desc[cta] = split;
   }
 
   ptx::tc_fence_before();
@@ -916,148 +891,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
   if (warp == C::LOADER + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM);
-  }
-}
-
-// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
-// unit.  A thread has sixteen values of one row (rows run fastest, in the
-// parts as in the threads, so that a warp reads whole lines); up to eight
-// groups of a block's threads share the parts of the same values (a unit is
-// split over as few as two CTAs and as many as all of them).
-constexpr int TJ_THREADS = 256;
-
-// (One group always, this rule, eight always, whole calls in us: 1 node over 3,000
-// positions 17.4, 14.8, 14.4; 4 x 5 over 9,000 29.8, 25.0, 24.3; 24 x 5 over 6,000
-// 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.)
-__device__ __forceinline__ int part_groups(int parts) { return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8; }
-
-template <int D, bool FP16>
-__global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
-  constexpr int MAXU = 2 * TR_MAX_SMS, WARPS = TJ_THREADS / 32;  // MAXU: split units at most
-  __shared__ SplitDesc desc_s[MAXU];
-  __shared__ int cta_s[MAXU], item_s[MAXU + 1], wsum[WARPS];
-  __shared__ float4 acc_s[4][TJ_THREADS];
-  __shared__ float2 ml_s[TJ_THREADS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the split units in the CTAs' order, and the items (blocks of cells of sixteen values) before each
-  const int cells = D / 16 * a.rows_cap;
-  constexpr int PER = (MAXU + TJ_THREADS - 1) / TJ_THREADS;
-  SplitDesc d[PER];
-  auto items_of = [&](const SplitDesc &x) {
-    const int each = TJ_THREADS / part_groups(x.parts);
-    return (cells + each - 1) / each;
-  };
-  int packed = 0;  // units << 20 | items: at most 320, and 320 * 16 * 128 / 32 below 2^15 of them
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = tid * PER + i;
-    d[i].parts = 0;
-    if (c < ctas) d[i] = a.desc[c];
-    if (d[i].parts > 0) packed += 1 << 20 | items_of(d[i]);
-  }
-  int before = packed, all = 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += t;
-  }
-  if (lane == 31) wsum[warp] = before;
-  before -= packed;
-  __syncthreads();
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += wsum[w];
-    all += wsum[w];
-  }
-  const int units = all >> 20, n_items = all & 0xFFFFF;
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (d[i].parts > 0) {
-      const int u = before >> 20;
-      desc_s[u] = d[i];
-      cta_s[u] = tid * PER + i;
-      item_s[u] = before & 0xFFFFF;
-      before += 1 << 20 | items_of(d[i]);
-    }
-  if (tid == 0) item_s[units] = n_items;
-  __syncthreads();
-
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    int u = 0;  // the last unit whose first item is at or before this one
-#pragma unroll
-    for (int step = 256; step; step >>= 1)
-      if (u + step < units && item_s[u + step] <= item) u += step;
-    const SplitDesc ds = desc_s[u];
-    const int c0 = cta_s[u], groups = part_groups(ds.parts), each = TJ_THREADS / groups, grp = tid / each;
-    const int e = (item - item_s[u]) * each + tid % each, c4 = e / a.rows_cap * 4, r = e % a.rows_cap;
-    const bool in = e < cells && r < ds.rows;
-    float M = -INFINITY, den = 0.f;
-    float4 acc[4] = {};
-    // A part in which the row saw nothing has the sum 0.  Its maximum does not
-    // tell: that is -infinity as well where every score is NaN (a maximum passes
-    // over NaN), and such a part, whose sum is NaN, makes the row NaN.
-    auto add = [&](float2 ml, const float4 (&v)[4]) {
-      if (ml.y == 0.f) return;
-      const float mn = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : ex2(M - mn), h = ex2(ml.x - mn);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[q].x = fmaf(v[q].x, h, acc[q].x * f);
-        acc[q].y = fmaf(v[q].y, h, acc[q].y * f);
-        acc[q].z = fmaf(v[q].z, h, acc[q].z * f);
-        acc[q].w = fmaf(v[q].w, h, acc[q].w * f);
-      }
-      den = fmaf(ml.y, h, den * f);
-      M = mn;
-    };
-    if (in) {
-      // part 0 lies in its CTA's second slot, the others in their CTAs' first
-      for (int i0 = grp; i0 < ds.parts; i0 += 2 * groups) {
-        float2 ml[2];
-        float4 v[2][4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int i = i0 + k * groups;
-          ml[k] = make_float2(-INFINITY, 0.f);
-          if (i < ds.parts) {
-            const size_t p = (size_t)2 * (c0 + i * ds.stride) + (i == 0 ? 1 : 0);
-            ml[k] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
-            const float4 *src = reinterpret_cast<const float4 *>(a.part) + (p * (D / 4) + c4) * a.rows_cap + r;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[k][q] = src[q * a.rows_cap];
-          }
-        }
-        add(ml[0], v[0]);
-        add(ml[1], v[1]);
-      }
-    }
-    if (groups > 1) {
-      __syncthreads();  // the last item's readers are done
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc_s[q][tid] = acc[q];
-      ml_s[tid] = make_float2(M, den);
-      __syncthreads();
-      if (grp == 0 && in)
-        for (int g = 1; g < groups; ++g) {
-          float4 v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc_s[q][g * each + tid];
-          add(ml_s[g * each + tid], v);
-        }
-    }
-    if (in && grp == 0) {
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      const int node = ds.node0 + r / a.G, head = ds.head0 + r % a.G;
-      uint4 *out = reinterpret_cast<uint4 *>(a.o + ((size_t)node * a.Hq + head) * D + c4 * 4);
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        uint4 x;
-        x.x = pack2<FP16>(acc[q].x * inv, acc[q].y * inv);
-        x.y = pack2<FP16>(acc[q].z * inv, acc[q].w * inv);
-        x.z = pack2<FP16>(acc[q + 1].x * inv, acc[q + 1].y * inv);
-        x.w = pack2<FP16>(acc[q + 1].z * inv, acc[q + 1].w * inv);
-        out[q / 2] = x;
-      }
-    }
   }
 }
 
@@ -1112,7 +945,7 @@ cudaError_t launch_tree(const TreeMaps &maps, const TreeArgs &a, int ctas, cudaS
   e = launch_dep(chain, tree_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
   prof_after(MOE_KERNEL_ATTN_TREE, s);
   if (e != cudaSuccess) return e;
-  return launch_dep(quiet, tree_join_kernel<D, FP16>, dim3(ctas * 2 / C::CTAS), dim3(TJ_THREADS), 0, s, a, ctas);
+  return launch_dep(quiet, join_kernel<D, FP16>, dim3(ctas * 2 / C::CTAS), dim3(JOIN_THREADS), 0, s, a.j, ctas);
 }
 
 template <bool FP16>
@@ -1181,16 +1014,19 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.Hkv = c->n_kv_heads;
   a.G = G;
   a.nt = moe::unit_nodes(G, max_nodes);
-  a.rows_cap = a.nt * G;
+  a.j.rows_cap = a.nt * G;
   a.nt_mul = 65536 / a.nt + 1;
   a.g_mul = 65536 / G + 1;
   a.page_box = c->page_size < 64 ? c->page_size : 64;
   a.scale_log2 = scale * 1.4426950408889634f;
   size_t ml_at, part_at;
-  moe::tree_ws(D, ctas, a.rows_cap, &ml_at, &part_at);
-  a.desc = static_cast<moe::SplitDesc *>(ws_d);
-  a.ml = moe::ws_ptr<float>(ws_d, ml_at);
-  a.part = moe::ws_ptr<float>(ws_d, part_at);
+  moe::tree_ws(D, ctas, a.j.rows_cap, &ml_at, &part_at);
+  a.j.o = a.o;
+  a.j.Hq = Hq;
+  a.j.G = G;
+  a.j.desc = static_cast<moe::SplitDesc *>(ws_d);
+  a.j.ml = moe::ws_ptr<float>(ws_d, ml_at);
+  a.j.part = moe::ws_ptr<float>(ws_d, part_at);
   const int64_t pool_rows = (int64_t)c->n_pages * c->page_size;
   const uint16_t *k = a.c.k + (size_t)layer * pool_rows * a.c.row, *v = a.c.v + (size_t)layer * pool_rows * a.c.row;
   const bool wide = D == 256;  // K tiles of two column spans
