@@ -69,6 +69,7 @@ MOE_KERNEL_ATTN_DECODE = 13
 MOE_KERNEL_ATTN_TREE = 14
 MOE_KERNEL_DRAFT_VERIFY = 15
 MOE_KERNEL_CACHE_COPY = 16
+MOE_KERNEL_ATTN_QCACHE = 17
 
 
 class MoeError(RuntimeError):

@@ -18,7 +18,7 @@ thread_local int32_t g_last_launches = 0;
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 
 // Profiling hook state, per kernel id (moe_profile_events), per thread.
-constexpr int kProfKernels = MOE_KERNEL_CACHE_COPY + 1;
+constexpr int kProfKernels = MOE_KERNEL_ATTN_QCACHE + 1;
 struct ProfState {
   int n = 0;
   int stride = 1;                   // bracket every stride-th launch

@@ -295,7 +295,8 @@ typedef enum {
   MOE_KERNEL_ATTN_DECODE = 13,   /* decode attention, per-block pass (attn.h)  */
   MOE_KERNEL_ATTN_TREE = 14,     /* tree attention over pages (tree.h)         */
   MOE_KERNEL_DRAFT_VERIFY = 15,  /* verification of drafts (tree.h)            */
-  MOE_KERNEL_CACHE_COPY = 16     /* rows of an append or a fork (cache.h)      */
+  MOE_KERNEL_CACHE_COPY = 16,    /* rows of an append or a fork (cache.h)      */
+  MOE_KERNEL_ATTN_QCACHE = 17    /* attention over the 8-bit cache (qcache.h)  */
 } moe_kernel;
 
 /* Profiling hook (one per kernel).  From now on, on the calling thread, the
