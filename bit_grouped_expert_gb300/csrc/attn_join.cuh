@@ -5,7 +5,6 @@
 #include "common.cuh"
 
 namespace moe {
-namespace {
 
 constexpr int JOIN_MAX_CTAS = 320;  // of the kernel before: two for each of 160 SMs at most
 
@@ -24,6 +23,8 @@ struct JoinArgs {
   int rows_cap;     // rows of a unit at most
   int Hq, G;        // query heads, and of a KV head
 };
+
+namespace {
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

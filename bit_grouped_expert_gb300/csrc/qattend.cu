@@ -4,17 +4,19 @@
 // rows of one matrix (row = token * G + head), so that a K or V tile read once
 // serves all of them.  The codes are matrix operands as they lie in the pages:
 // per tile of 128 positions
-//   S[128 rows x 128] = (Qh + Ql) . K^T    tcgen05 (e4m3), K in shared memory
-//   P = 2^(S scales - m)                   two threads a row, running maximum m and sum l
-//   O[128 rows x D]  += (Ph + Pl) . V      tcgen05 (e4m3), P in tensor memory, V in shared memory
+//   S[128 rows x 128] = (Qh + Ql) . K^T          tcgen05 (e4m3), K in shared memory
+//   P = 2^(S scales - m)                         two threads a row, running maximum m and sum l
+//   O[128 rows x D]  += (Ph + Pm + Pl) . V       tcgen05 (e5m2 x e4m3), P in tensor memory, V in shared memory
 // An MMA over 8-bit values runs twice as fast as one over 16-bit ones, so that
-// two of them, of a factor's upper and lower part, take as long as one:
+// factors may be sums of 8-bit parts:
 //   q times a power of two that takes its row's largest value to 224 .. 448 is
-//   Qh, its nearest e4m3, and Ql, the nearest e4m3 of the rest: 9 bits of every value
-//   and no less than 2^-10, 2^-18 of the row's largest (bf16's 8 bits are kept whole
-//   but for values below 2^-10 of the largest; of fp16's 11 two go);
-//   the weights P, at most 2^8.75, are cut the same way: off by 2^-8 of themselves or
-//   2^-10, that is 2^-17 of the weight at the running maximum, at most.
+//   Qh, its nearest e4m3, and Ql, the nearest e4m3 of the rest: to 2^-8 of every value
+//   or 2^-10, 2^-18 of the row's largest (bf16's 8 bits are kept whole but for values
+//   below 2^-10 of the largest; of fp16's 11 the last ones go);
+//   the weights P are three e5m2 parts, to 2^-9 of each or 2^-23 of the one at the
+//   running maximum.  (Two e4m3 parts keep as much of the large ones, but their range is
+//   small: O had to be rescaled wherever a maximum grew by more than 2^1.75, most
+//   tiles of 32 rows.)
 // A page's K scale multiplies its columns of S, its V scale its columns of P, taken
 // relative to the largest V scale so far, so that O stays one sum of one unit.
 //
@@ -26,8 +28,7 @@
 // Roles: eight warps own the rows, one loads (TMA: pages by the table's numbers,
 // K one tile ahead of V, into a ring, and the pages' scales), two issue the MMAs
 // of S (of the next tile during the softmax of this one) and of O, four cut the
-// next unit's queries.  Rescaling O on a new maximum is put off while the maximum
-// grows by less than 2^1.75.  Who waits on a barrier's parity must know that the phase
+// next unit's queries.  Who waits on a barrier's parity must know that the phase
 // before has passed: the comments at the waits say from what.
 //
 // Every wait is bounded: after one second the kernel records
@@ -35,23 +36,10 @@
 // and exits.
 #include <math.h>
 
-#include "attn_join.cuh"
-#include "kernels.h"
-#include "qcache.cuh"
-#include "rotary.cuh"
-#include "tc.h"
-#include "tc_ptx.cuh"
+#include "qattend.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int QT_ROWS = 128;      // rows of a unit (MMA M)
-constexpr int QT_TILE = 128;      // positions of a tile
-constexpr int QT_GROUP = 16;      // positions that share scales at least (the smallest page)
-constexpr int QT_MAX_SMS = JOIN_MAX_CTAS / 2;
-constexpr float QT_TOP = 7.f;     // a weight at the running maximum is 2^7
-constexpr float QT_SLACK = 1.75f; // growth of the maximum (log2) that O is not rescaled for: 2^8.75 < 448
-constexpr unsigned long long QT_TIMEOUT_NS = 1000000000ull;
 
 template <int D>
 struct QCfg {
@@ -66,55 +54,24 @@ struct QCfg {
   // Slots of the scales' ring.  The loader stores tile x's when it has issued the
   // load 2 x at least, so that the load 2 x - NS has been used up.  That is, NS = 5: K of
   // tile x - 2 or V of x - 3; 10: V of x - 6 or K of x - 5; 16: V of x - 9 or K of x - 8.  A K used up says
-  // that all row warps have begun the tile before it: they are past the scales
-  // of x - 4, x - 7, x - 10.
+  // that the product with V of two tiles before is done: the row warps are past the
+  // scales of x - 4, x - 7, x - 10.
   static constexpr int SCALES = NS == 5 ? 4 : NS == 10 ? 8 : 16;
   static constexpr int OFF_RING = 2 * Q_PART;
   static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
   static constexpr int SMEM = OFF_MISC + (D == 256 ? 3 : 4) * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  // Tensor memory columns: O, one S tile, two P tiles of two parts (four weights a column).
-  static constexpr uint32_t S_COL = D, P_COL = D + QT_TILE, P_PART = QT_TILE / 4, TMEM = 512;
-  static_assert(P_COL + 4 * P_PART <= TMEM, "tensor memory");
+  // Tensor memory columns: O, two S tiles; a tile's P, three parts of four weights a
+  // column, goes where its S was.
+  static constexpr uint32_t S_COL = D, P_PART = QT_TILE / 4, TMEM = 512;
+  static_assert(S_COL + 2 * QT_TILE <= TMEM && 3 * P_PART <= QT_TILE, "tensor memory");
 };
 
-struct QMaps {
-  CUtensorMap k, v;  // {ROWB, pool rows, heads * CHUNKS} bytes: boxes of one page's rows
-};
-
-struct AttendArgs {
-  QCacheView q;
-  const float *ks, *vs;  // the layer's scales
-  const uint16_t *x;
-  const int32_t *slots, *offsets;
-  uint16_t *o;
-  JoinArgs j;
-  int B, n_rows, max_rows, Hq, Hkv, G;
-  int nt;           // tokens of a unit
-  int g_mul;        // 2^16 / G + 1: x / G = x g_mul >> 16 for x < 2^8 (G <= 128)
-  int page_box;     // rows of a box (min(page, 128))
-  const uint8_t *v_layer;
-  float scale_log2;
-};
-
-struct QSeq {
-  int slot, L, lo, n;  // n == 0: nothing to do
-};
-
-struct QShared {  // what every wait looks at
-  int abort_flag;
-};
 template <typename C>
-struct QMisc : QShared {
-  uint64_t full[C::NS], empty[C::NS], sc_full[C::SCALES];
-  uint64_t q_full, q_free, s_full, s_free, p_ready[2], pv_done[2], o_free, pair_bar[4], final_bar;
-  uint32_t tmem;
-  int nonfinite[2];                // by the unit's parity: that unit, if NaN was taken out of its V
-  int b0;
-  QSeq s0;
-  long long off0;
-  int8_t q_exp[2][QT_ROWS];        // by the unit's parity
-  float scales[C::SCALES][2][8];   // of a tile's groups: K, V
+struct QMisc : QRing<C> {
+  uint64_t s_full[2], pair_bar[4];
+  int nonfinite[4];                // by the unit's number: that unit, if NaN was taken out of its V
+  int8_t q_exp[3][QT_ROWS];        // by the unit's number (its scores run when the product with V of two tiles before is done)
   union {
     long long wsum[C::WARPS];
     float row[2][2][QT_ROWS];      // later: what the two threads of a row exchange, [turn][half]
@@ -123,142 +80,6 @@ struct QMisc : QShared {
 static_assert(sizeof(QMisc<QCfg<256>>) <= 3 * 1024 && sizeof(QMisc<QCfg<128>>) <= 4 * 1024 &&
                   sizeof(QMisc<QCfg<64>>) <= 4 * 1024,
               "misc area");
-
-__device__ __forceinline__ QSeq q_load_seq(const AttendArgs &a, int b) {
-  const CacheView &c = a.q.c;
-  QSeq s;
-  s.slot = a.slots ? a.slots[b] : b;
-  s.lo = a.offsets[b];
-  const int hi = a.offsets[b + 1];
-  const bool in = s.slot >= 0 && s.slot < c.n_slots;
-  s.L = in ? slot_len(c, s.slot) : -1;
-  s.n = hi - s.lo;
-  if (s.L < 0 || s.lo < 0 || hi < s.lo || s.n > a.max_rows || hi > a.n_rows) {
-    set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
-    s.n = s.L = s.lo = 0;
-  }
-  return s;
-}
-
-// Positions that row tile rt's last row sees (none where that row is padding), and their tiles (one at least).
-__device__ __forceinline__ int sees_of(const AttendArgs &a, const QSeq &s, int rt) {
-  return max(0, s.L - s.n + min(s.n, (rt + 1) * a.nt));
-}
-__device__ __forceinline__ int tiles_of(const AttendArgs &a, const QSeq &s, int rt) {
-  return max(1, (sees_of(a, s, rt) + QT_TILE - 1) / QT_TILE);
-}
-__device__ __forceinline__ int row_tiles(const AttendArgs &a, const QSeq &s) { return (s.n + a.nt - 1) / a.nt; }
-// The count of a sequence's units, of one KV head.
-template <typename C>
-__device__ __forceinline__ long long head_count(const AttendArgs &a, const QSeq &s) {
-  long long t = 0;
-  for (int rt = 0, rts = row_tiles(a, s); rt < rts; ++rt) t += C::OVERHEAD + tiles_of(a, s, rt);
-  return t;
-}
-
-__device__ __noinline__ long long q_div_long(long long p, long long z) { return p / z; }
-__device__ __forceinline__ long long q_mul_div(long long x, int y, long long z) {
-  const long long p = x * y;
-  return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : q_div_long(p, z);
-}
-
-// A CTA's walk over the units of its run, in the order sequence, KV head, row
-// tile.  A unit counts OVH + its tiles, the overhead first.
-template <typename C>
-struct QWalk {
-  static constexpr int OVH = C::OVERHEAD;
-  const AttendArgs &a;
-  int b;
-  long long left;  // of the run, still to come
-  QSeq s;
-  int g, rt, off;  // unit, and where in its count the run's part begins
-  int nt_all;      // tiles of the unit
-  int t0, n;       // this CTA's: the first, and how many
-  bool fresh;
-
-  __device__ QWalk(const AttendArgs &a_, int b0, const QSeq &s0, long long off0, long long count)
-      : a(a_), b(b0), left(count), s(s0), rt(0), fresh(true) {
-    const long long each = head_count<C>(a, s);
-    g = (int)q_mul_div(off0, 1, each);
-    off0 -= g * each;
-    while (off0 >= OVH + (nt_all = tiles_of(a, s, rt))) {
-      off0 -= OVH + nt_all;
-      ++rt;
-    }
-    off = (int)off0;
-  }
-  // the next unit with tiles for this CTA; false when the run is done
-  __device__ bool next() {
-    while (left > 0) {
-      if (!fresh) {
-        off = 0;
-        if (++rt * a.nt >= s.n) {
-          rt = 0;
-          if (++g >= a.Hkv) {
-            g = 0;
-            do {  // left > 0: a later sequence has tiles
-              s = q_load_seq(a, ++b);
-            } while (s.n == 0 && b + 1 < a.B);
-            if (s.n == 0) return false;
-          }
-        }
-        nt_all = tiles_of(a, s, rt);
-      }
-      fresh = false;
-      const int take = (int)(left < OVH + nt_all - off ? left : (long long)(OVH + nt_all - off));
-      left -= take;
-      t0 = max(0, off - OVH);
-      n = max(0, off + take - OVH) - t0;
-      if (n > 0) return true;
-    }
-    return false;
-  }
-  __device__ int token0() const { return rt * a.nt; }
-  __device__ int tokens() const { return min(a.nt, s.n - rt * a.nt); }
-};
-
-__device__ __forceinline__ bool q_wait(uint64_t *bar, uint32_t parity, QShared *m, int32_t *status) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer();
-  uint32_t n = 0;
-  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000u)) {
-    if ((++n & 7u) == 0) {
-      if (*reinterpret_cast<volatile int *>(&m->abort_flag)) return false;
-      if (ptx::globaltimer() - t0 > QT_TIMEOUT_NS) {
-        *reinterpret_cast<volatile int *>(&m->abort_flag) = 1;
-        set_status(status, MOE_ERR_DEVICE_TIMEOUT);
-        return false;
-      }
-    }
-  }
-  return true;
-}
-// The same for a whole warp: one answer for all lanes, and the lanes together again.
-__device__ __forceinline__ bool q_wait_warp(uint64_t *bar, uint32_t parity, QShared *m, int32_t *status) {
-  return __all_sync(0xffffffffu, q_wait(bar, parity, m, status));
-}
-// Bounded wait used while draining after an abort.
-__device__ __forceinline__ void q_drain(uint64_t *bar, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if (ptx::globaltimer() - t0 > QT_TIMEOUT_NS) return;
-}
-
-// Position of K(j) / V(j) of a unit of n tiles in the ring's load order K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ uint32_t k_at(int j) { return j == 0 ? 0u : 2u * j - 1u; }
-__device__ __forceinline__ uint32_t v_at(int j, int n) { return j == n - 1 ? 2u * n - 1u : 2u * j + 2u; }
-
-// Two values as their nearest codes (hi) and the rests' (lo).
-__device__ __forceinline__ void cut(float x, float y, uint32_t &hi, uint32_t &lo) {
-  hi = to_codes(x, y);
-  const float2 got = from_codes(hi);
-  lo = to_codes(x - got.x, y - got.y);
-}
-
-// A code that is NaN among the four of a word: 0x7F or 0xFF.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0x80 in every such byte
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
@@ -294,7 +115,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     ptx::fence_mbar_init();
   } else if (tid == 64) {
     m->abort_flag = 0;
-    m->nonfinite[0] = m->nonfinite[1] = -1;
+    for (int i = 0; i < 4; ++i) m->nonfinite[i] = -1;
     ptx::mbar_init(&m->q_full, C::QUERY_WARPS);
     ptx::mbar_init(&m->q_free, 1);
     ptx::mbar_init(&m->final_bar, 2);
@@ -303,9 +124,8 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&m->p_ready[i], C::ROW_WARPS);
       ptx::mbar_init(&m->pv_done[i], 1);
+      ptx::mbar_init(&m->s_full[i], 1);
     }
-    ptx::mbar_init(&m->s_full, 1);
-    ptx::mbar_init(&m->s_free, C::ROW_WARPS);
     ptx::mbar_init(&m->o_free, C::ROW_WARPS);
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&m->pair_bar[i], 2);
     ptx::fence_mbar_init();
@@ -313,141 +133,34 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
   // what the kernel before writes (lengths, tables, codes, scales, queries) from here on,
   // by ordinary loads: a read-only one may look at what was there before
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // This CTA's run: every thread adds up some sequences' units, a scan gives
-  // their places, and the thread whose sequences hold the run's start writes
-  // down where that is.
-  const int per = (a.B + C::THREADS - 1) / C::THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
-  QSeq seq{0, 0, 0, 0};
-  long long held = 0;
-  for (int b = sb; b < se; ++b) {
-    seq = q_load_seq(a, b);
-    held += a.Hkv * head_count<C>(a, seq);
-  }
-  long long inc = held;
-#pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
-  }
-  if (lane == 31) m->wsum[warp] = inc;
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
+  long long end, T;
+  int runs;
+  const long long count = find_run<C>(a, m, end, T, runs);
   const uint32_t tmem = m->tmem;
-  long long before = inc - held, T = 0;
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += m->wsum[w];
-    T += m->wsum[w];
-  }
-  const int grid = gridDim.x, cta = blockIdx.x;
-  const int runs = (int)(T < (long long)grid ? T : (long long)grid);
-  if (cta >= runs) {  // less to do than CTAs
+  const int cta = blockIdx.x;
+  if (count == 0) {  // less to do than CTAs
     if (tid == 0) a.j.desc[cta].parts = 0;
     if (warp == C::ISSUE_S) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
-  const long long first = q_mul_div(T, cta, runs), end = q_mul_div(T, cta + 1, runs);
-  if (first >= before && first < before + held) {
-    long long at = before;
-    int b = sb;
-    if (per > 1)
-      for (;; ++b) {
-        seq = q_load_seq(a, b);
-        const long long t = a.Hkv * head_count<C>(a, seq);
-        if (first < at + t) break;
-        at += t;
-      }
-    m->b0 = b;
-    m->s0 = seq;
-    m->off0 = first - at;
-  }
-  __syncthreads();
-  QWalk<C> w(a, m->b0, m->s0, m->off0, end - first);
+  QWalk<C> w(a, m->b0, m->s0, m->off0, count);
   uint8_t *ring = smem + C::OFF_RING;
   int32_t *status = c.status;
 
   if (warp == C::LOADER) {
-    // ---------------------------------------------------------------- loads
-    const int pool_rows = c.n_pages << c.page_shift, in_page = (1 << c.page_shift) - 1;
-    const int boxes = QT_TILE / a.page_box;
-    const bool whole = boxes == 1;  // a page holds a tile's rows: one box
-    const int box = whole ? 0 : lane / C::CHUNKS, span = whole ? 0 : lane % C::CHUNKS;
-    const bool issues = whole ? lane == 0 : lane < boxes * C::CHUNKS;
-    const int box_at = span * C::SPAN + box * a.page_box * C::ROWB;
-    uint32_t ld = 0, tiles = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      const int z = w.g * C::CHUNKS, blocks = pages_of(sees_of(a, w.s, w.rt), c.page_shift);
-      const int32_t *table = c.table + (size_t)w.s.slot * c.max_pages;
-      int eb = -64, ent = 0;  // 32 table entries from block eb on, one a lane
-      // the page of position `pos`, lane by lane, all of them in the tile that
-      // begins at `base`; -1 where there is none
-      auto page_at = [&](int base, int pos) {
-        constexpr int MOST = QT_TILE / QT_GROUP;  // blocks of a tile at most; the tile before stays in view
-        const int blk0 = base >> c.page_shift;
-        if (blk0 < eb || blk0 + MOST > eb + 32) {
-          eb = max(0, blk0 - MOST);
-          ent = eb + lane < blocks ? table[eb + lane] : -1;
-          if (eb + lane < blocks && (unsigned)ent >= (unsigned)c.n_pages) {
-            set_status(status, MOE_ERR_DEVICE_BOUNDS);
-            ent = -1;
-          }
-        }
-        return __shfl_sync(0xffffffffu, ent, ((pos >> c.page_shift) - eb) & 31);
-      };
-      auto load = [&](const CUtensorMap *map, int t) {
-        const uint32_t slot = ld % C::NS;
-        if (!q_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, status)) return false;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&m->full[slot], C::SLOT);
-        __syncwarp();
-        const int pos = t * QT_TILE + box * a.page_box, page = page_at(t * QT_TILE, pos);
-        // (past the pool, read as zeros, where there is no page)
-        if (issues)
-          ptx::tma_load_3d(ring + slot * C::SLOT + box_at, map, &m->full[slot], 0,
-                           page < 0 ? pool_rows : (page << c.page_shift) + (pos & in_page), z + span);
-        ++ld;
-        return true;
-      };
-      // A tile's scales: a lane a group, K's in the first eight lanes, V's in the next; zero where there is no page.
-      float sc = 0.f;
-      auto fetch_scales = [&](int t) {
-        const int page = page_at(t * QT_TILE, t * QT_TILE + (lane & 7) * QT_GROUP);
-        sc = 0.f;
-        if (lane < 16 && page >= 0) sc = (lane < 8 ? a.ks : a.vs)[(size_t)page * a.Hkv + w.g];
-      };
-      auto store_scales = [&]() {
-        const uint32_t at = tiles++ % C::SCALES;
-        if (lane < 16) m->scales[at][lane >> 3][lane & 7] = sc;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&m->sc_full[at]);
-      };
-      fetch_scales(w.t0);
-      ok = load(&maps.k, w.t0);
-      if (ok) store_scales();
-      for (int j = 0; ok && j < w.n; ++j) {
-        if (j + 1 < w.n) {
-          fetch_scales(w.t0 + j + 1);
-          ok = load(&maps.k, w.t0 + j + 1);
-        }
-        ok = ok && load(&maps.v, w.t0 + j);
-        if (ok && j + 1 < w.n) store_scales();  // (loaded meanwhile)
-      }
-    }
-    if (!ok && lane == 0)  // loads of the last slots may still be in flight
-      for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
-        q_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
+    load_tiles<C>(maps, a, m, w, ring);
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
-    const uint32_t id_s = ptx::idesc_e4m3(QT_TILE, false), id_o = ptx::idesc_e4m3(D, true);
+    const uint32_t id_s = ptx::idesc_f8(QT_TILE, false, false, false, false), id_o = ptx::idesc_f8(D, true, false, false, true);
     const uint64_t qd = ptx::sdesc_rows(ptx::smem_u32(smem), C::ROWB, 16);
     uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
-    auto scores = [&](uint32_t pos, uint32_t t, bool first) {  // S of running tile t from the K tile at load `pos`
+    auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
       const uint32_t slot = pos % C::NS;
-      if (t >= 1 && !q_wait_warp(&m->s_free, (t - 1) & 1u, m, status)) return false;
-      // (a unit's first slots may follow the last unit's V of tile t - 2)
-      if (first && t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+      // P of tile t - 2 has been used up.  (So what the slot held before has been loaded:
+      // a K, which was waited for here, or a V of tile t - 3 or before.)
+      if (t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
       if (!q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
       ptx::tc_fence_after();
       const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, 16);
@@ -458,10 +171,10 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           for (int ch = 0; ch < C::CHUNKS; ++ch)
 #pragma unroll
             for (int i = 0; i < C::ROWB / 32; ++i)
-              ptx::mma_ss_e4m3(tmem + C::S_COL, qd + (part * C::Q_PART + ch * C::Q_SPAN + i * 32) / 16,
+              ptx::mma_ss_f8(tmem + C::S_COL + (t & 1) * QT_TILE, qd + (part * C::Q_PART + ch * C::Q_SPAN + i * 32) / 16,
                                kd + (ch * C::SPAN + i * 32) / 16, id_s, (part | ch | i) != 0);
         ptx::mma_commit(&m->empty[slot]);
-        ptx::mma_commit(&m->s_full);
+        ptx::mma_commit(&m->s_full[t & 1]);
       }
       __syncwarp();
       return true;
@@ -473,14 +186,14 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           !q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
-      const uint32_t p_col = tmem + C::P_COL + (t & 1) * 2 * C::P_PART;
+      const uint32_t p_col = tmem + C::S_COL + (t & 1) * QT_TILE;
       const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, C::SPAN);
       if (ptx::elect_one()) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int i = 0; i < QT_TILE / 32; ++i)
-            ptx::mma_ts_e4m3(tmem, p_col + part * C::P_PART + 8 * i, vd + i * 32 * C::ROWB / 16, id_o,
+            ptx::mma_ts_f8(tmem, p_col + part * C::P_PART + 8 * i, vd + i * 32 * C::ROWB / 16, id_o,
                              !first || part > 0 || i > 0);
         ptx::mma_commit(&m->empty[slot]);
         ptx::mma_commit(&m->pv_done[t & 1]);
@@ -489,10 +202,10 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       return true;
     };
     while (ok && w.next()) {
-      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_at(0), jj, true);
+      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_at(0), jj);
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
         if (does_s) {
-          if (j + 1 < w.n) ok = scores(ld + k_at(j + 1), jj + 1, false);
+          if (j + 1 < w.n) ok = scores(ld + k_at(j + 1), jj + 1);
           // the unit's last scores are under way
           if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
           __syncwarp();
@@ -533,30 +246,15 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           const int r = r0 + u * C::QUERY_WARPS * AT_ONCE;
           float f[8];
           unpack8<FP16>(x[u], f);
-          float most = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (fabsf(f[i]) < INFINITY) most = fmaxf(most, fabsf(f[i]));
-#pragma unroll
-          for (int o = 1; o < LANES; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          const int e = scale_exp(most);
-          const float back = exp2_int(-e);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v[2] = {f[2 * i] * back, f[2 * i + 1] * back};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (!(fabsf(v[k]) < INFINITY)) v[k] = NAN;  // (its rest is NaN as well)
-            cut(v[0], v[1], hi[i], lo[i]);
-          }
+          uint2 part[2];
+          const int e = cut_row<LANES, 2>(f, part);
           if (r < rows) {
             uint32_t off = r * C::ROWB + d % C::ROWB;
             off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
             uint8_t *to = smem + d / C::ROWB * C::Q_SPAN + off;
-            *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2 *>(to + C::Q_PART) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (d == 0) m->q_exp[units & 1][r] = (int8_t)e;
+            *reinterpret_cast<uint2 *>(to) = part[0];
+            *reinterpret_cast<uint2 *>(to + C::Q_PART) = part[1];
+            if (d == 0) m->q_exp[units % 3][r] = (int8_t)e;
           }
         }
       }
@@ -611,7 +309,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         split = SplitDesc{(int)q_mul_div(u1 * runs + T - 1, 1, T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
-      const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 1]) == units - 1;
+      const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
       const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
       const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
       if (fix) {  // NaN into O, apart from the usual way out: codes that were taken out of the edge's tiles
@@ -694,53 +392,32 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       for (int j = 0; j < un.n; ++j, ++jj) {
         const int t = un.t0 + j;
         const bool edge = (t + 1) * QT_TILE > un.all_see;
-        if (!(ok = q_wait_warp(&m->s_full, jj & 1u, m, status))) break;
-        // Every row warp, with rows or without, is at most two tiles ahead of O: the P
-        // tile of jj is free then, and no wait below or in the other roles can take
-        // a phase of its barrier for the one two before.
-        if (jj >= 2 && !(ok = q_wait_warp(&m->pv_done[jj & 1], ((jj - 2) >> 1) & 1u, m, status))) break;
-        // (this warp has waited for the slot's phase before, SCALES tiles ago)
-        if (!(ok = q_wait_warp(&m->sc_full[jj % C::SCALES], (jj / C::SCALES) & 1u, m, status))) break;
+        // The scores are there (and so the product with V of two tiles before is done, and no
+        // wait below or in the other roles can take a phase of its barrier for the one two
+        // before); the scales are there (this warp has waited for the slot's phase before, SCALES tiles ago).
+        if (!(ok = q_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, &m->sc_full[jj % C::SCALES], (jj / C::SCALES) & 1u,
+                               &m->s_full[jj & 1], (jj >> 1) & 1u, m, status)))
+          break;
         ptx::tc_fence_after();
         if (edge) {
-          // V rows that no row sees become zeros (0 x NaN is NaN), and among those
-          // that only some see the code NaN as well: finish() puts it where it belongs
+          // (codes NaN that are taken out: finish() puts them where they belong)
           const uint32_t pos = ld + v_at(j, un.n), slot = pos % C::NS;
           // the slots' last loads have been used up (else their barriers could still be a phase behind)
           if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
           ok = ok && q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status);
           if (!ok) break;
-          constexpr int PIECES = C::ROWB / 16;  // of a row in a span
-          for (int e = tid; e < QT_TILE * C::CHUNKS * PIECES; e += QT_ROWS * 2) {
-            const int q = e / PIECES % QT_TILE, at = t * QT_TILE + q;
-            if (at < un.all_see) continue;
-            uint4 *piece = reinterpret_cast<uint4 *>(ring + slot * C::SLOT + e * 16);
-            if (at >= un.some_see) {
-              *piece = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint4 x = *piece;
-              const uint32_t b0 = nan_codes(x.x), b1 = nan_codes(x.y), b2 = nan_codes(x.z), b3 = nan_codes(x.w);
-              if (b0 | b1 | b2 | b3) {
-                auto clear = [](uint32_t v, uint32_t bad) { return v & ~((bad >> 7) * 255u); };
-                *piece = make_uint4(clear(x.x, b0), clear(x.y, b1), clear(x.z, b2), clear(x.w, b3));
-                m->nonfinite[units & 1] = units;
-              }
-            }
-          }
-          ptx::fence_proxy_async_smem();
+          if (clear_edge<C, QT_ROWS * 2>(ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
+            m->nonfinite[units & 3] = units;
           __syncwarp();
         }
         if (active) {
           uint32_t x[COLS / 32][32];
+          const uint32_t s_col = lanes + C::S_COL + (jj & 1) * QT_TILE;
 #pragma unroll
-          for (int h = 0; h < COLS / 32; ++h)
-            ptx::tmem_ld_x32(lanes + C::S_COL + half * COLS + 32 * h, x[h]);
-          // (before the arrival: once the next unit's scores have run, the exponents
-          // of the one behind it may go to the same place)
-          if (j == 0) q_scale = exp2_int(m->q_exp[units & 1][r]) * a.scale_log2;
+          for (int h = 0; h < COLS / 32; ++h) ptx::tmem_ld_x32(s_col + half * COLS + 32 * h, x[h]);
+          if (j == 0) q_scale = exp2_int(m->q_exp[units % 3][r]) * a.scale_log2;
           ptx::tmem_wait_ld();
           ptx::tc_fence_before();
-          arrive(&m->s_free);
           if (edge) {
             const int left = own - t * QT_TILE - half * COLS + 1;  // of this thread's columns
 #pragma unroll
@@ -753,17 +430,19 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           for (int g = 0; g < COLS / QT_GROUP; ++g) {
             // (not zero: it multiplies -infinity; and a scale of zero leaves scores of next to nothing)
             kf[g] = fmaxf(q_scale * sc[0][half * (COLS / QT_GROUP) + g], 1e-37f);
-            float most = -INFINITY;
+            float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < QT_GROUP; ++i)
-              most = fmaxf(most, __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]));
-            tmax = fmaxf(tmax, most * kf[g]);
+              most[i & 1] = fmaxf(most[i & 1], __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]));
+            tmax = fmaxf(tmax, fmaxf(most[0], most[1]) * kf[g]);
           }
 #pragma unroll
           for (int g = 0; g < 8; ++g) vmax = fmaxf(vmax, sc[1][g]);
+          // (the two meet: both have their scores, and P may go where these were)
           tmax = fmaxf(tmax, exchange(tmax, ok));
           if (!ok) break;
-          const bool grows = in && tmax > mx + QT_SLACK, wider = vmax > ref;  // also the first score a row sees
+          ptx::tc_fence_after();
+          const bool grows = in && tmax > mx + QT_SLACK, wider = vmax > ref * QT_WIDER;  // also the first a row sees
           if (__any_sync(0xffffffffu, grows || wider)) {
             float f = grows ? (mx == -INFINITY ? 0.f : exp2f(mx - tmax)) : 1.f;
             if (grows) mx = tmax;
@@ -787,7 +466,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
             }
           }
           const float base = QT_TOP - (mx == -INFINITY ? 0.f : mx), inv_ref = ref > 0.f ? 1.f / ref : 0.f;
-          uint32_t hi[COLS / 4], lo[COLS / 4];
+          uint32_t part[3][COLS / 4];
           float acc[4] = {};
 #pragma unroll
           for (int i = 0; i < COLS; i += 4) {
@@ -799,19 +478,17 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
               acc[k] += p[k];
               p[k] *= vf;
             }
-            uint32_t h0, h1, l0, l1;
-            cut(p[0], p[1], h0, l0);
-            cut(p[2], p[3], h1, l1);
-            hi[i / 4] = h0 | h1 << 16;
-            lo[i / 4] = l0 | l1 << 16;
+            uint32_t h0, m0, l0, h1, m1, l1;
+            cut_weights(p[0], p[1], h0, m0, l0);
+            cut_weights(p[2], p[3], h1, m1, l1);
+            part[0][i / 4] = __byte_perm(h0, h1, 0x7531);
+            part[1][i / 4] = __byte_perm(m0, m1, 0x7531);
+            part[2][i / 4] = __byte_perm(l0, l1, 0x5410);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          const uint32_t p_col = lanes + C::P_COL + (jj & 1) * 2 * C::P_PART + half * (COLS / 4);
-          ptx::tmem_st_x16(p_col, hi);
-          ptx::tmem_st_x16(p_col + C::P_PART, lo);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) ptx::tmem_st_x16(s_col + k * C::P_PART + half * (COLS / 4), part[k]);
           ptx::tmem_wait_st();
-        } else {
-          arrive(&m->s_free);
         }
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
@@ -860,24 +537,27 @@ size_t attend_ws(int D, int ctas, int rows_cap, size_t *ml_at, size_t *part_at) 
 }
 
 template <int D, bool FP16>
-cudaError_t launch_attend(const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+cudaError_t launch_rows(const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
   using C = QCfg<D>;
   // per device and cheap: set on every call rather than remembered
   cudaError_t e = cudaFuncSetAttribute(qattend_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const bool chain = prof_chain(MOE_KERNEL_ATTN_QCACHE), quiet = prof_quiet(MOE_KERNEL_ATTN_QCACHE);
-  prof_before(MOE_KERNEL_ATTN_QCACHE, s);
-  e = launch_dep(chain, qattend_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a);
-  prof_after(MOE_KERNEL_ATTN_QCACHE, s);
-  if (e != cudaSuccess) return e;
-  return launch_dep(quiet, join_kernel<D, FP16>, dim3(ctas * 2), dim3(JOIN_THREADS), 0, s, a.j, ctas);
+  return launch_dep(prof_chain(MOE_KERNEL_ATTN_QCACHE), qattend_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s,
+                    maps, a);
 }
 
 template <bool FP16>
-cudaError_t launch_attend_d(int D, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
-  return D == 64    ? launch_attend<64, FP16>(maps, a, ctas, s)
-         : D == 128 ? launch_attend<128, FP16>(maps, a, ctas, s)
-                    : launch_attend<256, FP16>(maps, a, ctas, s);
+cudaError_t launch_attend(int D, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+  const bool quiet = prof_quiet(MOE_KERNEL_ATTN_QCACHE);
+  prof_before(MOE_KERNEL_ATTN_QCACHE, s);
+  const cudaError_t e = a.j.rows_cap <= QD_MOST ? launch_attend_few(D, FP16, maps, a, ctas, s)
+                        : D == 64               ? launch_rows<64, FP16>(maps, a, ctas, s)
+                        : D == 128              ? launch_rows<128, FP16>(maps, a, ctas, s)
+                                                : launch_rows<256, FP16>(maps, a, ctas, s);
+  prof_after(MOE_KERNEL_ATTN_QCACHE, s);
+  if (e != cudaSuccess) return e;
+  auto join = D == 64 ? join_kernel<64, FP16> : D == 128 ? join_kernel<128, FP16> : join_kernel<256, FP16>;
+  return launch_dep(quiet, join, dim3(ctas * 2), dim3(JOIN_THREADS), 0, s, a.j, ctas);
 }
 
 }  // namespace
@@ -961,7 +641,7 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
       !moe::code_map(&maps.v, a.v_layer, pool_rows, c->n_kv_heads, D, a.page_box, spans))
     return moe::note_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = dtype == MOE_FP16 ? moe::launch_attend_d<true>(D, maps, a, ctas, s)
-                        : moe::launch_attend_d<false>(D, maps, a, ctas, s);
+  e = dtype == MOE_FP16 ? moe::launch_attend<true>(D, maps, a, ctas, s)
+                        : moe::launch_attend<false>(D, maps, a, ctas, s);
   return moe::note_cuda_error(e);
 }

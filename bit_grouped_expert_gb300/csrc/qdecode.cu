@@ -1,0 +1,586 @@
+// Attention over the 8-bit paged KV cache for few rows (qcache.h, qattend.cu): up
+// to 40 rows (query heads of a KV head times tokens) a unit, as decoding has them.
+//
+// There the matrices stand the other way up: positions, not rows, fill the
+// 128 lanes of an MMA, so that a thread has one position and a share of the
+// rows, and little work is repeated for rows that are not there:
+//   S^T[128 positions x 3 R] = K . [Qh Qm Ql]^T    tcgen05 (e4m3), all in shared memory
+//   P = 2^(S scales - m)                           a position's rows by two threads
+//   O^T[D x 3 R]            += V^T . [Ph Pm Pl]^T  tcgen05 (e4m3 x e5m2), all in shared memory
+// The parts of q (three e4m3 here, which keep fp16 whole too) and of the weights (qattend.cu)
+// are columns of one product, added up where it is read: K and V go through the tensor
+// cores once.
+//
+// A row's maximum is spread over 128 threads, and is not needed as long as no
+// score passes the running one by 2^7: each tile the four warps that share the
+// rows exchange one flag, and only where it is up they find the maxima and rescale.
+// Sums stay in their threads until the unit ends.
+//
+// Units, runs, roles, waits and the joining kernel are qattend.cu's, with two S
+// and two P buffers, and one warp for the queries.
+#include <math.h>
+
+#include "qattend.cuh"
+
+namespace moe {
+namespace {
+
+// RT: rows of a thread; a unit's rows are two halves of RT.
+template <int D, int RT>
+struct DCfg {
+  static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
+  static constexpr int CHUNKS = D / ROWB;           // column spans
+  // (12 warps have 168 registers a thread, 13 would have 128)
+  static constexpr int ROW_WARPS = 8, LOADER = 8, ISSUE_S = 9, ISSUE_O = 10, QUERY = 11, WARPS = 12, THREADS = WARPS * 32;
+  static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
+  static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
+  // rows, and columns of a product: three parts of them (the columns behind those are not looked at)
+  static constexpr int R = 2 * RT, N = (3 * R + 15) / 16 * 16;
+  static constexpr int Q_SPAN = N * ROWB, P_TILE = N * QT_TILE;
+  static constexpr int NS = D == 256 ? 5 : D == 128 ? 10 : 16;  // ring slots
+  // Slots of the scales' ring, as in qattend.cu; here a K used up says that all row
+  // warps have read the scores of two tiles before it.  They are past the scales of x - 5,
+  // x - 8, x - 11.
+  static constexpr int SCALES = NS == 16 ? 16 : 8;
+  static constexpr int OFF_P = CHUNKS * Q_SPAN;
+  static constexpr int OFF_RING = OFF_P + 2 * P_TILE;
+  static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
+  static constexpr int MISC = D == 64 ? 4096 : 3072, SMEM = OFF_MISC + MISC;
+  static_assert(SMEM <= 227 * 1024 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "shared memory");
+  // Tensor memory columns: two S tiles, O of each 128 values of a head.
+  static constexpr int O_TILES = D == 256 ? 2 : 1;
+  static constexpr uint32_t O_COL = 2 * N, USED = (2 + O_TILES) * N;
+  static constexpr uint32_t TMEM = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+  static_assert(USED <= 512 && RT % 4 == 0 && R % 8 == 0, "rows");
+};
+
+template <typename C, int RT>
+struct DMisc : QRing<C> {
+  uint64_t s_full[2], s_free[2], meet[2];
+  int nonfinite[4];                  // by the unit's number: that unit, if NaN was taken out of its V
+  __align__(16) float q_f[4][C::R];  // by the unit's number: what a row's scores are multiplied by
+  float base[2][RT];                 // 2^6 over the running maximum, in log2; infinity before the first score
+  union {
+    long long wsum[C::WARPS];
+    struct {                         // later: what the four warps of a half exchange
+      int grows[2][2][4];            // [turn][half][warp]
+      float most[2][4][RT];          // [half][warp][row]
+    };
+  };
+};
+
+// Four columns at a time of a warp's lanes, N in all.
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    uint32_t x[4];
+    ptx::tmem_ld(taddr + i, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[i + k] = __uint_as_float(x[k]);
+  }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
+    qdecode_kernel(const __grid_constant__ QMaps maps, const __grid_constant__ AttendArgs a, const int fp16) {
+  using C = DCfg<D, RT>;
+  using M = DMisc<C, RT>;
+  static_assert(sizeof(M) <= C::MISC, "misc area");
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
+  M *m = reinterpret_cast<M *>(smem + C::OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const CacheView &c = a.q.c;
+  // the joining kernel may be scheduled now; it waits for this grid to finish
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (ptx::smem_u32(smem) & 1023u) {  // not placed as declared: no kernel then, rather than wrong tiles
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) {
+      set_status(c.status, MOE_ERR_UNSUPPORTED);
+      a.j.desc[blockIdx.x].parts = 0;
+    }
+    return;
+  }
+  if (warp == C::LOADER && lane == 0) {
+    ptx::prefetch_tmap(&maps.k);
+    ptx::prefetch_tmap(&maps.v);
+  }
+  if (warp == C::ISSUE_S) {
+    ptx::tmem_alloc(&m->tmem, C::TMEM);
+    ptx::tmem_relinquish();
+  }
+  if (tid >= 32 && tid < 32 + C::NS) {
+    ptx::mbar_init(&m->full[tid - 32], 1);
+    ptx::mbar_init(&m->empty[tid - 32], 1);
+    ptx::fence_mbar_init();
+  } else if (tid >= 64 && tid < 64 + C::SCALES) {
+    ptx::mbar_init(&m->sc_full[tid - 64], 1);
+    ptx::fence_mbar_init();
+  } else if (tid >= 128 && tid < 128 + 2 * RT) {
+    m->base[0][tid - 128] = INFINITY;
+  } else if (tid == 96) {
+    m->abort_flag = 0;
+    ptx::mbar_init(&m->q_full, 1);
+    ptx::mbar_init(&m->q_free, 1);
+    ptx::mbar_init(&m->final_bar, 2);
+    ptx::mbar_init(&m->o_free, C::ROW_WARPS);
+    for (int i = 0; i < 4; ++i) m->nonfinite[i] = -1;
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&m->p_ready[i], C::ROW_WARPS);
+      ptx::mbar_init(&m->pv_done[i], 1);
+      ptx::mbar_init(&m->s_full[i], 1);
+      ptx::mbar_init(&m->s_free[i], C::ROW_WARPS);
+      ptx::mbar_init(&m->meet[i], 4);
+    }
+    ptx::fence_mbar_init();
+  }
+  // what the kernel before writes (lengths, tables, codes, scales, queries) from here on,
+  // by ordinary loads: a read-only one may look at what was there before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  long long end, T;
+  int runs;
+  const long long count = find_run<C>(a, m, end, T, runs);
+  const uint32_t tmem = m->tmem;
+  const int cta = blockIdx.x;
+  if (count == 0) {  // less to do than CTAs
+    if (tid == 0) a.j.desc[cta].parts = 0;
+    if (warp == C::ISSUE_S) ptx::tmem_dealloc(tmem, C::TMEM);
+    return;
+  }
+  QWalk<C> w(a, m->b0, m->s0, m->off0, count);
+  uint8_t *ring = smem + C::OFF_RING, *p_tiles = smem + C::OFF_P;
+  int32_t *status = c.status;
+
+  if (warp == C::LOADER) {
+    load_tiles<C>(maps, a, m, w, ring);
+  } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
+    // ----------------------------------------------------------------- MMAs
+    const bool does_s = warp == C::ISSUE_S;
+    const uint32_t id_s = ptx::idesc_f8(C::N, false, false, false, false), id_o = ptx::idesc_f8(C::N, false, true, true, false);
+    const uint64_t qd = ptx::sdesc_rows(ptx::smem_u32(smem), C::ROWB, 16);
+    uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
+    bool ok = true;
+    auto scores = [&](uint32_t pos, uint32_t t, bool first) {  // S^T of running tile t from the K tile at load `pos`
+      const uint32_t slot = pos % C::NS;
+      if (t >= 2 && !q_wait_warp(&m->s_free[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+      // What the slot held before has been loaded: a K by an earlier wait here, a V
+      // of tile t - 4 or before since the row warps, at tile t - 2, have waited for its product.  A
+      // unit's first slot may follow the last unit's V of tile t - 3:
+      if (first && t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
+      if (!q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+      ptx::tc_fence_after();
+      const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, 16);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int ch = 0; ch < C::CHUNKS; ++ch)
+#pragma unroll
+          for (int i = 0; i < C::ROWB / 32; ++i)
+            ptx::mma_ss_f8(tmem + (t & 1) * C::N, kd + (ch * C::SPAN + i * 32) / 16,
+                             qd + (ch * C::Q_SPAN + i * 32) / 16, id_s, (ch | i) != 0);
+        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->s_full[t & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto values = [&](uint32_t pos, uint32_t t, bool first) {  // O^T += V^T P^T of running tile t
+      const uint32_t slot = pos % C::NS;
+      if (!q_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
+          (first && units > 0 && !q_wait_warp(&m->o_free, (units - 1) & 1u, m, status)) ||
+          !q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))
+        return false;
+      ptx::tc_fence_after();
+      const uint64_t pd = ptx::sdesc_rows(ptx::smem_u32(p_tiles + (t & 1) * C::P_TILE), 128, 16);
+      // (heads of 64 values: the product's upper 64 rows are the lower ones again)
+      const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, D == 64 ? 0 : C::SPAN);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int ot = 0; ot < C::O_TILES; ++ot)
+#pragma unroll
+          for (int i = 0; i < QT_TILE / 32; ++i)
+            ptx::mma_ss_f8(tmem + C::O_COL + ot * C::N, vd + (ot * C::SPAN + i * 32 * C::ROWB) / 16, pd + i * 32 / 16,
+                             id_o, !first || i > 0);
+        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->pv_done[t & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && w.next()) {
+      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_at(0), jj, true);
+      for (int j = 0; ok && j < w.n; ++j, ++jj) {
+        if (does_s) {
+          if (j + 1 < w.n) ok = scores(ld + k_at(j + 1), jj + 1, false);
+          // the unit's last scores are under way
+          if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
+          __syncwarp();
+        } else {
+          ok = values(ld + v_at(j, w.n), jj, j == 0);
+        }
+      }
+      ld += 2 * w.n;
+      ++units;
+    }
+    __syncwarp();
+    if (ptx::elect_one()) ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
+    __syncwarp();
+    q_drain(&m->final_bar, 0);
+  } else if (warp >= C::QUERY) {
+    // -------------------------------------------------------------- queries
+    constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;  // of a row; rows a warp cuts at once
+    constexpr int AHEAD = C::R / AT_ONCE % 8 == 0 ? 8 : C::R / AT_ONCE % 4 == 0 ? 4 : 2;  // loads in flight
+    static_assert(C::R % (AHEAD * AT_ONCE) == 0, "no rows behind the last");
+    const int d = lane % LANES * 8;
+    uint32_t units = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      // the last unit's scores are done
+      if (units > 0 && !(ok = q_wait_warp(&m->q_free, (units - 1) & 1u, m, status))) break;
+      const int rows = w.tokens() * a.G;
+      for (int r0 = lane / LANES; r0 < C::R; r0 += AHEAD * AT_ONCE) {
+        uint4 x[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int r = r0 + u * AT_ONCE, token = r * a.g_mul >> 16;
+          x[u] = make_uint4(0u, 0u, 0u, 0u);  // (rows that are not there: zeros)
+          if (r < rows)
+            x[u] = *reinterpret_cast<const uint4 *>(
+                a.x + ((size_t)(w.s.lo + w.token0() + token) * a.Hq + w.g * a.G + (r - token * a.G)) * D + d);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int r = r0 + u * AT_ONCE;
+          float f[8];
+          if (fp16)
+            unpack8<true>(x[u], f);
+          else
+            unpack8<false>(x[u], f);
+          uint2 part[3];
+          const int e = cut_row<LANES, 3>(f, part);
+          uint32_t off = r * C::ROWB + d % C::ROWB;
+          off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
+          uint8_t *to = smem + d / C::ROWB * C::Q_SPAN + off;
+#pragma unroll
+          for (int k = 0; k < 3; ++k)  // (R is a multiple of 8: the same swizzle)
+            *reinterpret_cast<uint2 *>(to + k * C::R * C::ROWB) = part[k];
+          if (d == 0) m->q_f[units & 3][r] = exp2_int(e) * a.scale_log2;
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&m->q_full);
+      ++units;
+    }
+  } else {
+    // ----------------------------------------------------------------- rows
+    const int half = warp >> 2, quad = warp & 3, at = quad * 32 + lane;  // this thread's position of a tile, value of O
+    const int r0 = half * RT;                                            // its first row
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + r0;
+    uint32_t ld = 0, jj = 0, meets = 0;
+    int units = 0;
+    bool ok = true;
+    SplitDesc split{};
+    // one arrival a warp, for all of its lanes
+    auto arrive = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    auto meet = [&]() {  // the half's four warps (a wait that can give up, as all others)
+      arrive(&m->meet[half]);
+      return q_wait_warp(&m->meet[half], meets++ & 1u, m, status);
+    };
+    struct Unit {
+      int slot, lo, token0, rows, g, t0, n, nt_all;
+      int pos0;               // position of its first token
+      int all_see, some_see;  // positions that all of its rows see, that its last one does
+      long long done;         // where this CTA's part ends in the count of all
+    } un{};
+    float sum[RT], ref = 0.f;
+    // The unit whose tiles were the last: its result is taken out of tensor
+    // memory while the next unit's first scores run.
+    auto finish = [&]() {
+      const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
+      const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
+      // sums over the half's positions
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (lane == 0) m->most[half][quad][i] = sum[i];
+      }
+      if (!meet()) return false;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        sum[i] = (m->most[half][0][i] + m->most[half][1][i]) + (m->most[half][2][i] + m->most[half][3][i]);
+      if (at < RT) {  // the maxima: to the joining kernel, and from the start for the next unit
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          if (i == at) mine = sum[i];
+        if (!whole && r0 + at < un.rows)
+          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r0 + at) * 2) =
+              make_float2(QT_TOP - m->base[half][at], mine);
+        m->base[half][at] = INFINITY;
+      }
+      if (!meet()) return false;  // read by all before they are written again
+      if (!q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
+      ptx::tc_fence_after();
+      if (!whole && starts) {
+        const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
+        split = SplitDesc{(int)q_mul_div(u1 * runs + T - 1, 1, T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
+      }
+      // PV has ended, and with it every write of the flag
+      const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
+#pragma unroll 1
+      for (int ot = 0; ot < C::O_TILES; ++ot) {
+          const int d = ot * 128 + at;
+          const uint32_t col = lanes + C::O_COL + ot * C::N;
+          float o[RT], mid[RT], lo[RT];
+          __syncwarp();
+          read_columns(col, o);
+          read_columns(col + C::R, mid);
+          read_columns(col + 2 * C::R, lo);
+          ptx::tmem_wait_ld();
+          if (D == 64 && at >= 64) continue;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) o[i] = ((o[i] + mid[i]) + lo[i]) * ref;
+          if (fix) {  // codes NaN that were taken out of the edge's tiles, for the rows that see them
+            const int p1 = min(un.some_see, (un.t0 + un.n) * QT_TILE);
+            const int32_t *table = c.table + (size_t)un.slot * c.max_pages;
+            for (int p = max(un.all_see, un.t0 * QT_TILE); p < p1; ++p) {
+              const unsigned page = (unsigned)table[p >> c.page_shift];
+              if (page >= (unsigned)c.n_pages) continue;
+              const uint8_t code =
+                  a.v_layer[((((size_t)page << c.page_shift) + (p & ((1 << c.page_shift) - 1))) * a.Hkv + un.g) * D + d];
+              if ((code & 0x7F) != 0x7F) continue;
+#pragma unroll
+              for (int i = 0; i < RT; ++i)
+                if (p <= un.pos0 + ((r0 + i) * a.g_mul >> 16)) o[i] = NAN;
+            }
+          }
+          uint16_t *out = a.o + ((size_t)(un.lo + un.token0) * a.Hq + un.g * a.G) * D + d;
+          float *part = a.j.part + ((pslot * (D / 4) + d / 4) * a.j.rows_cap) * 4 + d % 4;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const int r = r0 + i, token = r * a.g_mul >> 16;
+            if (r >= un.rows) continue;
+            if (whole) {
+              const float y = sum[i] == 0.f ? 0.f : o[i] * (1.f / sum[i]);
+              out[((size_t)token * a.Hq + (r - token * a.G)) * D] =
+                  fp16 ? __half_as_ushort(__float2half_rn(y)) : f32_to_bf16(y);
+            } else {
+              part[r * 4] = o[i];
+            }
+          }
+        }
+      ptx::tc_fence_before();
+      arrive(&m->o_free);
+      return true;
+    };
+    while (ok) {
+      const bool more = w.next();
+      if (un.n > 0) ok = finish();
+      if (!more || !ok) break;
+      const int pos0 = w.s.L - w.s.n + w.token0();
+      un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, pos0, 0, 0, end - w.left};
+      un.all_see = max(0, pos0 + 1);
+      un.some_see = max(0, pos0 + w.tokens());
+#pragma unroll
+      for (int i = 0; i < RT; ++i) sum[i] = 0.f;
+      ref = 0.f;
+      for (int j = 0; j < un.n; ++j, ++jj) {
+        const int t = un.t0 + j;
+        const bool edge = (t + 1) * QT_TILE > un.all_see;
+        // The scores are there; the P tile of jj is free, so that no wait below or in the other
+        // roles can take a phase of its barrier for the one two before (the first two
+        // tiles' barrier is a phase behind: asked for the one before its first, it says yes); the
+        // scales are there (this warp has waited for the slot's phase before, SCALES tiles ago).
+        if (!(ok = q_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, &m->pv_done[jj & 1], ((jj >> 1) & 1u) ^ 1u,
+                               &m->sc_full[jj % C::SCALES], (jj / C::SCALES) & 1u, m, status)))
+          break;
+        ptx::tc_fence_after();
+        if (edge) {
+          // (codes NaN that are taken out: finish() puts them where they belong)
+          const uint32_t pos = ld + v_at(j, un.n), slot = pos % C::NS;
+          // the slots' last loads have been used up (else their barriers could still be a phase behind)
+          if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
+          ok = ok && q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status);
+          if (!ok) break;
+          if (clear_edge<C, C::ROW_WARPS * 32>(ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
+            m->nonfinite[units & 3] = units;
+          __syncwarp();
+        }
+        const float(*sc)[8] = m->scales[jj % C::SCALES];
+        const float ks = sc[0][at / QT_GROUP], vs = sc[1][at / QT_GROUP];
+        float vmax = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) vmax = fmaxf(vmax, sc[1][g]);
+        // this position's scores
+        float s[RT], x[RT];
+        {
+          float mid[RT], lo[RT];
+          const uint32_t col = lanes + (jj & 1) * C::N;
+          read_columns(col, s);
+          read_columns(col + C::R, mid);
+          read_columns(col + 2 * C::R, lo);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < RT; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(&m->q_f[units & 3][r0 + i]);
+            const float qf[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[i + k] = ((s[i + k] + mid[i + k]) + lo[i + k]) * (qf[k] * ks);
+          }
+        }
+        ptx::tc_fence_before();
+        arrive(&m->s_free[jj & 1]);
+        if (edge) {
+          const int first = pos0 - (t * QT_TILE + at);  // row r sees the position if -first <= its token
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            if (r0 + i >= un.rows || first + ((r0 + i) * a.g_mul >> 16) < 0) s[i] = -INFINITY;
+        }
+        // what it is over the running maximum; infinite where that is still to be found
+        bool grows = vmax > ref * QT_WIDER;
+        auto over_maximum = [&]() {
+#pragma unroll
+          for (int i = 0; i < RT; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(&m->base[half][i]);
+            const float base[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[i + k] = s[i + k] == -INFINITY ? -INFINITY : s[i + k] + base[k];
+              grows |= x[i + k] > QT_TOP + QT_SLACK;
+            }
+          }
+        };
+        over_maximum();
+        grows = __any_sync(0xffffffffu, grows);
+        const uint32_t turn = jj & 1u;
+        if (lane == 0) m->grows[turn][half][quad] = grows;
+        if (!(ok = meet())) break;
+        {
+          const volatile int *f = m->grows[turn][half];
+          grows = (f[0] | f[1] | f[2] | f[3]) != 0;
+        }
+        if (grows) {
+          float v_f = 1.f;
+          if (vmax > ref * QT_WIDER) {
+            v_f = ref / vmax;
+            ref = vmax;
+          }
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            float most = s[i];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            if (lane == 0) m->most[half][quad][i] = most;
+          }
+          if (!(ok = meet())) break;
+          float f[RT];
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
+                                     fmaxf(m->most[half][2][i], m->most[half][3][i]));
+            const float was = m->base[half][i];
+            const bool up = most + was > QT_TOP + QT_SLACK;  // (of a row that has seen nothing yet: any score)
+            f[i] = up ? ex2(QT_TOP - most - was) : 1.f;
+            sum[i] *= f[i];
+            f[i] *= v_f;
+            x[i] = up ? QT_TOP - most : was;
+          }
+          if (!(ok = meet())) break;  // read by all before they are written again
+          if (quad == 0 && lane == 0)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) m->base[half][i] = x[i];
+          if (j > 0) {  // O holds the earlier tiles
+            if (!(ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < 3 * C::O_TILES; ++k) {
+              const uint32_t col = lanes + C::O_COL + k / 3 * C::N + k % 3 * C::R;
+              float v[RT];
+              read_columns(col, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < RT; i += 4) {
+                uint32_t y[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) y[q] = __float_as_uint(v[i + q] * f[i + q]);
+                ptx::tmem_st(col + i, y);
+              }
+            }
+            ptx::tmem_wait_st();
+          }
+          if (!(ok = meet())) break;  // the maxima are there
+          over_maximum();
+        }
+        // the weights, a byte a row and part: the lanes' bytes lie side by side
+        const float vf = ref > 0.f ? vs / ref : 0.f;
+        uint8_t *p_tile = p_tiles + (jj & 1) * C::P_TILE;
+#pragma unroll
+        for (int i = 0; i < RT; i += 2) {
+          float p[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            p[k] = ex2(x[i + k]);
+            sum[i + k] += p[k];
+          }
+          uint32_t hi, mid, lo;
+          cut_weights(p[0] * vf, p[1] * vf, hi, mid, lo);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = r0 + i + k;
+            uint8_t *to = p_tile + r * QT_TILE + (at ^ (r & 7) << 4);
+            to[0] = (uint8_t)(hi >> (16 * k + 8));
+            to[C::R * QT_TILE] = (uint8_t)(mid >> (16 * k + 8));
+            to[2 * C::R * QT_TILE] = (uint8_t)(lo >> 8 * k);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        arrive(&m->p_ready[jj & 1]);
+      }
+      ld += 2 * un.n;
+      ++units;
+    }
+    if (tid == 0) a.j.desc[cta] = split;
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == C::ISSUE_S) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+template <int D, int RT>
+cudaError_t launch_few(bool fp16, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+  using C = DCfg<D, RT>;
+  // per device and cheap: set on every call rather than remembered
+  cudaError_t e = cudaFuncSetAttribute(qdecode_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_dep(prof_chain(MOE_KERNEL_ATTN_QCACHE), qdecode_kernel<D, RT>, dim3(ctas), dim3(C::THREADS), C::SMEM, s,
+                    maps, a, (int)fp16);
+}
+
+template <int D>
+cudaError_t launch_few_d(bool fp16, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+  const int rows = a.j.rows_cap;
+  return rows <= 8    ? launch_few<D, 4>(fp16, maps, a, ctas, s)
+         : rows <= 16 ? launch_few<D, 8>(fp16, maps, a, ctas, s)
+         : rows <= 32 ? launch_few<D, 16>(fp16, maps, a, ctas, s)
+                      : launch_few<D, 20>(fp16, maps, a, ctas, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(int D, bool fp16, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+  return D == 64    ? launch_few_d<64>(fp16, maps, a, ctas, s)
+         : D == 128 ? launch_few_d<128>(fp16, maps, a, ctas, s)
+                    : launch_few_d<256>(fp16, maps, a, ctas, s);
+}
+
+}  // namespace moe
