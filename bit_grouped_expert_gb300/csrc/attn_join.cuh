@@ -18,9 +18,10 @@ struct SplitDesc {
 struct JoinArgs {
   SplitDesc *desc;  // [grid]
   float *ml;        // [2 * grid][rows_cap][2]
-  float *part;      // [2 * grid][D / 4][rows_cap][4]
+  float *part;      // [2 * grid][D / 4][rows_cap][4], or with row_major [2 * grid][rows_cap][D]
   uint16_t *o;      // [rows][Hq][D]
   int rows_cap;     // rows of a unit at most
+  int row_major;
   int Hq, G;        // query heads, and of a KV head
 };
 
@@ -144,9 +145,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
           if (i < ds.parts) {
             const size_t p = (size_t)2 * (c0 + i * ds.stride) + (i == 0 ? 1 : 0);
             ml[k] = reinterpret_cast<const float2 *>(a.ml)[p * a.rows_cap + r];
-            const float4 *src = reinterpret_cast<const float4 *>(a.part) + (p * (D / 4) + c4) * a.rows_cap + r;
+            const float4 *src = reinterpret_cast<const float4 *>(a.part) + p * (D / 4) * a.rows_cap +
+                                (a.row_major ? r * (D / 4) + c4 : c4 * a.rows_cap + r);
+            const int step = a.row_major ? 1 : a.rows_cap;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[k][q] = src[q * a.rows_cap];
+            for (int q = 0; q < 4; ++q) v[k][q] = src[q * step];
           }
         }
         add(ml[0], v[0]);

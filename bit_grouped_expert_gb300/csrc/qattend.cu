@@ -25,8 +25,8 @@
 // per CTA, whatever the lengths: a unit that spans CTAs leaves partial results
 // (m, l, O in fp32), which a second kernel joins (attn_join.cuh).
 //
-// Roles: eight warps own the rows, one loads (TMA: pages by the table's numbers,
-// K one tile ahead of V, into a ring, and the pages' scales), two issue the MMAs
+// Roles: eight warps own the rows, two load (TMA: pages by the table's numbers, K
+// with the pages' scales and V, each into a ring of its own), two issue the MMAs
 // of S (of the next tile during the softmax of this one) and of O, four cut the
 // next unit's queries.  Who waits on a barrier's parity must know that the phase
 // before has passed: the comments at the waits say from what.
@@ -45,20 +45,19 @@ template <int D>
 struct QCfg {
   static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
   static constexpr int CHUNKS = D / ROWB;           // column spans
-  static constexpr int ROW_WARPS = 8, LOADER = 8, ISSUE_S = 9, ISSUE_O = 10, QUERY = 11, QUERY_WARPS = 4;
+  static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11, QUERY = 12, QUERY_WARPS = 4;
   static constexpr int WARPS = QUERY + QUERY_WARPS, THREADS = WARPS * 32;
   static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   static constexpr int Q_SPAN = QT_ROWS * ROWB, Q_PART = CHUNKS * Q_SPAN;
-  static constexpr int NS = D == 256 ? 5 : D == 128 ? 10 : 16;  // ring slots
-  // Slots of the scales' ring.  The loader stores tile x's when it has issued the
-  // load 2 x at least, so that the load 2 x - NS has been used up.  That is, NS = 5: K of
-  // tile x - 2 or V of x - 3; 10: V of x - 6 or K of x - 5; 16: V of x - 9 or K of x - 8.  A K used up says
-  // that the product with V of two tiles before is done: the row warps are past the
-  // scales of x - 4, x - 7, x - 10.
-  static constexpr int SCALES = NS == 5 ? 4 : NS == 10 ? 8 : 16;
+  static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 3 : NSK;  // ring slots of K, of V
+  // Slots of the scales' ring.  Those of tile x are asked for when K of tile x - NSK has been
+  // used up, which was after the product with V of the tile two before that: all row warps
+  // are past the scales of tile x - NSK - 2.
+  static constexpr int SCALES = D == 256 ? 4 : D == 128 ? 8 : 16;
+  static_assert(SCALES >= NSK + 2, "scales");
   static constexpr int OFF_RING = 2 * Q_PART;
-  static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
+  static constexpr int OFF_V = OFF_RING + NSK * SLOT, OFF_MISC = OFF_V + NSV * SLOT;
   static constexpr int SMEM = OFF_MISC + (D == 256 ? 3 : 4) * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // Tensor memory columns: O, two S tiles; a tile's P, three parts of four weights a
@@ -100,18 +99,22 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     }
     return;
   }
-  if (warp == C::LOADER && lane == 0) {
-    ptx::prefetch_tmap(&maps.k);
-    ptx::prefetch_tmap(&maps.v);
-  }
+  if (warp == C::LOAD_K && lane == 0) ptx::prefetch_tmap(&maps.k);
+  if (warp == C::LOAD_V && lane == 0) ptx::prefetch_tmap(&maps.v);
   if (warp == C::ISSUE_S) {
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
-  if (tid >= 32 && tid < 32 + C::NS) {
-    ptx::mbar_init(&m->full[tid - 32], 1);
-    ptx::mbar_init(&m->empty[tid - 32], 1);
-    if (tid < 32 + C::SCALES) ptx::mbar_init(&m->sc_full[tid - 32], 1);
+  if (tid >= 32 && tid < 32 + C::SCALES) {
+    ptx::mbar_init(&m->sc_full[tid - 32], 16);
+    ptx::fence_mbar_init();
+  } else if (tid >= 128 && tid < 128 + C::NSK) {
+    ptx::mbar_init(&m->k_full[tid - 128], 1);
+    ptx::mbar_init(&m->k_empty[tid - 128], 1);
+    ptx::fence_mbar_init();
+  } else if (tid >= 160 && tid < 160 + C::NSV) {
+    ptx::mbar_init(&m->v_full[tid - 160], 1);
+    ptx::mbar_init(&m->v_empty[tid - 160], 1);
     ptx::fence_mbar_init();
   } else if (tid == 64) {
     m->abort_flag = 0;
@@ -144,26 +147,28 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     return;
   }
   QWalk<C> w(a, m->b0, m->s0, m->off0, count);
-  uint8_t *ring = smem + C::OFF_RING;
+  uint8_t *k_ring = smem + C::OFF_RING, *v_ring = smem + C::OFF_V;
   int32_t *status = c.status;
 
-  if (warp == C::LOADER) {
-    load_tiles<C>(maps, a, m, w, ring);
+  if (warp == C::LOAD_K) {
+    load_tiles<C, false>(&maps.k, a, m, w, k_ring);
+  } else if (warp == C::LOAD_V) {
+    load_tiles<C, true>(&maps.v, a, m, w, v_ring);
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
     const uint32_t id_s = ptx::idesc_f8(QT_TILE, false, false, false, false), id_o = ptx::idesc_f8(D, true, false, false, true);
     const uint64_t qd = ptx::sdesc_rows(ptx::smem_u32(smem), C::ROWB, 16);
-    uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
+    uint32_t units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
-    auto scores = [&](uint32_t pos, uint32_t t) {  // S of running tile t from the K tile at load `pos`
-      const uint32_t slot = pos % C::NS;
-      // P of tile t - 2 has been used up.  (So what the slot held before has been loaded:
-      // a K, which was waited for here, or a V of tile t - 3 or before.)
-      if (t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-      if (!q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+    auto scores = [&](uint32_t t) {  // S of running tile t
+      const uint32_t slot = t % C::NSK;
+      // P of tile t - 2 has been used up
+      if ((t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) ||
+          !q_wait_warp(&m->k_full[slot], (t / C::NSK) & 1u, m, status))
+        return false;
       ptx::tc_fence_after();
-      const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, 16);
+      const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(k_ring + slot * C::SLOT), C::ROWB, 16);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int part = 0; part < 2; ++part)
@@ -173,21 +178,21 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
             for (int i = 0; i < C::ROWB / 32; ++i)
               ptx::mma_ss_f8(tmem + C::S_COL + (t & 1) * QT_TILE, qd + (part * C::Q_PART + ch * C::Q_SPAN + i * 32) / 16,
                                kd + (ch * C::SPAN + i * 32) / 16, id_s, (part | ch | i) != 0);
-        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->k_empty[slot]);
         ptx::mma_commit(&m->s_full[t & 1]);
       }
       __syncwarp();
       return true;
     };
-    auto values = [&](uint32_t pos, uint32_t t, bool first) {  // O += P V of running tile t
-      const uint32_t slot = pos % C::NS;
+    auto values = [&](uint32_t t, bool first) {  // O += P V of running tile t
+      const uint32_t slot = t % C::NSV;
       if (!q_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
           (first && units > 0 && !q_wait_warp(&m->o_free, (units - 1) & 1u, m, status)) ||
-          !q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))
+          !q_wait_warp(&m->v_full[slot], (t / C::NSV) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
       const uint32_t p_col = tmem + C::S_COL + (t & 1) * QT_TILE;
-      const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, C::SPAN);
+      const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(v_ring + slot * C::SLOT), C::ROWB, C::SPAN);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int part = 0; part < 3; ++part)
@@ -195,25 +200,24 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           for (int i = 0; i < QT_TILE / 32; ++i)
             ptx::mma_ts_f8(tmem, p_col + part * C::P_PART + 8 * i, vd + i * 32 * C::ROWB / 16, id_o,
                              !first || part > 0 || i > 0);
-        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->v_empty[slot]);
         ptx::mma_commit(&m->pv_done[t & 1]);
       }
       __syncwarp();
       return true;
     };
     while (ok && w.next()) {
-      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_at(0), jj);
+      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(jj);
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
         if (does_s) {
-          if (j + 1 < w.n) ok = scores(ld + k_at(j + 1), jj + 1);
+          if (j + 1 < w.n) ok = scores(jj + 1);
           // the unit's last scores are under way
           if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
           __syncwarp();
         } else {
-          ok = values(ld + v_at(j, w.n), jj, j == 0);
+          ok = values(jj, j == 0);
         }
       }
-      ld += 2 * w.n;
       ++units;
     }
     __syncwarp();
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     const int r = tid & (QT_ROWS - 1), half = tid / QT_ROWS;
     const int my_token = r * a.g_mul >> 16, my_head = r - my_token * a.G;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t ld = 0, jj = 0, pairs = 0;
+    uint32_t jj = 0, pairs = 0;
     int units = 0;
     bool ok = true;
     SplitDesc split{};
@@ -401,12 +405,12 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         ptx::tc_fence_after();
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
-          const uint32_t pos = ld + v_at(j, un.n), slot = pos % C::NS;
-          // the slots' last loads have been used up (else their barriers could still be a phase behind)
+          const uint32_t slot = jj % C::NSV;
+          // the slot's last load has been used up (else its barrier could still be a phase behind)
           if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
-          ok = ok && q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status);
+          ok = ok && q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status);
           if (!ok) break;
-          if (clear_edge<C, QT_ROWS * 2>(ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
+          if (clear_edge<C, QT_ROWS * 2>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
             m->nonfinite[units & 3] = units;
           __syncwarp();
         }
@@ -493,7 +497,6 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
       }
-      ld += 2 * un.n;
       ++units;
     }
     if (tid == 0) a.j.desc[cta] = split;
@@ -519,7 +522,10 @@ bool code_map(CUtensorMap *map, const void *p, int64_t rows, int heads, int D, i
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(p), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, rowb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             D == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+             : D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                        : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,  // no more than the row: the next head is another's
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int attend_ctas(int sms) { return sms < QT_MAX_SMS ? sms : QT_MAX_SMS; }
@@ -632,6 +638,7 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
   a.j.desc = static_cast<moe::SplitDesc *>(ws_d);
   a.j.ml = moe::ws_ptr<float>(ws_d, ml_at);
   a.j.part = moe::ws_ptr<float>(ws_d, part_at);
+  a.j.row_major = a.j.rows_cap <= moe::QD_MOST;
   a.j.o = a.o;
   a.j.Hq = Hq;
   a.j.G = G;

@@ -54,7 +54,7 @@ struct QShared {
 };
 template <typename C>
 struct QRing : QShared {
-  uint64_t full[C::NS], empty[C::NS], sc_full[C::SCALES];
+  uint64_t k_full[C::NSK], k_empty[C::NSK], v_full[C::NSV], v_empty[C::NSV], sc_full[C::SCALES];
   float scales[C::SCALES][2][8];   // of a tile's groups: K, V
 };
 __device__ __forceinline__ QSeq q_load_seq(const AttendArgs &a, int b) {
@@ -184,10 +184,6 @@ __device__ __forceinline__ void q_drain(uint64_t *bar, uint32_t parity) {
     if (ptx::globaltimer() - t0 > QT_TIMEOUT_NS) return;
 }
 
-// Position of K(j) / V(j) of a unit of n tiles in the ring's load order K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ uint32_t k_at(int j) { return j == 0 ? 0u : 2u * j - 1u; }
-__device__ __forceinline__ uint32_t v_at(int j, int n) { return j == n - 1 ? 2u * n - 1u : 2u * j + 2u; }
-
 // This CTA's run: every thread adds up some sequences' units, a scan gives
 // their places, and the thread whose sequences hold the run's start writes
 // down where that is.  Returns the run's length, 0 for none; end: where it
@@ -240,28 +236,29 @@ __device__ __forceinline__ long long find_run(const AttendArgs &a, M *m, long lo
   return end - first;
 }
 
-// The loading warp: K and V tiles into the ring, in the order of k_at and v_at, and their scales.
-template <typename C, typename M>
-__device__ __forceinline__ void load_tiles(const QMaps &maps, const AttendArgs &a, M *m, QWalk<C> &w, uint8_t *ring) {
+// A loading warp: a unit's K tiles and the scales of K and V, or its V tiles, into their ring.
+template <typename C, bool V, typename M>
+__device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendArgs &a, M *m, QWalk<C> &w, uint8_t *ring) {
+  constexpr int NS = V ? C::NSV : C::NSK;
   const CacheView &c = a.q.c;
   const int lane = threadIdx.x & 31;
+  uint64_t *full = V ? m->v_full : m->k_full, *empty = V ? m->v_empty : m->k_empty;
   const int pool_rows = c.n_pages << c.page_shift, in_page = (1 << c.page_shift) - 1;
   const int boxes = QT_TILE / a.page_box;
   const bool whole = boxes == 1;  // a page holds a tile's rows: one box
   const int box = whole ? 0 : lane / C::CHUNKS, span = whole ? 0 : lane % C::CHUNKS;
   const bool issues = whole ? lane == 0 : lane < boxes * C::CHUNKS;
   const int box_at = span * C::SPAN + box * a.page_box * C::ROWB;
-  uint32_t ld = 0, tiles = 0;
+  uint32_t tiles = 0;
   bool ok = true;
   while (ok && w.next()) {
-    const int z = w.g * C::CHUNKS, blocks = pages_of(sees_of(a, w.s, w.rt), c.page_shift);
+    const int z = w.g * C::CHUNKS + span, blocks = pages_of(sees_of(a, w.s, w.rt), c.page_shift);
     const int32_t *table = c.table + (size_t)w.s.slot * c.max_pages;
-    // 64 table entries from block eb on, two a lane: the tile whose V is loaded next
-    // begins in the first 32, so the two tiles behind it (8 blocks each at most) lie
-    // in the 64, and those fetched last are not looked at before the next tile.
+    // 64 table entries from block eb on, two a lane: the tile loaded next (8 blocks at most) begins in
+    // the first 32, so that those fetched last are not looked at at once.
     auto entry = [&](int j) { return j < blocks ? table[j] : -1; };
     int eb = (w.t0 * QT_TILE >> c.page_shift) & ~31, ent0 = entry(eb + lane), ent1 = entry(eb + 32 + lane);
-    // the page of position `pos`, lane by lane, of one of the three tiles; -1 where there is none
+    // the page of position `pos`, lane by lane, of the tile; -1 where there is none
     auto page_at = [&](int pos) {
       const int j = (pos >> c.page_shift) - eb;
       const int p0 = __shfl_sync(0xffffffffu, ent0, j & 31), p1 = __shfl_sync(0xffffffffu, ent1, j & 31);
@@ -270,51 +267,40 @@ __device__ __forceinline__ void load_tiles(const QMaps &maps, const AttendArgs &
       if (eb + j < blocks) set_status(c.status, MOE_ERR_DEVICE_BOUNDS);
       return -1;
     };
-    auto load = [&](const CUtensorMap *map, int t) {
-      const uint32_t slot = ld % C::NS;
-      const int pos = t * QT_TILE + box * a.page_box, page = page_at(pos);
-      if (!q_wait_warp(&m->empty[slot], ((ld / C::NS) & 1u) ^ 1u, m, c.status)) return false;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(&m->full[slot], C::SLOT);
-      __syncwarp();
-      // (past the pool, read as zeros, where there is no page)
-      if (issues)
-        ptx::tma_load_3d(ring + slot * C::SLOT + box_at, map, &m->full[slot], 0,
-                         page < 0 ? pool_rows : (page << c.page_shift) + (pos & in_page), z + span);
-      ++ld;
-      return true;
-    };
-    // A tile's scales, a tile ahead of its K: a lane a group, K's in the first eight lanes, V's in the
-    // next; zero where there is no page.
-    auto scales = [&](int t) {
-      const int page = page_at(t * QT_TILE + (lane & 7) * QT_GROUP);
-      return lane < 16 && page >= 0 ? (lane < 8 ? a.ks : a.vs)[(size_t)page * a.Hkv + w.g] : 0.f;
-    };
-    auto store_scales = [&](float sc) {
-      const uint32_t at = tiles++ % C::SCALES;
-      if (lane < 16) m->scales[at][lane >> 3][lane & 7] = sc;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&m->sc_full[at]);
-    };
-    float sc = scales(w.t0), sc_next = w.n > 1 ? scales(w.t0 + 1) : 0.f;
-    ok = load(&maps.k, w.t0);
-    if (ok) store_scales(sc);
-    for (int j = 0; ok && j < w.n; ++j) {
+    for (int j = 0; j < w.n; ++j, ++tiles) {
       const int t = w.t0 + j;
       if ((t * QT_TILE >> c.page_shift) >= eb + 32) {
         eb += 32;
         ent0 = ent1;
         ent1 = entry(eb + 32 + lane);
       }
-      sc = sc_next;
-      if (j + 2 < w.n) sc_next = scales(t + 2);
-      if (j + 1 < w.n) ok = load(&maps.k, t + 1);
-      ok = ok && load(&maps.v, t);
-      if (ok && j + 1 < w.n) store_scales(sc);
+      const uint32_t slot = tiles % NS;
+      const int pos = t * QT_TILE + box * a.page_box, page = page_at(pos);
+      if (!(ok = q_wait_warp(&empty[slot], ((tiles / NS) & 1u) ^ 1u, m, c.status))) break;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], C::SLOT);
+      __syncwarp();
+      // (past the pool, read as zeros, where there is no page)
+      if (issues)
+        ptx::tma_load_3d(ring + slot * C::SLOT + box_at, map, &full[slot], 0,
+                         page < 0 ? pool_rows : (page << c.page_shift) + (pos & in_page), z);
+      // The tile's scales: a lane a group, K's in the first eight lanes, V's in the next; zero where
+      // there is no page.  (Straight to shared memory: a load into a register, even one
+      // used a tile later, held this warp up for its latency, 0.5 us a tile.)
+      if (!V) {
+        const uint32_t at = tiles % C::SCALES;
+        const int group = page_at(t * QT_TILE + (lane & 7) * QT_GROUP);
+        if (lane < 16) {
+          const float *src = (lane < 8 ? a.ks : a.vs) + (group < 0 ? 0 : (size_t)group * a.Hkv + w.g);
+          ptx::cp_async_4(&m->scales[at][lane >> 3][lane & 7], src, group < 0 ? 0 : 4);
+          ptx::cp_async_arrive_noinc(&m->sc_full[at]);
+        }
+        __syncwarp();
+      }
     }
   }
+  if (!V) ptx::cp_async_wait_all();
   if (!ok && lane == 0)  // loads of the last slots may still be in flight
-    for (uint32_t i = ld > (uint32_t)C::NS ? ld - C::NS : 0; i < ld; ++i)
-      q_drain(&m->full[i % C::NS], (i / C::NS) & 1u);
+    for (uint32_t i = tiles > (uint32_t)NS ? tiles - NS : 0; i < tiles; ++i) q_drain(&full[i % NS], (i / NS) & 1u);
 }
 
 // Two weights in three e5m2 parts: as fp16, of which an e5m2 value is the upper

@@ -17,7 +17,7 @@
 // Sums stay in their threads until the unit ends.
 //
 // Units, runs, roles, waits and the joining kernel are qattend.cu's, with two S
-// and two P buffers, and one warp for the queries.
+// and two P buffers, and the row warps cutting the queries between units.
 #include <math.h>
 
 #include "qattend.cuh"
@@ -31,20 +31,21 @@ struct DCfg {
   static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
   static constexpr int CHUNKS = D / ROWB;           // column spans
   // (12 warps have 168 registers a thread, 13 would have 128)
-  static constexpr int ROW_WARPS = 8, LOADER = 8, ISSUE_S = 9, ISSUE_O = 10, QUERY = 11, WARPS = 12, THREADS = WARPS * 32;
+  static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11, WARPS = 12, THREADS = WARPS * 32;
   static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   // rows, and columns of a product: three parts of them (the columns behind those are not looked at)
   static constexpr int R = 2 * RT, N = (3 * R + 15) / 16 * 16;
   static constexpr int Q_SPAN = N * ROWB, P_TILE = N * QT_TILE;
-  static constexpr int NS = D == 256 ? 5 : D == 128 ? 10 : 16;  // ring slots
-  // Slots of the scales' ring, as in qattend.cu; here a K used up says that all row
-  // warps have read the scores of two tiles before it.  They are past the scales of x - 5,
-  // x - 8, x - 11.
-  static constexpr int SCALES = NS == 16 ? 16 : 8;
+  static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 3 : NSK;  // ring slots of K, of V
+  // Slots of the scales' ring.  Those of tile x are asked for when K of tile x - NSK has been
+  // used up, so that all row warps have read the scores of the tile two before that: they
+  // are past the scales of tile x - NSK - 3.
+  static constexpr int SCALES = D == 64 ? 16 : 8;
+  static_assert(SCALES >= NSK + 3, "scales");
   static constexpr int OFF_P = CHUNKS * Q_SPAN;
   static constexpr int OFF_RING = OFF_P + 2 * P_TILE;
-  static constexpr int OFF_MISC = OFF_RING + NS * SLOT;
+  static constexpr int OFF_V = OFF_RING + NSK * SLOT, OFF_MISC = OFF_V + NSV * SLOT;
   static constexpr int MISC = D == 64 ? 4096 : 3072, SMEM = OFF_MISC + MISC;
   static_assert(SMEM <= 227 * 1024 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "shared memory");
   // Tensor memory columns: two S tiles, O of each 128 values of a head.
@@ -69,17 +70,91 @@ struct DMisc : QRing<C> {
   };
 };
 
-// Four columns at a time of a warp's lanes, N in all.
+// N columns of a warp's lanes (N a multiple of 4), as few instructions as do.
 template <int N>
 __device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[N]) {
+  constexpr int W = N % 16 == 0 ? 16 : N % 8 == 0 ? 8 : 4;
+  constexpr int HEAD = N > 16 && W == 4 ? 16 : 0;
+  if constexpr (HEAD > 0) {
+    uint32_t x[16];
+    ptx::tmem_ld(taddr, x);
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    uint32_t x[4];
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]);
+  }
+#pragma unroll
+  for (int i = HEAD; i < N; i += W) {
+    uint32_t x[W];
     ptx::tmem_ld(taddr + i, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[i + k] = __uint_as_float(x[k]);
+    for (int k = 0; k < W; ++k) v[i + k] = __uint_as_float(x[k]);
   }
 }
+
+// The sum (or maximum) over a warp's lanes of N values each, N a multiple of 4: two steps
+// hand half of the values to the other lane, so that 1.5 N exchanges do instead of 5 N.
+// Lane l is left with those of rows (l / 8) * N / 4 .. of N / 4.
+template <int N, typename F>
+__device__ __forceinline__ void fold(const float (&v)[N], float (&out)[N / 4], F op) {
+  const int lane = threadIdx.x & 31;
+  float h[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const bool up = lane & 16;
+    const float keep = up ? v[N / 2 + i] : v[i], give = up ? v[i] : v[N / 2 + i];
+    h[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const bool up = lane & 8;
+    const float keep = up ? h[N / 4 + i] : h[i], give = up ? h[i] : h[N / 4 + i];
+    out[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) out[i] = op(out[i], __shfl_xor_sync(0xffffffffu, out[i], o));
+  }
+}
+
+// What a warp holds of a unit's queries: rows (u * warps + its own) * AT_ONCE + lane / LANES, u = 0 .. UPW - 1.
+template <typename C, int D, int WARPS>
+struct Queries {
+  static constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+  static constexpr int UPW = (C::R + WARPS * AT_ONCE - 1) / (WARPS * AT_ONCE);
+  uint4 x[UPW];
+  __device__ __forceinline__ static int row(int u, int warp) {
+    return (u * WARPS + warp) * AT_ONCE + (int)(threadIdx.x & 31) / LANES;
+  }
+  // (rows that are not there: zeros)
+  __device__ __forceinline__ void load(const AttendArgs &a, const QWalk<C> &w, int warp) {
+    const int rows = w.tokens() * a.G, d = (int)(threadIdx.x & 31) % LANES * 8;
+#pragma unroll
+    for (int u = 0; u < UPW; ++u) {
+      const int r = row(u, warp), token = r * a.g_mul >> 16;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows)
+        x[u] = *reinterpret_cast<const uint4 *>(
+            a.x + ((size_t)(w.s.lo + w.token0() + token) * a.Hq + w.g * a.G + (r - token * a.G)) * D + d);
+    }
+  }
+  __device__ __forceinline__ int cut(int u, int fp16, uint2 (&part)[3]) const {
+    float f[8];
+    if (fp16)
+      unpack8<true>(x[u], f);
+    else
+      unpack8<false>(x[u], f);
+    return cut_row<LANES, 3>(f, part);
+  }
+  // a row's parts to the operand's place, its factor to q_f
+  __device__ __forceinline__ static void store(uint8_t *q_tile, float *q_f, int r, const uint2 (&part)[3], float factor) {
+    const int d = (int)(threadIdx.x & 31) % LANES * 8;
+    if (r >= C::R) return;
+    uint32_t off = r * C::ROWB + d % C::ROWB;
+    off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
+    uint8_t *to = q_tile + d / C::ROWB * C::Q_SPAN + off;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)  // (R is a multiple of 8: the same swizzle)
+      *reinterpret_cast<uint2 *>(to + k * C::R * C::ROWB) = part[k];
+    if (d == 0) q_f[r] = factor;
+  }
+};
 
 template <int D, int RT>
 __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
@@ -102,27 +177,28 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     }
     return;
   }
-  if (warp == C::LOADER && lane == 0) {
-    ptx::prefetch_tmap(&maps.k);
-    ptx::prefetch_tmap(&maps.v);
-  }
+  if (warp == C::LOAD_K && lane == 0) ptx::prefetch_tmap(&maps.k);
+  if (warp == C::LOAD_V && lane == 0) ptx::prefetch_tmap(&maps.v);
   if (warp == C::ISSUE_S) {
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
   }
-  if (tid >= 32 && tid < 32 + C::NS) {
-    ptx::mbar_init(&m->full[tid - 32], 1);
-    ptx::mbar_init(&m->empty[tid - 32], 1);
+  if (tid >= 32 && tid < 32 + C::NSK) {
+    ptx::mbar_init(&m->k_full[tid - 32], 1);
+    ptx::mbar_init(&m->k_empty[tid - 32], 1);
+    ptx::fence_mbar_init();
+  } else if (tid >= 48 && tid < 48 + C::NSV) {
+    ptx::mbar_init(&m->v_full[tid - 48], 1);
+    ptx::mbar_init(&m->v_empty[tid - 48], 1);
     ptx::fence_mbar_init();
   } else if (tid >= 64 && tid < 64 + C::SCALES) {
-    ptx::mbar_init(&m->sc_full[tid - 64], 1);
+    ptx::mbar_init(&m->sc_full[tid - 64], 16);
     ptx::fence_mbar_init();
   } else if (tid >= 128 && tid < 128 + 2 * RT) {
     m->base[0][tid - 128] = INFINITY;
   } else if (tid == 96) {
     m->abort_flag = 0;
-    ptx::mbar_init(&m->q_full, 1);
-    ptx::mbar_init(&m->q_free, 1);
+    ptx::mbar_init(&m->q_full, C::ROW_WARPS);
     ptx::mbar_init(&m->final_bar, 2);
     ptx::mbar_init(&m->o_free, C::ROW_WARPS);
     for (int i = 0; i < 4; ++i) m->nonfinite[i] = -1;
@@ -149,28 +225,27 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     return;
   }
   QWalk<C> w(a, m->b0, m->s0, m->off0, count);
-  uint8_t *ring = smem + C::OFF_RING, *p_tiles = smem + C::OFF_P;
+  uint8_t *k_ring = smem + C::OFF_RING, *v_ring = smem + C::OFF_V, *p_tiles = smem + C::OFF_P;
   int32_t *status = c.status;
 
-  if (warp == C::LOADER) {
-    load_tiles<C>(maps, a, m, w, ring);
+  if (warp == C::LOAD_K) {
+    load_tiles<C, false>(&maps.k, a, m, w, k_ring);
+  } else if (warp == C::LOAD_V) {
+    load_tiles<C, true>(&maps.v, a, m, w, v_ring);
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
     const uint32_t id_s = ptx::idesc_f8(C::N, false, false, false, false), id_o = ptx::idesc_f8(C::N, false, true, true, false);
     const uint64_t qd = ptx::sdesc_rows(ptx::smem_u32(smem), C::ROWB, 16);
-    uint32_t ld = 0, units = 0, jj = 0;  // jj: running tile count
+    uint32_t units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
-    auto scores = [&](uint32_t pos, uint32_t t, bool first) {  // S^T of running tile t from the K tile at load `pos`
-      const uint32_t slot = pos % C::NS;
-      if (t >= 2 && !q_wait_warp(&m->s_free[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-      // What the slot held before has been loaded: a K by an earlier wait here, a V
-      // of tile t - 4 or before since the row warps, at tile t - 2, have waited for its product.  A
-      // unit's first slot may follow the last unit's V of tile t - 3:
-      if (first && t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) return false;
-      if (!q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status)) return false;
+    auto scores = [&](uint32_t t) {  // S^T of running tile t
+      const uint32_t slot = t % C::NSK;
+      if ((t >= 2 && !q_wait_warp(&m->s_free[t & 1], ((t - 2) >> 1) & 1u, m, status)) ||
+          !q_wait_warp(&m->k_full[slot], (t / C::NSK) & 1u, m, status))
+        return false;
       ptx::tc_fence_after();
-      const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, 16);
+      const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(k_ring + slot * C::SLOT), C::ROWB, 16);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int ch = 0; ch < C::CHUNKS; ++ch)
@@ -178,22 +253,22 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           for (int i = 0; i < C::ROWB / 32; ++i)
             ptx::mma_ss_f8(tmem + (t & 1) * C::N, kd + (ch * C::SPAN + i * 32) / 16,
                              qd + (ch * C::Q_SPAN + i * 32) / 16, id_s, (ch | i) != 0);
-        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->k_empty[slot]);
         ptx::mma_commit(&m->s_full[t & 1]);
       }
       __syncwarp();
       return true;
     };
-    auto values = [&](uint32_t pos, uint32_t t, bool first) {  // O^T += V^T P^T of running tile t
-      const uint32_t slot = pos % C::NS;
+    auto values = [&](uint32_t t, bool first) {  // O^T += V^T P^T of running tile t
+      const uint32_t slot = t % C::NSV;
       if (!q_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
           (first && units > 0 && !q_wait_warp(&m->o_free, (units - 1) & 1u, m, status)) ||
-          !q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status))
+          !q_wait_warp(&m->v_full[slot], (t / C::NSV) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
       const uint64_t pd = ptx::sdesc_rows(ptx::smem_u32(p_tiles + (t & 1) * C::P_TILE), 128, 16);
       // (heads of 64 values: the product's upper 64 rows are the lower ones again)
-      const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(ring + slot * C::SLOT), C::ROWB, D == 64 ? 0 : C::SPAN);
+      const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(v_ring + slot * C::SLOT), C::ROWB, D == 64 ? 0 : C::SPAN);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int ot = 0; ot < C::O_TILES; ++ot)
@@ -201,83 +276,32 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           for (int i = 0; i < QT_TILE / 32; ++i)
             ptx::mma_ss_f8(tmem + C::O_COL + ot * C::N, vd + (ot * C::SPAN + i * 32 * C::ROWB) / 16, pd + i * 32 / 16,
                              id_o, !first || i > 0);
-        ptx::mma_commit(&m->empty[slot]);
+        ptx::mma_commit(&m->v_empty[slot]);
         ptx::mma_commit(&m->pv_done[t & 1]);
       }
       __syncwarp();
       return true;
     };
     while (ok && w.next()) {
-      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(ld + k_at(0), jj, true);
+      if (does_s) ok = q_wait_warp(&m->q_full, units & 1u, m, status) && scores(jj);
       for (int j = 0; ok && j < w.n; ++j, ++jj) {
-        if (does_s) {
-          if (j + 1 < w.n) ok = scores(ld + k_at(j + 1), jj + 1, false);
-          // the unit's last scores are under way
-          if (ok && j + 1 == max(1, w.n - 1) && ptx::elect_one()) ptx::mma_commit(&m->q_free);
-          __syncwarp();
-        } else {
-          ok = values(ld + v_at(j, w.n), jj, j == 0);
-        }
+        if (!does_s)
+          ok = values(jj, j == 0);
+        else if (j + 1 < w.n)
+          ok = scores(jj + 1);
       }
-      ld += 2 * w.n;
       ++units;
     }
     __syncwarp();
     if (ptx::elect_one()) ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
     __syncwarp();
     q_drain(&m->final_bar, 0);
-  } else if (warp >= C::QUERY) {
-    // -------------------------------------------------------------- queries
-    constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;  // of a row; rows a warp cuts at once
-    constexpr int AHEAD = C::R / AT_ONCE % 8 == 0 ? 8 : C::R / AT_ONCE % 4 == 0 ? 4 : 2;  // loads in flight
-    static_assert(C::R % (AHEAD * AT_ONCE) == 0, "no rows behind the last");
-    const int d = lane % LANES * 8;
-    uint32_t units = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      // the last unit's scores are done
-      if (units > 0 && !(ok = q_wait_warp(&m->q_free, (units - 1) & 1u, m, status))) break;
-      const int rows = w.tokens() * a.G;
-      for (int r0 = lane / LANES; r0 < C::R; r0 += AHEAD * AT_ONCE) {
-        uint4 x[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int r = r0 + u * AT_ONCE, token = r * a.g_mul >> 16;
-          x[u] = make_uint4(0u, 0u, 0u, 0u);  // (rows that are not there: zeros)
-          if (r < rows)
-            x[u] = *reinterpret_cast<const uint4 *>(
-                a.x + ((size_t)(w.s.lo + w.token0() + token) * a.Hq + w.g * a.G + (r - token * a.G)) * D + d);
-        }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int r = r0 + u * AT_ONCE;
-          float f[8];
-          if (fp16)
-            unpack8<true>(x[u], f);
-          else
-            unpack8<false>(x[u], f);
-          uint2 part[3];
-          const int e = cut_row<LANES, 3>(f, part);
-          uint32_t off = r * C::ROWB + d % C::ROWB;
-          off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
-          uint8_t *to = smem + d / C::ROWB * C::Q_SPAN + off;
-#pragma unroll
-          for (int k = 0; k < 3; ++k)  // (R is a multiple of 8: the same swizzle)
-            *reinterpret_cast<uint2 *>(to + k * C::R * C::ROWB) = part[k];
-          if (d == 0) m->q_f[units & 3][r] = exp2_int(e) * a.scale_log2;
-        }
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&m->q_full);
-      ++units;
-    }
   } else {
     // ----------------------------------------------------------------- rows
     const int half = warp >> 2, quad = warp & 3, at = quad * 32 + lane;  // this thread's position of a tile, value of O
     const int r0 = half * RT;                                            // its first row
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + r0;
-    uint32_t ld = 0, jj = 0, meets = 0;
+    uint32_t jj = 0, meets = 0;
     int units = 0;
     bool ok = true;
     SplitDesc split{};
@@ -303,12 +327,11 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
       // sums over the half's positions
+      float mine4[RT / 4];
+      fold(sum, mine4, [](float x, float y) { return x + y; });
+      if ((lane & 7) == 0)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        if (lane == 0) m->most[half][quad][i] = sum[i];
-      }
+        for (int i = 0; i < RT / 4; ++i) m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
       if (!meet()) return false;
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -360,7 +383,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
             }
           }
           uint16_t *out = a.o + ((size_t)(un.lo + un.token0) * a.Hq + un.g * a.G) * D + d;
-          float *part = a.j.part + ((pslot * (D / 4) + d / 4) * a.j.rows_cap) * 4 + d % 4;
+          float *part = a.j.part + pslot * a.j.rows_cap * D + d;
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const int r = r0 + i, token = r * a.g_mul >> 16;
@@ -370,7 +393,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
               out[((size_t)token * a.Hq + (r - token * a.G)) * D] =
                   fp16 ? __half_as_ushort(__float2half_rn(y)) : f32_to_bf16(y);
             } else {
-              part[r * 4] = o[i];
+              part[(size_t)r * D] = o[i];
             }
           }
         }
@@ -380,8 +403,20 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     };
     while (ok) {
       const bool more = w.next();
+      using Q = Queries<C, D, C::ROW_WARPS>;
+      Q q;
+      if (more) q.load(a, w, warp);  // (on their way during finish())
       if (un.n > 0) ok = finish();
       if (!more || !ok) break;
+      // the last unit's scores are done: this warp has read them
+#pragma unroll
+      for (int u = 0; u < Q::UPW; ++u) {
+        uint2 part[3];
+        const int e = q.cut(u, fp16, part);
+        Q::store(smem, m->q_f[units & 3], Q::row(u, warp), part, exp2_int(e) * a.scale_log2);
+      }
+      ptx::fence_proxy_async_smem();
+      arrive(&m->q_full);
       const int pos0 = w.s.L - w.s.n + w.token0();
       un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, pos0, 0, 0, end - w.left};
       un.all_see = max(0, pos0 + 1);
@@ -402,12 +437,12 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         ptx::tc_fence_after();
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
-          const uint32_t pos = ld + v_at(j, un.n), slot = pos % C::NS;
-          // the slots' last loads have been used up (else their barriers could still be a phase behind)
+          const uint32_t slot = jj % C::NSV;
+          // the slot's last load has been used up (else its barrier could still be a phase behind)
           if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
-          ok = ok && q_wait_warp(&m->full[slot], (pos / C::NS) & 1u, m, status);
+          ok = ok && q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status);
           if (!ok) break;
-          if (clear_edge<C, C::ROW_WARPS * 32>(ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
+          if (clear_edge<C, C::ROW_WARPS * 32>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
             m->nonfinite[units & 3] = units;
           __syncwarp();
         }
@@ -441,19 +476,24 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           for (int i = 0; i < RT; ++i)
             if (r0 + i >= un.rows || first + ((r0 + i) * a.g_mul >> 16) < 0) s[i] = -INFINITY;
         }
-        // what it is over the running maximum; infinite where that is still to be found
+        // what they are over the running maximum; infinite where that is still to be found
         bool grows = vmax > ref * QT_WIDER;
         auto over_maximum = [&]() {
+          float most = -INFINITY;
 #pragma unroll
           for (int i = 0; i < RT; i += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(&m->base[half][i]);
             const float base[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[i + k] = s[i + k] == -INFINITY ? -INFINITY : s[i + k] + base[k];
-              grows |= x[i + k] > QT_TOP + QT_SLACK;
-            }
+            for (int k = 0; k < 4; ++k) x[i + k] = s[i + k] + base[k];
           }
+          if (edge)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+              if (s[i] == -INFINITY) x[i] = -INFINITY;  // (and not NaN before the first score)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) most = fmaxf(most, x[i]);
+          grows |= most > QT_TOP + QT_SLACK;
         };
         over_maximum();
         grows = __any_sync(0xffffffffu, grows);
@@ -470,13 +510,11 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
             v_f = ref / vmax;
             ref = vmax;
           }
+          float mine4[RT / 4];
+          fold(s, mine4, [](float x, float y) { return fmaxf(x, y); });
+          if ((lane & 7) == 0)
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            float most = s[i];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            if (lane == 0) m->most[half][quad][i] = most;
-          }
+            for (int i = 0; i < RT / 4; ++i) m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
           if (!(ok = meet())) break;
           float f[RT];
 #pragma unroll
@@ -484,7 +522,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
             const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
                                      fmaxf(m->most[half][2][i], m->most[half][3][i]));
             const float was = m->base[half][i];
-            const bool up = most + was > QT_TOP + QT_SLACK;  // (of a row that has seen nothing yet: any score)
+            const bool up = most > -INFINITY && most + was > QT_TOP + QT_SLACK;  // (of a row that has seen nothing yet: any score)
             f[i] = up ? ex2(QT_TOP - most - was) : 1.f;
             sum[i] *= f[i];
             f[i] *= v_f;
@@ -542,7 +580,6 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
       }
-      ld += 2 * un.n;
       ++units;
     }
     if (tid == 0) a.j.desc[cta] = split;

@@ -1021,6 +1021,7 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   a.scale_log2 = scale * 1.4426950408889634f;
   size_t ml_at, part_at;
   moe::tree_ws(D, ctas, a.j.rows_cap, &ml_at, &part_at);
+  a.j.row_major = 0;
   a.j.o = a.o;
   a.j.Hq = Hq;
   a.j.G = G;
