@@ -22,6 +22,7 @@ struct JoinArgs {
   uint16_t *o;      // [rows][Hq][D]
   int rows_cap;     // rows of a unit at most
   int row_major;
+  int most_groups;  // threads that share a unit's values at most: 8 or 32
   int Hq, G;        // query heads, and of a KV head
 };
 
@@ -53,7 +54,9 @@ constexpr int JOIN_THREADS = 256;
 // (One group always, this rule, eight always, whole calls in us: 1 node over 3,000
 // positions 17.4, 14.8, 14.4; 4 x 5 over 9,000 29.8, 25.0, 24.3; 24 x 5 over 6,000
 // 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.)
-__device__ __forceinline__ int part_groups(int parts) { return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : 8; }
+__device__ __forceinline__ int part_groups(int parts, int most) {
+  return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : parts <= 32 ? 8 : most;
+}
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ JoinArgs a, int ctas) {
@@ -69,10 +72,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   constexpr int PER = (MAXU + JOIN_THREADS - 1) / JOIN_THREADS;
   SplitDesc d[PER];
   auto items_of = [&](const SplitDesc &x) {
-    const int each = JOIN_THREADS / part_groups(x.parts);
+    const int each = JOIN_THREADS / part_groups(x.parts, a.most_groups);
     return (cells + each - 1) / each;
   };
-  int packed = 0;  // units << 20 | items: at most 320, and 320 * 16 * 128 / 32 below 2^15 of them
+  int packed = 0;  // units << 20 | items: at most 320, and 320 * 16 * 128 / 8 below 2^17 of them
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = tid * PER + i;
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     for (int step = 256; step; step >>= 1)
       if (u + step < units && item_s[u + step] <= item) u += step;
     const SplitDesc ds = desc_s[u];
-    const int c0 = cta_s[u], groups = part_groups(ds.parts), each = JOIN_THREADS / groups, grp = tid / each;
+    const int c0 = cta_s[u], groups = part_groups(ds.parts, a.most_groups), each = JOIN_THREADS / groups, grp = tid / each;
     const int e = (item - item_s[u]) * each + tid % each, c4 = e / a.rows_cap * 4, r = e % a.rows_cap;
     const bool in = e < cells && r < ds.rows;
     float M = -INFINITY, den = 0.f;

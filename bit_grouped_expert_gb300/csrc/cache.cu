@@ -152,7 +152,10 @@ __global__ void __launch_bounds__(THREADS) append_plan_kernel(const __grid_const
     c.lens[slot] = L + n;
     if (cow) atomicSub(&c.refs[old_page], 1);
   }
-  if (b == 0) *a.rows = rows;
+  if (b == 0) {
+    a.rows[0] = rows;
+    a.rows[1] = 0;
+  }
   __syncthreads();
   for (int k = b; k < total; k += THREADS) {
     const int s = segment_of(first_s, a.B, k), page = a.pages[k];

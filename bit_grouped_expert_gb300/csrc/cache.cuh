@@ -87,7 +87,7 @@ struct AppendArgs {
   const uint16_t *k_new, *v_new;
   const int32_t *slots, *offsets, *n_keep, *path;
   int path_stride, B, n_rows;
-  int32_t *rows;   // [1] rows to copy, 0 if the call changes nothing
+  int32_t *rows;   // [2] rows to copy, 0 if the call changes nothing; jobs handed out (0 at first)
   AppendSeg *seg;  // [B]
   int32_t *pages;  // the pages found
   int per_job;     // layers a warp copies of a row

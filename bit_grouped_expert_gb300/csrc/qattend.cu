@@ -406,10 +406,9 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
           const uint32_t slot = jj % C::NSV;
-          // the slot's last load has been used up (else its barrier could still be a phase behind)
-          if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
-          ok = ok && q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status);
-          if (!ok) break;
+          // (the slot's last load, of tile jj - 3 or before, has been used up: its phase has passed)
+          static_assert(C::NSV >= 3, "V slots");
+          if (!(ok = q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status))) break;
           if (clear_edge<C, QT_ROWS * 2>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
             m->nonfinite[units & 3] = units;
           __syncwarp();
@@ -639,6 +638,7 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
   a.j.ml = moe::ws_ptr<float>(ws_d, ml_at);
   a.j.part = moe::ws_ptr<float>(ws_d, part_at);
   a.j.row_major = a.j.rows_cap <= moe::QD_MOST;
+  a.j.most_groups = 32;
   a.j.o = a.o;
   a.j.Hq = Hq;
   a.j.G = G;

@@ -316,7 +316,9 @@ __device__ __forceinline__ void cut_weights(float x, float y, uint32_t &hi, uint
   hi = half_pair<true>(x, y);
   mid = minus(hi, hi & UPPER);
   const uint32_t rest = minus(mid, mid & UPPER);
-  lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw *>(&rest), __NV_SATFINITE, __NV_E5M2);
+  uint16_t last;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(last) : "r"(rest));
+  lo = last;
 }
 
 // A code that is NaN among the four of a word: 0x7F or 0xFF.

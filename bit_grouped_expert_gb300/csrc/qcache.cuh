@@ -1,7 +1,6 @@
 // Device view of the 8-bit paged KV cache (qcache.h) and its numbers.
 #pragma once
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "cache.cuh"
 #include "qcache.h"
@@ -16,11 +15,14 @@ struct QCacheView {
 
 // Two values' e4m3 codes (nearest, ties to even; beyond 448 the largest; NaN stays), the first in the low byte.
 __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+  uint16_t codes;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(codes) : "f"(hi), "f"(lo));
+  return codes;
 }
 // Two codes' values (exact in fp16).
 __device__ __forceinline__ float2 from_codes(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 

@@ -32,11 +32,14 @@ struct DCfg {
   static constexpr int CHUNKS = D / ROWB;           // column spans
   // (12 warps have 168 registers a thread, 13 would have 128)
   static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11, WARPS = 12, THREADS = WARPS * 32;
-  static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
+  // What a unit costs besides its tiles, in tiles (some 3.5 us: its first maxima, its queries, its result).
+  static constexpr int OVERHEAD = D == 256 ? 3 : 5;
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
-  // rows, and columns of a product: three parts of them (the columns behind those are not looked at)
-  static constexpr int R = 2 * RT, N = (3 * R + 15) / 16 * 16;
-  static constexpr int Q_SPAN = N * ROWB, P_TILE = N * QT_TILE;
+  // Rows, and columns of a product: a half's three parts side by side, so that what
+  // a thread reads of S and writes of P lies together (the columns behind them are not looked at).
+  static constexpr int R = 2 * RT, HALF = (3 * RT + 15) / 16 * 16, N = 2 * HALF;
+  __device__ static int column(int r, int part) { return r / RT * HALF + part * RT + r % RT; }
+  static constexpr int Q_SPAN = N * ROWB, P_TILE = QT_TILE * 128;
   static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 3 : NSK;  // ring slots of K, of V
   // Slots of the scales' ring.  Those of tile x are asked for when K of tile x - NSK has been
   // used up, so that all row warps have read the scores of the tile two before that: they
@@ -70,23 +73,15 @@ struct DMisc : QRing<C> {
   };
 };
 
-// N columns of a warp's lanes (N a multiple of 4), as few instructions as do.
+// N columns of a warp's lanes, a multiple of 16.
 template <int N>
-__device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[N]) {
-  constexpr int W = N % 16 == 0 ? 16 : N % 8 == 0 ? 8 : 4;
-  constexpr int HEAD = N > 16 && W == 4 ? 16 : 0;
-  if constexpr (HEAD > 0) {
+__device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16) {
     uint32_t x[16];
-    ptx::tmem_ld(taddr, x);
+    ptx::tmem_ld_x16(taddr + i, x);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[k]);
-  }
-#pragma unroll
-  for (int i = HEAD; i < N; i += W) {
-    uint32_t x[W];
-    ptx::tmem_ld(taddr + i, x);
-#pragma unroll
-    for (int k = 0; k < W; ++k) v[i + k] = __uint_as_float(x[k]);
+    for (int k = 0; k < 16; ++k) v[i + k] = x[k];
   }
 }
 
@@ -146,12 +141,12 @@ struct Queries {
   __device__ __forceinline__ static void store(uint8_t *q_tile, float *q_f, int r, const uint2 (&part)[3], float factor) {
     const int d = (int)(threadIdx.x & 31) % LANES * 8;
     if (r >= C::R) return;
-    uint32_t off = r * C::ROWB + d % C::ROWB;
-    off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
-    uint8_t *to = q_tile + d / C::ROWB * C::Q_SPAN + off;
 #pragma unroll
-    for (int k = 0; k < 3; ++k)  // (R is a multiple of 8: the same swizzle)
-      *reinterpret_cast<uint2 *>(to + k * C::R * C::ROWB) = part[k];
+    for (int k = 0; k < 3; ++k) {
+      uint32_t off = C::column(r, k) * C::ROWB + d % C::ROWB;
+      off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
+      *reinterpret_cast<uint2 *>(q_tile + d / C::ROWB * C::Q_SPAN + off) = part[k];
+    }
     if (d == 0) q_f[r] = factor;
   }
 };
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
-    const uint32_t id_s = ptx::idesc_f8(C::N, false, false, false, false), id_o = ptx::idesc_f8(C::N, false, true, true, false);
+    const uint32_t id_s = ptx::idesc_f8(C::N, false, false, false, false), id_o = ptx::idesc_f8(C::N, false, true, true, true);
     const uint64_t qd = ptx::sdesc_rows(ptx::smem_u32(smem), C::ROWB, 16);
     uint32_t units = 0, jj = 0;  // jj: running tile count
     bool ok = true;
@@ -266,7 +261,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           !q_wait_warp(&m->v_full[slot], (t / C::NSV) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
-      const uint64_t pd = ptx::sdesc_rows(ptx::smem_u32(p_tiles + (t & 1) * C::P_TILE), 128, 16);
+      const uint64_t pd = ptx::sdesc_rows(ptx::smem_u32(p_tiles + (t & 1) * C::P_TILE), 128, 16);  // a position's weights a row
       // (heads of 64 values: the product's upper 64 rows are the lower ones again)
       const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(v_ring + slot * C::SLOT), C::ROWB, D == 64 ? 0 : C::SPAN);
       if (ptx::elect_one()) {
@@ -274,8 +269,8 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         for (int ot = 0; ot < C::O_TILES; ++ot)
 #pragma unroll
           for (int i = 0; i < QT_TILE / 32; ++i)
-            ptx::mma_ss_f8(tmem + C::O_COL + ot * C::N, vd + (ot * C::SPAN + i * 32 * C::ROWB) / 16, pd + i * 32 / 16,
-                             id_o, !first || i > 0);
+            ptx::mma_ss_f8(tmem + C::O_COL + ot * C::N, vd + (ot * C::SPAN + i * 32 * C::ROWB) / 16,
+                           pd + i * 32 * 128 / 16, id_o, !first || i > 0);
         ptx::mma_commit(&m->v_empty[slot]);
         ptx::mma_commit(&m->pv_done[t & 1]);
       }
@@ -300,7 +295,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     // ----------------------------------------------------------------- rows
     const int half = warp >> 2, quad = warp & 3, at = quad * 32 + lane;  // this thread's position of a tile, value of O
     const int r0 = half * RT;                                            // its first row
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + r0;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * C::HALF;
     uint32_t jj = 0, meets = 0;
     int units = 0;
     bool ok = true;
@@ -321,8 +316,11 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       long long done;         // where this CTA's part ends in the count of all
     } un{};
     float sum[RT], ref = 0.f;
-    // The unit whose tiles were the last: its result is taken out of tensor
-    // memory while the next unit's first scores run.
+    // the sum of a row's three parts
+    auto three = [](const uint32_t(&v)[C::HALF], int i) {
+      return (__uint_as_float(v[i]) + __uint_as_float(v[RT + i])) + __uint_as_float(v[2 * RT + i]);
+    };
+    // The unit's result out of tensor memory, while the next unit's first scores run.
     auto finish = [&]() {
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       const size_t pslot = (size_t)2 * cta + (starts ? 1 : 0);
@@ -358,16 +356,14 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
 #pragma unroll 1
       for (int ot = 0; ot < C::O_TILES; ++ot) {
           const int d = ot * 128 + at;
-          const uint32_t col = lanes + C::O_COL + ot * C::N;
-          float o[RT], mid[RT], lo[RT];
+          uint32_t v[C::HALF];
           __syncwarp();
-          read_columns(col, o);
-          read_columns(col + C::R, mid);
-          read_columns(col + 2 * C::R, lo);
+          read_columns(lanes + C::O_COL + ot * C::N, v);
           ptx::tmem_wait_ld();
           if (D == 64 && at >= 64) continue;
+          float o[RT];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) o[i] = ((o[i] + mid[i]) + lo[i]) * ref;
+          for (int i = 0; i < RT; ++i) o[i] = three(v, i) * ref;
           if (fix) {  // codes NaN that were taken out of the edge's tiles, for the rows that see them
             const int p1 = min(un.some_see, (un.t0 + un.n) * QT_TILE);
             const int32_t *table = c.table + (size_t)un.slot * c.max_pages;
@@ -401,26 +397,29 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       arrive(&m->o_free);
       return true;
     };
-    while (ok) {
-      const bool more = w.next();
-      using Q = Queries<C, D, C::ROW_WARPS>;
-      Q q;
-      if (more) q.load(a, w, warp);  // (on their way during finish())
-      if (un.n > 0) ok = finish();
-      if (!more || !ok) break;
-      // the last unit's scores are done: this warp has read them
+    using Q = Queries<C, D, C::ROW_WARPS>;
+    auto cut_queries = [&](const Q &q, int unit) {
 #pragma unroll
       for (int u = 0; u < Q::UPW; ++u) {
         uint2 part[3];
         const int e = q.cut(u, fp16, part);
-        Q::store(smem, m->q_f[units & 3], Q::row(u, warp), part, exp2_int(e) * a.scale_log2);
+        Q::store(smem, m->q_f[unit & 3], Q::row(u, warp), part, exp2_int(e) * a.scale_log2);
       }
       ptx::fence_proxy_async_smem();
       arrive(&m->q_full);
+    };
+    bool more = w.next();
+    if (more) {
+      Q q;
+      q.load(a, w, warp);
+      cut_queries(q, 0);
+    }
+    while (ok && more) {
       const int pos0 = w.s.L - w.s.n + w.token0();
       un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, pos0, 0, 0, end - w.left};
       un.all_see = max(0, pos0 + 1);
       un.some_see = max(0, pos0 + w.tokens());
+      more = w.next();  // the unit behind this one
 #pragma unroll
       for (int i = 0; i < RT; ++i) sum[i] = 0.f;
       ref = 0.f;
@@ -438,10 +437,9 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
           const uint32_t slot = jj % C::NSV;
-          // the slot's last load has been used up (else its barrier could still be a phase behind)
-          if (jj >= 1) ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status);
-          ok = ok && q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status);
-          if (!ok) break;
+          // (the slot's last load, of tile jj - 3 or before, has been used up: its phase has passed)
+          static_assert(C::NSV >= 3, "V slots");
+          if (!(ok = q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status))) break;
           if (clear_edge<C, C::ROW_WARPS * 32>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
             m->nonfinite[units & 3] = units;
           __syncwarp();
@@ -454,22 +452,26 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         // this position's scores
         float s[RT], x[RT];
         {
-          float mid[RT], lo[RT];
-          const uint32_t col = lanes + (jj & 1) * C::N;
-          read_columns(col, s);
-          read_columns(col + C::R, mid);
-          read_columns(col + 2 * C::R, lo);
+          uint32_t v[C::HALF];
+          read_columns(lanes + (jj & 1) * C::N, v);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < RT; i += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(&m->q_f[units & 3][r0 + i]);
             const float qf[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[i + k] = ((s[i + k] + mid[i + k]) + lo[i + k]) * (qf[k] * ks);
+            for (int k = 0; k < 4; ++k) s[i + k] = three(v, i + k) * (qf[k] * ks);
           }
         }
         ptx::tc_fence_before();
         arrive(&m->s_free[jj & 1]);
+        // The unit's scores are done: the next one's queries may go to their place, so
+        // that its first scores run during this one's end.
+        if (j == un.n - 1 && more) {
+          Q q;
+          q.load(a, w, warp);
+          cut_queries(q, units + 1);
+        }
         if (edge) {
           const int first = pos0 - (t * QT_TILE + at);  // row r sees the position if -first <= its token
 #pragma unroll
@@ -536,17 +538,19 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
             if (!(ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < 3 * C::O_TILES; ++k) {
-              const uint32_t col = lanes + C::O_COL + k / 3 * C::N + k % 3 * C::R;
-              float v[RT];
+            for (int ot = 0; ot < C::O_TILES; ++ot) {
+              const uint32_t col = lanes + C::O_COL + ot * C::N;
+              uint32_t v[C::HALF];
               read_columns(col, v);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < RT; i += 4) {
-                uint32_t y[4];
+              for (int i = 0; i < 3 * RT; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[i % RT]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) y[q] = __float_as_uint(v[i + q] * f[i + q]);
-                ptx::tmem_st(col + i, y);
+              for (int i = 0; i < C::HALF; i += 16) {
+                uint32_t y[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) y[q] = v[i + q];
+                ptx::tmem_st_x16(col + i, y);
               }
             }
             ptx::tmem_wait_st();
@@ -554,33 +558,35 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           if (!(ok = meet())) break;  // the maxima are there
           over_maximum();
         }
-        // the weights, a byte a row and part: the lanes' bytes lie side by side
+        // the weights: this position's row of the tile, a byte a row and part
         const float vf = ref > 0.f ? vs / ref : 0.f;
-        uint8_t *p_tile = p_tiles + (jj & 1) * C::P_TILE;
+        uint32_t p_row[C::HALF / 4] = {};
 #pragma unroll
-        for (int i = 0; i < RT; i += 2) {
-          float p[2];
+        for (int i = 0; i < RT; i += 4) {
+          float p[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 4; ++k) {
             p[k] = ex2(x[i + k]);
             sum[i + k] += p[k];
           }
-          uint32_t hi, mid, lo;
-          cut_weights(p[0] * vf, p[1] * vf, hi, mid, lo);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int r = r0 + i + k;
-            uint8_t *to = p_tile + r * QT_TILE + (at ^ (r & 7) << 4);
-            to[0] = (uint8_t)(hi >> (16 * k + 8));
-            to[C::R * QT_TILE] = (uint8_t)(mid >> (16 * k + 8));
-            to[2 * C::R * QT_TILE] = (uint8_t)(lo >> 8 * k);
-          }
+          uint32_t h0, m0, l0, h1, m1, l1;
+          cut_weights(p[0] * vf, p[1] * vf, h0, m0, l0);
+          cut_weights(p[2] * vf, p[3] * vf, h1, m1, l1);
+          p_row[i / 4] = __byte_perm(h0, h1, 0x7531);
+          p_row[(RT + i) / 4] = __byte_perm(m0, m1, 0x7531);
+          p_row[(2 * RT + i) / 4] = __byte_perm(l0, l1, 0x5410);
         }
+        uint8_t *p_tile = p_tiles + (jj & 1) * C::P_TILE + at * 128;
+#pragma unroll
+        for (int i = 0; i < C::HALF; i += 16)
+          *reinterpret_cast<uint4 *>(p_tile + ((half * C::HALF + i) ^ (at & 7) << 4)) =
+              make_uint4(p_row[i / 4], p_row[i / 4 + 1], p_row[i / 4 + 2], p_row[i / 4 + 3]);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
       }
       ++units;
+      if (ok) ok = finish();
     }
     if (tid == 0) a.j.desc[cta] = split;
   }

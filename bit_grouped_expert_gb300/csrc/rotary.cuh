@@ -30,8 +30,14 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&x)[8]) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = half_value<FP16>(w[i] & 0xFFFFu);
-    x[2 * i + 1] = half_value<FP16>(w[i] >> 16);
+    if constexpr (FP16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
   }
 }
 template <bool FP16>
@@ -40,39 +46,31 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     half_pair<FP16>(x[6], x[7]));
 }
 
-// What a thread knows of its item: the two runs of eight values (a, then b),
-// whether they are turned, and how.
-struct RotaryItem {
-  int a, b;   // offsets in the head
-  bool turns, inter;
-  float c[8], s[8];  // cos and sin of pairs 8j .. 8j + 7 at the position set last
-  uint64_t rate[8];
-  float factor;
+// Cosines and sines of an item's pairs, 8 j .. 8 j + 7, at the position set last.
+struct RotaryPairs {
+  float c[8], s[8];
 
-  __device__ __forceinline__ RotaryItem(const attn_rotary_table *t, int j) {
-    turns = t && j < t->dim / 16;
-    inter = !turns || t->interleaved;
-    a = inter ? 16 * j : 8 * j;
-    b = inter ? 16 * j + 8 : t->dim / 2 + 8 * j;
-    factor = turns ? t->factor : 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rate[i] = turns ? t->turns[8 * j + i] : 0;
-  }
-  // p times the rate overflows by whole turns: what is left, read as signed, is
-  // the angle within half a turn to either side.
-  __device__ __forceinline__ void at(int p) {
-    if (!turns) return;
+  // p times the rate overflows by whole turns: what is left is the angle, whose
+  // nearest quarter turn is taken off as a whole number.  The rest, within an eighth of a
+  // turn, keeps 2^-24 of itself in fp32, and the series of sine and cosine to the
+  // ninth and tenth power are off by 2^-29 there.
+  template <typename F>
+  __device__ __forceinline__ void at(int p, F rate, float factor) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint64_t turn = (uint64_t)(int64_t)p * rate[i];
-      sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s[i], &c[i]);
-      c[i] *= factor;
-      s[i] *= factor;
+      const uint32_t turn = (uint32_t)((uint64_t)(int64_t)p * rate(i) >> 32);
+      const uint32_t quarter = (turn + 0x20000000u) >> 30;
+      const float x = (float)(int32_t)(turn - (quarter << 30)) * (6.283185307f * 0x1p-32f), xx = x * x;
+      const float v = fmaf(x * xx, fmaf(xx, fmaf(xx, fmaf(xx, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+      const float u =
+          fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+      const float f = quarter & 2 ? -factor : factor;  // half a turn on
+      c[i] = (quarter & 1 ? -v : u) * f;               // a quarter turn on
+      s[i] = (quarter & 1 ? u : v) * f;
     }
   }
-  // the values of runs a and b, turned where they are
-  __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8]) const {
-    if (!turns) return;
+  // the values of the item's two runs
+  __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], bool inter) const {
     if (inter) {
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
@@ -90,6 +88,39 @@ struct RotaryItem {
         y[i] = u * s[i] + y[i] * c[i];
       }
     }
+  }
+};
+
+// What a thread knows of its item: the two runs of eight values (a, then b),
+// whether they are turned, and how.
+struct RotaryItem : RotaryPairs {
+  int a, b;   // offsets in the head
+  bool turns, inter;
+  uint64_t rate[8];
+  float factor;
+
+  __device__ __forceinline__ RotaryItem(const attn_rotary_table *t, int j) {
+    turns = t && j < t->dim / 16;
+    inter = !turns || t->interleaved;
+    a = inter ? 16 * j : 8 * j;
+    b = inter ? 16 * j + 8 : t->dim / 2 + 8 * j;
+    factor = turns ? t->factor : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rate[i] = turns ? t->turns[8 * j + i] : 0;
+  }
+  __device__ __forceinline__ void at(int p) {
+    if (turns) RotaryPairs::at(p, [&](int i) { return rate[i]; }, factor);
+  }
+  // sixteen-bit values, turned and rounded once; those that are not turned keep their bits
+  template <bool FP16>
+  __device__ __forceinline__ void turn_halves(uint4 &p, uint4 &q) const {
+    if (!turns) return;
+    float x[8], y[8];
+    unpack8<FP16>(p, x);
+    unpack8<FP16>(q, y);
+    turn(x, y, inter);
+    p = pack8<FP16>(x);
+    q = pack8<FP16>(y);
   }
 };
 

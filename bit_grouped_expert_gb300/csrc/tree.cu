@@ -1022,6 +1022,7 @@ extern "C" moe_status attn_tree(const attn_cache *c, int32_t layer, const void *
   size_t ml_at, part_at;
   moe::tree_ws(D, ctas, a.j.rows_cap, &ml_at, &part_at);
   a.j.row_major = 0;
+  a.j.most_groups = 8;
   a.j.o = a.o;
   a.j.Hq = Hq;
   a.j.G = G;
