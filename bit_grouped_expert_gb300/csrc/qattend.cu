@@ -47,30 +47,33 @@ struct QCfg {
   static constexpr int CHUNKS = D / ROWB;           // column spans
   static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11, QUERY = 12, QUERY_WARPS = 4;
   static constexpr int WARPS = QUERY + QUERY_WARPS, THREADS = WARPS * 32;
-  static constexpr int OVERHEAD = 1;                // what a unit costs besides its tiles, in tiles
+  static constexpr int OVERHEAD = 3;                // what a unit costs besides its tiles, in tiles
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   static constexpr int Q_SPAN = QT_ROWS * ROWB, Q_PART = CHUNKS * Q_SPAN;
   static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 3 : NSK;  // ring slots of K, of V
   // Slots of the scales' ring.  Those of tile x are asked for when K of tile x - NSK has been
-  // used up, which was after the product with V of the tile two before that: all row warps
-  // are past the scales of tile x - NSK - 2.
+  // used up, which was after all row warps had read the scores of the tile before: they are past
+  // the scales of tile x - NSK - 2.
   static constexpr int SCALES = D == 256 ? 4 : D == 128 ? 8 : 16;
   static_assert(SCALES >= NSK + 2, "scales");
   static constexpr int OFF_RING = 2 * Q_PART;
   static constexpr int OFF_V = OFF_RING + NSK * SLOT, OFF_MISC = OFF_V + NSV * SLOT;
   static constexpr int SMEM = OFF_MISC + (D == 256 ? 3 : 4) * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  // Tensor memory columns: O, two S tiles; a tile's P, three parts of four weights a
-  // column, goes where its S was.
-  static constexpr uint32_t S_COL = D, P_PART = QT_TILE / 4, TMEM = 512;
-  static_assert(S_COL + 2 * QT_TILE <= TMEM && 3 * P_PART <= QT_TILE, "tensor memory");
+  // Tensor memory columns: O, one S tile, one P tile of three parts, four weights a
+  // column.  The rows take a whole S tile into registers first thing, so that the next one's
+  // MMAs run during the softmax, and write P last thing, when the product with the one
+  // before is done.  (Two tiles, each first S and then P, made the scores of a tile wait for the
+  // product of two before: 2.2 us a tile of 128 rows instead of 1.6.)
+  static constexpr uint32_t S_COL = D, P_COL = D + QT_TILE, P_PART = QT_TILE / 4, TMEM = 512;
+  static_assert(P_COL + 3 * P_PART <= TMEM, "tensor memory");
 };
 
 template <typename C>
 struct QMisc : QRing<C> {
-  uint64_t s_full[2], pair_bar[4];
+  uint64_t s_full, s_free, pair_bar[4];
   int nonfinite[4];                // by the unit's number: that unit, if NaN was taken out of its V
-  int8_t q_exp[3][QT_ROWS];        // by the unit's number (its scores run when the product with V of two tiles before is done)
+  int8_t q_exp[3][QT_ROWS];        // by the unit's number
   union {
     long long wsum[C::WARPS];
     float row[2][2][QT_ROWS];      // later: what the two threads of a row exchange, [turn][half]
@@ -124,11 +127,10 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     ptx::mbar_init(&m->final_bar, 2);
     ptx::fence_mbar_init();
   } else if (tid == 96) {
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&m->p_ready[i], C::ROW_WARPS);
-      ptx::mbar_init(&m->pv_done[i], 1);
-      ptx::mbar_init(&m->s_full[i], 1);
-    }
+    ptx::mbar_init(&m->p_ready[0], C::ROW_WARPS);
+    ptx::mbar_init(&m->pv_done[0], 1);
+    ptx::mbar_init(&m->s_full, 1);
+    ptx::mbar_init(&m->s_free, C::ROW_WARPS);
     ptx::mbar_init(&m->o_free, C::ROW_WARPS);
     for (int i = 0; i < 4; ++i) ptx::mbar_init(&m->pair_bar[i], 2);
     ptx::fence_mbar_init();
@@ -163,8 +165,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     bool ok = true;
     auto scores = [&](uint32_t t) {  // S of running tile t
       const uint32_t slot = t % C::NSK;
-      // P of tile t - 2 has been used up
-      if ((t >= 2 && !q_wait_warp(&m->pv_done[t & 1], ((t - 2) >> 1) & 1u, m, status)) ||
+      if ((t >= 1 && !q_wait_warp(&m->s_free, (t - 1) & 1u, m, status)) ||
           !q_wait_warp(&m->k_full[slot], (t / C::NSK) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
@@ -176,22 +177,22 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           for (int ch = 0; ch < C::CHUNKS; ++ch)
 #pragma unroll
             for (int i = 0; i < C::ROWB / 32; ++i)
-              ptx::mma_ss_f8(tmem + C::S_COL + (t & 1) * QT_TILE, qd + (part * C::Q_PART + ch * C::Q_SPAN + i * 32) / 16,
+              ptx::mma_ss_f8(tmem + C::S_COL, qd + (part * C::Q_PART + ch * C::Q_SPAN + i * 32) / 16,
                                kd + (ch * C::SPAN + i * 32) / 16, id_s, (part | ch | i) != 0);
         ptx::mma_commit(&m->k_empty[slot]);
-        ptx::mma_commit(&m->s_full[t & 1]);
+        ptx::mma_commit(&m->s_full);
       }
       __syncwarp();
       return true;
     };
     auto values = [&](uint32_t t, bool first) {  // O += P V of running tile t
       const uint32_t slot = t % C::NSV;
-      if (!q_wait_warp(&m->p_ready[t & 1], (t >> 1) & 1u, m, status) ||
+      if (!q_wait_warp(&m->p_ready[0], t & 1u, m, status) ||
           (first && units > 0 && !q_wait_warp(&m->o_free, (units - 1) & 1u, m, status)) ||
           !q_wait_warp(&m->v_full[slot], (t / C::NSV) & 1u, m, status))
         return false;
       ptx::tc_fence_after();
-      const uint32_t p_col = tmem + C::S_COL + (t & 1) * QT_TILE;
+      const uint32_t p_col = tmem + C::P_COL;
       const uint64_t vd = ptx::sdesc_rows(ptx::smem_u32(v_ring + slot * C::SLOT), C::ROWB, C::SPAN);
       if (ptx::elect_one()) {
 #pragma unroll
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
             ptx::mma_ts_f8(tmem, p_col + part * C::P_PART + 8 * i, vd + i * 32 * C::ROWB / 16, id_o,
                              !first || part > 0 || i > 0);
         ptx::mma_commit(&m->v_empty[slot]);
-        ptx::mma_commit(&m->pv_done[t & 1]);
+        ptx::mma_commit(&m->pv_done[0]);
       }
       __syncwarp();
       return true;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       // the last unit's scores are done
       if (units > 0 && !(ok = q_wait_warp(&m->q_free, (units - 1) & 1u, m, status))) break;
       const int rows = w.tokens() * a.G;
-      constexpr int AHEAD = 4;  // rows in flight
+      constexpr int AHEAD = 8;  // rows in flight
       for (int r0 = (qw * AT_ONCE + lane / LANES); r0 - lane / LANES < rows; r0 += AHEAD * C::QUERY_WARPS * AT_ONCE) {
         uint4 x[AHEAD];
 #pragma unroll
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     bool in = false;
     int own = -1;  // the last position that this row sees
     auto finish = [&]() {
-      if (!q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
+      if (!q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
       bool got;
       sum += exchange(sum, got);
@@ -396,17 +397,15 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       for (int j = 0; j < un.n; ++j, ++jj) {
         const int t = un.t0 + j;
         const bool edge = (t + 1) * QT_TILE > un.all_see;
-        // The scores are there (and so the product with V of two tiles before is done, and no
-        // wait below or in the other roles can take a phase of its barrier for the one two
-        // before); the scales are there (this warp has waited for the slot's phase before, SCALES tiles ago).
-        if (!(ok = q_wait_warp(&m->s_full[jj & 1], (jj >> 1) & 1u, &m->sc_full[jj % C::SCALES], (jj / C::SCALES) & 1u,
-                               &m->s_full[jj & 1], (jj >> 1) & 1u, m, status)))
+        // The scores are there, and the scales (this warp has waited for their slot's phase before, SCALES tiles ago).
+        if (!(ok = q_wait_warp(&m->s_full, jj & 1u, &m->sc_full[jj % C::SCALES], (jj / C::SCALES) & 1u, &m->s_full, jj & 1u,
+                               m, status)))
           break;
         ptx::tc_fence_after();
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
           const uint32_t slot = jj % C::NSV;
-          // (the slot's last load, of tile jj - 3 or before, has been used up: its phase has passed)
+          // (the slot's last load, of tile jj - 3 or before, has been used up: this warp has waited for the product)
           static_assert(C::NSV >= 3, "V slots");
           if (!(ok = q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status))) break;
           if (clear_edge<C, QT_ROWS * 2>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
@@ -415,12 +414,15 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         }
         if (active) {
           uint32_t x[COLS / 32][32];
-          const uint32_t s_col = lanes + C::S_COL + (jj & 1) * QT_TILE;
+          const uint32_t s_col = lanes + C::S_COL;
 #pragma unroll
           for (int h = 0; h < COLS / 32; ++h) ptx::tmem_ld_x32(s_col + half * COLS + 32 * h, x[h]);
+          // (before the arrival: once the next unit's scores have run, the exponents
+          // of one behind it may go to the same place)
           if (j == 0) q_scale = exp2_int(m->q_exp[units % 3][r]) * a.scale_log2;
           ptx::tmem_wait_ld();
           ptx::tc_fence_before();
+          arrive(&m->s_free);
           if (edge) {
             const int left = own - t * QT_TILE - half * COLS + 1;  // of this thread's columns
 #pragma unroll
@@ -441,10 +443,8 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           }
 #pragma unroll
           for (int g = 0; g < 8; ++g) vmax = fmaxf(vmax, sc[1][g]);
-          // (the two meet: both have their scores, and P may go where these were)
           tmax = fmaxf(tmax, exchange(tmax, ok));
           if (!ok) break;
-          ptx::tc_fence_after();
           const bool grows = in && tmax > mx + QT_SLACK, wider = vmax > ref * QT_WIDER;  // also the first a row sees
           if (__any_sync(0xffffffffu, grows || wider)) {
             float f = grows ? (mx == -INFINITY ? 0.f : exp2f(mx - tmax)) : 1.f;
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
               ref = vmax;
             }
             if (j > 0) {  // O holds the earlier tiles
-              if (!(ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
+              if (!(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
               ptx::tc_fence_after();
 #pragma unroll 1
               for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
@@ -489,12 +489,19 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
             part[2][i / 4] = __byte_perm(l0, l1, 0x5410);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          // the product with the tile before is done: its P has been used up
+          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
+          ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 3; ++k) ptx::tmem_st_x16(s_col + k * C::P_PART + half * (COLS / 4), part[k]);
+          for (int k = 0; k < 3; ++k) ptx::tmem_st_x16(lanes + C::P_COL + k * C::P_PART + half * (COLS / 4), part[k]);
           ptx::tmem_wait_st();
+        } else {
+          arrive(&m->s_free);
+          // (as the others: who is ahead of the product by two would take a phase of p_ready for the one before)
+          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
         }
         ptx::tc_fence_before();
-        arrive(&m->p_ready[jj & 1]);
+        arrive(&m->p_ready[0]);
       }
       ++units;
     }
