@@ -27,8 +27,9 @@
 //
 // Roles: eight warps own the rows, two load (TMA: pages by the table's numbers, K
 // with the pages' scales and V, each into a ring of its own), two issue the MMAs
-// of S (of the next tile during the softmax of this one) and of O, four cut the
-// next unit's queries.  Who waits on a barrier's parity must know that the phase
+// of S (of the next tile during the softmax of this one) and of O.  The queries' parts
+// are made beforehand, by a kernel of their own, so that they come as they are needed, by
+// TMA.  (Four warps that cut the next unit's took 12 us for 128 rows.)  Who waits on a barrier's parity must know that the phase
 // before has passed: the comments at the waits say from what.
 //
 // Every wait is bounded: after one second the kernel records
@@ -45,8 +46,8 @@ template <int D>
 struct QCfg {
   static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
   static constexpr int CHUNKS = D / ROWB;           // column spans
-  static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11, QUERY = 12, QUERY_WARPS = 4;
-  static constexpr int WARPS = QUERY + QUERY_WARPS, THREADS = WARPS * 32;
+  static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11;
+  static constexpr int WARPS = 12, THREADS = WARPS * 32;  // (168 registers a thread; 13 warps would have 128)
   static constexpr int OVERHEAD = 3;                // what a unit costs besides its tiles, in tiles
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   static constexpr int Q_SPAN = QT_ROWS * ROWB, Q_PART = CHUNKS * Q_SPAN;
@@ -73,7 +74,6 @@ template <typename C>
 struct QMisc : QRing<C> {
   uint64_t s_full, s_free, pair_bar[4];
   int nonfinite[4];                // by the unit's number: that unit, if NaN was taken out of its V
-  int8_t q_exp[3][QT_ROWS];        // by the unit's number
   union {
     long long wsum[C::WARPS];
     float row[2][2][QT_ROWS];      // later: what the two threads of a row exchange, [turn][half]
@@ -85,7 +85,8 @@ static_assert(sizeof(QMisc<QCfg<256>>) <= 3 * 1024 && sizeof(QMisc<QCfg<128>>) <
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
-    qattend_kernel(const __grid_constant__ QMaps maps, const __grid_constant__ AttendArgs a) {
+    qattend_kernel(const __grid_constant__ QMaps maps, const __grid_constant__ CUtensorMap q_map,
+                   const __grid_constant__ AttendArgs a) {
   using C = QCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
   QMisc<C> *m = reinterpret_cast<QMisc<C> *>(smem + C::OFF_MISC);
@@ -103,7 +104,10 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     return;
   }
   if (warp == C::LOAD_K && lane == 0) ptx::prefetch_tmap(&maps.k);
-  if (warp == C::LOAD_V && lane == 0) ptx::prefetch_tmap(&maps.v);
+  if (warp == C::LOAD_V && lane == 0) {
+    ptx::prefetch_tmap(&maps.v);
+    ptx::prefetch_tmap(&q_map);
+  }
   if (warp == C::ISSUE_S) {
     ptx::tmem_alloc(&m->tmem, C::TMEM);
     ptx::tmem_relinquish();
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
   } else if (tid == 64) {
     m->abort_flag = 0;
     for (int i = 0; i < 4; ++i) m->nonfinite[i] = -1;
-    ptx::mbar_init(&m->q_full, C::QUERY_WARPS);
+    ptx::mbar_init(&m->q_full, 1);
     ptx::mbar_init(&m->q_free, 1);
     ptx::mbar_init(&m->final_bar, 2);
     ptx::fence_mbar_init();
@@ -153,9 +157,22 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
   int32_t *status = c.status;
 
   if (warp == C::LOAD_K) {
-    load_tiles<C, false>(&maps.k, a, m, w, k_ring);
+    load_tiles<C, false>(&maps.k, a, m, w, k_ring, [](uint32_t) { return true; });
   } else if (warp == C::LOAD_V) {
-    load_tiles<C, true>(&maps.v, a, m, w, v_ring);
+    // a unit's queries, both parts, when the last unit's scores are done; then its V tiles
+    uint32_t issued = 0;
+    load_tiles<C, true>(&maps.v, a, m, w, v_ring, [&](uint32_t units) {
+      if (units > 0 && !q_wait_warp(&m->q_free, (units - 1) & 1u, m, status)) return false;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.j.rows_cap * 2 * D));
+        for (int ch = 0; ch < 2 * C::CHUNKS; ++ch)
+          ptx::tma_load_4d(smem + ch * C::Q_SPAN, &q_map, &m->q_full, 0, w.g * a.G, w.s.lo + w.token0(), ch);
+      }
+      __syncwarp();
+      ++issued;
+      return true;
+    });
+    if (lane == 0 && issued > 0) q_drain(&m->q_full, (issued - 1) & 1u);  // none on its way when the CTA ends
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
@@ -225,49 +242,6 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
     if (ptx::elect_one()) ptx::mma_commit(&m->final_bar);  // every MMA done before tensor memory is freed
     __syncwarp();
     q_drain(&m->final_bar, 0);
-  } else if (warp >= C::QUERY) {
-    // -------------------------------------------------------------- queries
-    constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;  // of a row; rows a warp cuts at once
-    const int qw = warp - C::QUERY, d = lane % LANES * 8;
-    uint32_t units = 0;
-    bool ok = true;
-    while (ok && w.next()) {
-      // the last unit's scores are done
-      if (units > 0 && !(ok = q_wait_warp(&m->q_free, (units - 1) & 1u, m, status))) break;
-      const int rows = w.tokens() * a.G;
-      constexpr int AHEAD = 8;  // rows in flight
-      for (int r0 = (qw * AT_ONCE + lane / LANES); r0 - lane / LANES < rows; r0 += AHEAD * C::QUERY_WARPS * AT_ONCE) {
-        uint4 x[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int r = r0 + u * C::QUERY_WARPS * AT_ONCE, token = r * a.g_mul >> 16;
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows)
-            x[u] = *reinterpret_cast<const uint4 *>(
-                a.x + ((size_t)(w.s.lo + w.token0() + token) * a.Hq + w.g * a.G + (r - token * a.G)) * D + d);
-        }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int r = r0 + u * C::QUERY_WARPS * AT_ONCE;
-          float f[8];
-          unpack8<FP16>(x[u], f);
-          uint2 part[2];
-          const int e = cut_row<LANES, 2>(f, part);
-          if (r < rows) {
-            uint32_t off = r * C::ROWB + d % C::ROWB;
-            off ^= (C::ROWB == 128 ? off >> 7 & 7 : off >> 7 & 3) << 4;
-            uint8_t *to = smem + d / C::ROWB * C::Q_SPAN + off;
-            *reinterpret_cast<uint2 *>(to) = part[0];
-            *reinterpret_cast<uint2 *>(to + C::Q_PART) = part[1];
-            if (d == 0) m->q_exp[units % 3][r] = (int8_t)e;
-          }
-        }
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&m->q_full);
-      ++units;
-    }
   } else {
     // ----------------------------------------------------------------- rows
     constexpr int COLS = QT_TILE / 2, OCOLS = D / 2;  // this thread's columns of S and of O
@@ -393,7 +367,8 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       const bool active = (warp & 3) * 32 < un.rows;  // the warp has rows
       mx = -INFINITY;
       sum = ref = 0.f;
-      float q_scale = 0.f;
+      const float q_scale =
+          in ? a.q_factor[(size_t)(un.lo + un.token0 + my_token) * a.Hq + un.g * a.G + my_head] * a.scale_log2 : 0.f;
       for (int j = 0; j < un.n; ++j, ++jj) {
         const int t = un.t0 + j;
         const bool edge = (t + 1) * QT_TILE > un.all_see;
@@ -417,9 +392,6 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
           const uint32_t s_col = lanes + C::S_COL;
 #pragma unroll
           for (int h = 0; h < COLS / 32; ++h) ptx::tmem_ld_x32(s_col + half * COLS + 32 * h, x[h]);
-          // (before the arrival: once the next unit's scores have run, the exponents
-          // of one behind it may go to the same place)
-          if (j == 0) q_scale = exp2_int(m->q_exp[units % 3][r]) * a.scale_log2;
           ptx::tmem_wait_ld();
           ptx::tc_fence_before();
           arrive(&m->s_free);
@@ -516,7 +488,40 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
   }
 }
 
+// Parts and factors of all queries: [row][head][part][D], a few heads a warp.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(256) cut_queries_kernel(const uint16_t *x, uint8_t *parts, float *factor, int n) {
+  constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+  start_dependent();
+  const int lane = threadIdx.x & 31, d = lane % LANES * 8;
+  for (int r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * AT_ONCE; r0 < n; r0 += gridDim.x * 8 * AT_ONCE) {
+    const int r = r0 + lane / LANES;
+    float f[8] = {};
+    if (r < n) unpack8<FP16>(*reinterpret_cast<const uint4 *>(x + (size_t)r * D + d), f);
+    uint2 part[2];
+    const int e = cut_row<LANES, 2>(f, part);
+    if (r >= n) continue;
+    *reinterpret_cast<uint2 *>(parts + (size_t)r * 2 * D + d) = part[0];
+    *reinterpret_cast<uint2 *>(parts + (size_t)r * 2 * D + D + d) = part[1];
+    if (d == 0) factor[r] = exp2_int(e);
+  }
+}
+
 // ---------------------------------------------------------------- host
+
+// A unit's queries: boxes of G heads x nt tokens of one column span of a part.
+bool parts_map(CUtensorMap *map, const void *p, int rows, int Hq, int D, int G, int nt) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int rowb = D < 128 ? D : 128;
+  cuuint64_t dims[4] = {(cuuint64_t)rowb, (cuuint64_t)Hq, (cuuint64_t)rows, (cuuint64_t)(2 * D / rowb)};
+  cuuint64_t strides[3] = {(cuuint64_t)2 * D, (cuuint64_t)Hq * 2 * D, (cuuint64_t)rowb};
+  cuuint32_t box[4] = {(cuuint32_t)rowb, (cuuint32_t)G, (cuuint32_t)nt, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, rowb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool code_map(CUtensorMap *map, const void *p, int64_t rows, int heads, int D, int box_rows, int box_spans) {
   auto enc = tensor_map_encoder();
@@ -541,32 +546,48 @@ int unit_tokens(int G, int max_rows) {
   return nt < max_rows ? nt : max_rows;
 }
 
-// Workspace: the split units, then maxima and sums, then partial outputs.
-size_t attend_ws(int D, int ctas, int rows_cap, size_t *ml_at, size_t *part_at) {
-  *ml_at = (size_t)ctas * sizeof(SplitDesc);
-  *part_at = *ml_at + ((size_t)2 * ctas * rows_cap * 8 + 255) / 256 * 256;
-  return *part_at + (size_t)2 * ctas * rows_cap * D * 4;
+// Workspace: the split units, then maxima and sums, then partial outputs; for whole
+// matrices also the queries' parts and factors.
+struct AttendSpace {
+  size_t ml, part, q_parts, q_factor, all;
+};
+AttendSpace attend_ws(int D, int ctas, int rows_cap, int64_t q_rows) {
+  AttendSpace w;
+  w.ml = (size_t)ctas * sizeof(SplitDesc);
+  w.part = w.ml + ((size_t)2 * ctas * rows_cap * 8 + 255) / 256 * 256;
+  w.q_parts = w.all = w.part + (size_t)2 * ctas * rows_cap * D * 4;
+  w.q_factor = w.q_parts + (size_t)q_rows * 2 * D;
+  if (rows_cap > QD_MOST) w.all = w.q_factor + (size_t)q_rows * 4;
+  return w;
 }
 
 template <int D, bool FP16>
-cudaError_t launch_rows(const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+cudaError_t launch_rows(const QMaps &maps, const AttendArgs &a, void *q_parts, float *q_factor, int ctas, cudaStream_t s) {
   using C = QCfg<D>;
+  CUtensorMap q_map;
+  if (!parts_map(&q_map, q_parts, a.n_rows, a.Hq, D, a.G, a.nt)) return cudaErrorInvalidValue;
   // per device and cheap: set on every call rather than remembered
   cudaError_t e = cudaFuncSetAttribute(qattend_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dep(prof_chain(MOE_KERNEL_ATTN_QCACHE), qattend_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s,
-                    maps, a);
+  const int n = a.n_rows * a.Hq, need = (n + 8 * (256 / D) - 1) / (8 * (256 / D));
+  e = launch_dep(prof_chain(0), cut_queries_kernel<D, FP16>, dim3(need < 152 * 8 ? need : 152 * 8), dim3(256), 0, s, a.x,
+                 static_cast<uint8_t *>(q_parts), q_factor, n);
+  if (e != cudaSuccess) return e;
+  const bool pdl = prof_quiet(MOE_KERNEL_ATTN_QCACHE);
+  prof_before(MOE_KERNEL_ATTN_QCACHE, s);
+  e = launch_dep(pdl, qattend_kernel<D, FP16>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, q_map, a);
+  prof_after(MOE_KERNEL_ATTN_QCACHE, s);
+  return e;
 }
 
 template <bool FP16>
-cudaError_t launch_attend(int D, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s) {
+cudaError_t launch_attend(int D, const QMaps &maps, const AttendArgs &a, void *q_parts, float *q_factor, int ctas,
+                          cudaStream_t s) {
   const bool quiet = prof_quiet(MOE_KERNEL_ATTN_QCACHE);
-  prof_before(MOE_KERNEL_ATTN_QCACHE, s);
   const cudaError_t e = a.j.rows_cap <= QD_MOST ? launch_attend_few(D, FP16, maps, a, ctas, s)
-                        : D == 64               ? launch_rows<64, FP16>(maps, a, ctas, s)
-                        : D == 128              ? launch_rows<128, FP16>(maps, a, ctas, s)
-                                                : launch_rows<256, FP16>(maps, a, ctas, s);
-  prof_after(MOE_KERNEL_ATTN_QCACHE, s);
+                        : D == 64               ? launch_rows<64, FP16>(maps, a, q_parts, q_factor, ctas, s)
+                        : D == 128              ? launch_rows<128, FP16>(maps, a, q_parts, q_factor, ctas, s)
+                                                : launch_rows<256, FP16>(maps, a, q_parts, q_factor, ctas, s);
   if (e != cudaSuccess) return e;
   auto join = D == 64 ? join_kernel<64, FP16> : D == 128 ? join_kernel<128, FP16> : join_kernel<256, FP16>;
   return launch_dep(quiet, join, dim3(ctas * 2), dim3(JOIN_THREADS), 0, s, a.j, ctas);
@@ -582,8 +603,8 @@ extern "C" size_t attn_qcache_attend_workspace_bytes(const attn_qcache *c, int32
       Hq % c->n_kv_heads || Hq / c->n_kv_heads > moe::QT_ROWS)
     return 0;
   const int G = Hq / c->n_kv_heads;
-  size_t ml, part;
-  return moe::attend_ws(c->head_dim, moe::attend_ctas(moe::QT_MAX_SMS), G * moe::unit_tokens(G, max_rows), &ml, &part);
+  return moe::attend_ws(c->head_dim, moe::attend_ctas(moe::QT_MAX_SMS), G * moe::unit_tokens(G, max_rows),
+                        (int64_t)n_rows * Hq).all;
 }
 
 extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, const void *q_d, int32_t dtype,
@@ -604,6 +625,7 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
   if (!q_d || !offsets_d || !ws_d || !o_d) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned16(q_d) || !aligned16(slots_d) || !aligned16(offsets_d) || !aligned16(ws_d) || !aligned16(o_d))
     return MOE_ERR_MISALIGNED;
+  if ((int64_t)n_rows * Hq > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t no = (size_t)n_rows * Hq * D * 2;
   const int64_t pool_rows = (int64_t)c->n_pages * c->page_size;
   const size_t layer_bytes = (size_t)pool_rows * c->n_kv_heads * D, np = c->n_layers * layer_bytes;
@@ -638,12 +660,14 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
   const uint8_t *k = static_cast<const uint8_t *>(c->k_d) + layer * layer_bytes;
   a.v_layer = static_cast<const uint8_t *>(c->v_d) + layer * layer_bytes;
   a.scale_log2 = scale * 1.4426950408889634f;
-  size_t ml_at, part_at;
   a.j.rows_cap = a.nt * G;
-  moe::attend_ws(D, ctas, a.j.rows_cap, &ml_at, &part_at);
+  const moe::AttendSpace w = moe::attend_ws(D, ctas, a.j.rows_cap, (int64_t)n_rows * Hq);
   a.j.desc = static_cast<moe::SplitDesc *>(ws_d);
-  a.j.ml = moe::ws_ptr<float>(ws_d, ml_at);
-  a.j.part = moe::ws_ptr<float>(ws_d, part_at);
+  a.j.ml = moe::ws_ptr<float>(ws_d, w.ml);
+  a.j.part = moe::ws_ptr<float>(ws_d, w.part);
+  void *q_parts = moe::ws_ptr<uint8_t>(ws_d, w.q_parts);
+  float *q_factor = moe::ws_ptr<float>(ws_d, w.q_factor);
+  a.q_factor = q_factor;
   a.j.row_major = a.j.rows_cap <= moe::QD_MOST;
   a.j.most_groups = 32;
   a.j.o = a.o;
@@ -655,7 +679,7 @@ extern "C" moe_status attn_qcache_attend(const attn_qcache *c, int32_t layer, co
       !moe::code_map(&maps.v, a.v_layer, pool_rows, c->n_kv_heads, D, a.page_box, spans))
     return moe::note_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = dtype == MOE_FP16 ? moe::launch_attend<true>(D, maps, a, ctas, s)
-                        : moe::launch_attend<false>(D, maps, a, ctas, s);
+  e = dtype == MOE_FP16 ? moe::launch_attend<true>(D, maps, a, q_parts, q_factor, ctas, s)
+                        : moe::launch_attend<false>(D, maps, a, q_parts, q_factor, ctas, s);
   return moe::note_cuda_error(e);
 }

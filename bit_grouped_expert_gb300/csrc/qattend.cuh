@@ -27,6 +27,7 @@ struct QMaps {
 struct AttendArgs {
   QCacheView q;
   const float *ks, *vs;  // the layer's scales
+  const float *q_factor; // [n_rows][Hq] what a query's parts are to be multiplied by (whole matrices)
   const uint16_t *x;
   const int32_t *slots, *offsets;
   uint16_t *o;
@@ -237,8 +238,10 @@ __device__ __forceinline__ long long find_run(const AttendArgs &a, M *m, long lo
 }
 
 // A loading warp: a unit's K tiles and the scales of K and V, or its V tiles, into their ring.
-template <typename C, bool V, typename M>
-__device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendArgs &a, M *m, QWalk<C> &w, uint8_t *ring) {
+// first: what to do before the first tile of each unit (false: give up).
+template <typename C, bool V, typename M, typename F>
+__device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendArgs &a, M *m, QWalk<C> &w, uint8_t *ring,
+                                           F first) {
   constexpr int NS = V ? C::NSV : C::NSK;
   const CacheView &c = a.q.c;
   const int lane = threadIdx.x & 31;
@@ -249,9 +252,10 @@ __device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendA
   const int box = whole ? 0 : lane / C::CHUNKS, span = whole ? 0 : lane % C::CHUNKS;
   const bool issues = whole ? lane == 0 : lane < boxes * C::CHUNKS;
   const int box_at = span * C::SPAN + box * a.page_box * C::ROWB;
-  uint32_t tiles = 0;
+  uint32_t tiles = 0, units = 0;
   bool ok = true;
   while (ok && w.next()) {
+    if (!(ok = first(units++))) break;
     const int z = w.g * C::CHUNKS + span, blocks = pages_of(sees_of(a, w.s, w.rt), c.page_shift);
     const int32_t *table = c.table + (size_t)w.s.slot * c.max_pages;
     // 64 table entries from block eb on, two a lane: the tile loaded next (8 blocks at most) begins in

@@ -224,9 +224,9 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
   int32_t *status = c.status;
 
   if (warp == C::LOAD_K) {
-    load_tiles<C, false>(&maps.k, a, m, w, k_ring);
+    load_tiles<C, false>(&maps.k, a, m, w, k_ring, [](uint32_t) { return true; });
   } else if (warp == C::LOAD_V) {
-    load_tiles<C, true>(&maps.v, a, m, w, v_ring);
+    load_tiles<C, true>(&maps.v, a, m, w, v_ring, [](uint32_t) { return true; });
   } else if (warp == C::ISSUE_S || warp == C::ISSUE_O) {
     // ----------------------------------------------------------------- MMAs
     const bool does_s = warp == C::ISSUE_S;
@@ -605,8 +605,11 @@ cudaError_t launch_few(bool fp16, const QMaps &maps, const AttendArgs &a, int ct
   // per device and cheap: set on every call rather than remembered
   cudaError_t e = cudaFuncSetAttribute(qdecode_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dep(prof_chain(MOE_KERNEL_ATTN_QCACHE), qdecode_kernel<D, RT>, dim3(ctas), dim3(C::THREADS), C::SMEM, s,
-                    maps, a, (int)fp16);
+  const bool chain = prof_chain(MOE_KERNEL_ATTN_QCACHE);
+  prof_before(MOE_KERNEL_ATTN_QCACHE, s);
+  e = launch_dep(chain, qdecode_kernel<D, RT>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, maps, a, (int)fp16);
+  prof_after(MOE_KERNEL_ATTN_QCACHE, s);
+  return e;
 }
 
 template <int D>
