@@ -390,7 +390,7 @@ __device__ __forceinline__ bool clear_edge(uint8_t *tile, int pos, int all_see, 
 }
 
 // qdecode.cu: the kernel for units of up to QD_MOST rows.
-constexpr int QD_MOST = 40;
+constexpr int QD_MOST = 16;
 cudaError_t launch_attend_few(int D, bool fp16, const QMaps &maps, const AttendArgs &a, int ctas, cudaStream_t s);
 
 }  // namespace moe
