@@ -8,13 +8,12 @@
 //   P = 2^(S scales - m)                         two threads a row, running maximum m and sum l
 //   O[128 rows x D]  += (Ph + Pm + Pl) . V       tcgen05 (e5m2 x e4m3), P in tensor memory, V in shared memory
 // An MMA over 8-bit values runs twice as fast as one over 16-bit ones, so that
-// factors may be sums of 8-bit parts:
-//   q times a power of two that takes its row's largest value to 224 .. 448 is
-//   Qh, its nearest e4m3, and Ql, the nearest e4m3 of the rest: to 2^-8 of every value
-//   or 2^-10, 2^-18 of the row's largest (bf16's 8 bits are kept whole but for values
-//   below 2^-10 of the largest; of fp16's 11 the last ones go);
-//   the weights P are three e5m2 parts, to 2^-9 of each or 2^-23 of the one at the
-//   running maximum.  (Two e4m3 parts keep as much of the large ones, but their range is
+// factors may be sums of 8-bit parts, each the nearest to what the ones before leave:
+//   q times a power of two that takes its row's largest value to 224 .. 448 is two e4m3
+//   parts of bf16, three of fp16: to 2^-9 (2^-14) of every value, which is to say whole, or
+//   to 2^-10, 2^-18 of the row's largest;
+//   the weights P are three e5m2 parts, to 2^-11 of each or 2^-23 of the one at the
+//   running maximum.  (Two e4m3 parts keep 2^-9 of the large ones, but their range is
 //   small: O had to be rescaled wherever a maximum grew by more than 2^1.75, most
 //   tiles of 32 rows.)
 // A page's K scale multiplies its columns of S, its V scale its columns of P, taken
@@ -42,7 +41,8 @@
 namespace moe {
 namespace {
 
-template <int D>
+// PARTS: e4m3 parts of a query, 2 for bf16, 3 for fp16.
+template <int D, int PARTS>
 struct QCfg {
   static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
   static constexpr int CHUNKS = D / ROWB;           // column spans
@@ -51,13 +51,13 @@ struct QCfg {
   static constexpr int OVERHEAD = 3;                // what a unit costs besides its tiles, in tiles
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   static constexpr int Q_SPAN = QT_ROWS * ROWB, Q_PART = CHUNKS * Q_SPAN;
-  static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 3 : NSK;  // ring slots of K, of V
+  static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 5 - PARTS : NSK;  // ring slots of K, of V
   // Slots of the scales' ring.  Those of tile x are asked for when K of tile x - NSK has been
   // used up, which was after all row warps had read the scores of the tile before: they are past
   // the scales of tile x - NSK - 2.
   static constexpr int SCALES = D == 256 ? 4 : D == 128 ? 8 : 16;
   static_assert(SCALES >= NSK + 2, "scales");
-  static constexpr int OFF_RING = 2 * Q_PART;
+  static constexpr int OFF_RING = PARTS * Q_PART;
   static constexpr int OFF_V = OFF_RING + NSK * SLOT, OFF_MISC = OFF_V + NSV * SLOT;
   static constexpr int SMEM = OFF_MISC + (D == 256 ? 3 : 4) * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -79,15 +79,16 @@ struct QMisc : QRing<C> {
     float row[2][2][QT_ROWS];      // later: what the two threads of a row exchange, [turn][half]
   };
 };
-static_assert(sizeof(QMisc<QCfg<256>>) <= 3 * 1024 && sizeof(QMisc<QCfg<128>>) <= 4 * 1024 &&
-                  sizeof(QMisc<QCfg<64>>) <= 4 * 1024,
+static_assert(sizeof(QMisc<QCfg<256, 2>>) <= 3 * 1024 && sizeof(QMisc<QCfg<128, 2>>) <= 4 * 1024 &&
+                  sizeof(QMisc<QCfg<64, 2>>) <= 4 * 1024,
               "misc area");
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
     qattend_kernel(const __grid_constant__ QMaps maps, const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ AttendArgs a) {
-  using C = QCfg<D>;
+  constexpr int PARTS = FP16 ? 3 : 2;
+  using C = QCfg<D, PARTS>;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles want 1024
   QMisc<C> *m = reinterpret_cast<QMisc<C> *>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,13 +160,13 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
   if (warp == C::LOAD_K) {
     load_tiles<C, false>(&maps.k, a, m, w, k_ring, [](uint32_t) { return true; });
   } else if (warp == C::LOAD_V) {
-    // a unit's queries, both parts, when the last unit's scores are done; then its V tiles
+    // a unit's queries, all parts, when the last unit's scores are done; then its V tiles
     uint32_t issued = 0;
     load_tiles<C, true>(&maps.v, a, m, w, v_ring, [&](uint32_t units) {
       if (units > 0 && !q_wait_warp(&m->q_free, (units - 1) & 1u, m, status)) return false;
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.j.rows_cap * 2 * D));
-        for (int ch = 0; ch < 2 * C::CHUNKS; ++ch)
+        ptx::mbar_arrive_expect_tx(&m->q_full, (uint32_t)(a.j.rows_cap * PARTS * D));
+        for (int ch = 0; ch < PARTS * C::CHUNKS; ++ch)
           ptx::tma_load_4d(smem + ch * C::Q_SPAN, &q_map, &m->q_full, 0, w.g * a.G, w.s.lo + w.token0(), ch);
       }
       __syncwarp();
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
       const uint64_t kd = ptx::sdesc_rows(ptx::smem_u32(k_ring + slot * C::SLOT), C::ROWB, 16);
       if (ptx::elect_one()) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
           for (int ch = 0; ch < C::CHUNKS; ++ch)
 #pragma unroll
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
         if (edge) {
           // (codes NaN that are taken out: finish() puts them where they belong)
           const uint32_t slot = jj % C::NSV;
-          // (the slot's last load, of tile jj - 3 or before, has been used up: this warp has waited for the product)
-          static_assert(C::NSV >= 3, "V slots");
+          // (the slot's last load, of tile jj - 2 or before, has been used up: this warp has waited for the product)
+          static_assert(C::NSV >= 2, "V slots");
           if (!(ok = q_wait_warp(&m->v_full[slot], (jj / C::NSV) & 1u, m, status))) break;
           if (clear_edge<C, QT_ROWS * 2>(v_ring + slot * C::SLOT, t * QT_TILE, un.all_see, un.some_see))
             m->nonfinite[units & 3] = units;
@@ -491,18 +492,18 @@ __global__ void __launch_bounds__(QCfg<D>::THREADS, 1)
 // Parts and factors of all queries: [row][head][part][D], a few heads a warp.
 template <int D, bool FP16>
 __global__ void __launch_bounds__(256) cut_queries_kernel(const uint16_t *x, uint8_t *parts, float *factor, int n) {
-  constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+  constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, PARTS = FP16 ? 3 : 2;
   start_dependent();
   const int lane = threadIdx.x & 31, d = lane % LANES * 8;
   for (int r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * AT_ONCE; r0 < n; r0 += gridDim.x * 8 * AT_ONCE) {
     const int r = r0 + lane / LANES;
     float f[8] = {};
     if (r < n) unpack8<FP16>(*reinterpret_cast<const uint4 *>(x + (size_t)r * D + d), f);
-    uint2 part[2];
-    const int e = cut_row<LANES, 2>(f, part);
+    uint2 part[PARTS];
+    const int e = cut_row<LANES, PARTS>(f, part);
     if (r >= n) continue;
-    *reinterpret_cast<uint2 *>(parts + (size_t)r * 2 * D + d) = part[0];
-    *reinterpret_cast<uint2 *>(parts + (size_t)r * 2 * D + D + d) = part[1];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) *reinterpret_cast<uint2 *>(parts + ((size_t)r * PARTS + k) * D + d) = part[k];
     if (d == 0) factor[r] = exp2_int(e);
   }
 }
@@ -510,12 +511,12 @@ __global__ void __launch_bounds__(256) cut_queries_kernel(const uint16_t *x, uin
 // ---------------------------------------------------------------- host
 
 // A unit's queries: boxes of G heads x nt tokens of one column span of a part.
-bool parts_map(CUtensorMap *map, const void *p, int rows, int Hq, int D, int G, int nt) {
+bool parts_map(CUtensorMap *map, const void *p, int rows, int Hq, int D, int parts, int G, int nt) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const int rowb = D < 128 ? D : 128;
-  cuuint64_t dims[4] = {(cuuint64_t)rowb, (cuuint64_t)Hq, (cuuint64_t)rows, (cuuint64_t)(2 * D / rowb)};
-  cuuint64_t strides[3] = {(cuuint64_t)2 * D, (cuuint64_t)Hq * 2 * D, (cuuint64_t)rowb};
+  cuuint64_t dims[4] = {(cuuint64_t)rowb, (cuuint64_t)Hq, (cuuint64_t)rows, (cuuint64_t)(parts * D / rowb)};
+  cuuint64_t strides[3] = {(cuuint64_t)parts * D, (cuuint64_t)Hq * parts * D, (cuuint64_t)rowb};
   cuuint32_t box[4] = {(cuuint32_t)rowb, (cuuint32_t)G, (cuuint32_t)nt, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(p), dims, strides, box, estr,
@@ -556,16 +557,17 @@ AttendSpace attend_ws(int D, int ctas, int rows_cap, int64_t q_rows) {
   w.ml = (size_t)ctas * sizeof(SplitDesc);
   w.part = w.ml + ((size_t)2 * ctas * rows_cap * 8 + 255) / 256 * 256;
   w.q_parts = w.all = w.part + (size_t)2 * ctas * rows_cap * D * 4;
-  w.q_factor = w.q_parts + (size_t)q_rows * 2 * D;
+  w.q_factor = w.q_parts + (size_t)q_rows * 3 * D;  // (bf16 takes two parts)
   if (rows_cap > QD_MOST) w.all = w.q_factor + (size_t)q_rows * 4;
   return w;
 }
 
 template <int D, bool FP16>
 cudaError_t launch_rows(const QMaps &maps, const AttendArgs &a, void *q_parts, float *q_factor, int ctas, cudaStream_t s) {
-  using C = QCfg<D>;
+  constexpr int PARTS = FP16 ? 3 : 2;
+  using C = QCfg<D, PARTS>;
   CUtensorMap q_map;
-  if (!parts_map(&q_map, q_parts, a.n_rows, a.Hq, D, a.G, a.nt)) return cudaErrorInvalidValue;
+  if (!parts_map(&q_map, q_parts, a.n_rows, a.Hq, D, PARTS, a.G, a.nt)) return cudaErrorInvalidValue;
   // per device and cheap: set on every call rather than remembered
   cudaError_t e = cudaFuncSetAttribute(qattend_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;

@@ -307,22 +307,25 @@ __device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendA
     for (uint32_t i = tiles > (uint32_t)NS ? tiles - NS : 0; i < tiles; ++i) q_drain(&full[i % NS], (i / NS) & 1u);
 }
 
-// Two weights in three e5m2 parts: as fp16, of which an e5m2 value is the upper
-// byte, cut off twice and rounded at last.  Off by 2^-9 of a weight (and fp16's 2^-12), or half of
-// e5m2's least step, 2^-17, which is 2^-23 of the weight at the running maximum.
+// Two weights in three e5m2 parts, each the nearest to what the ones before leave: as
+// fp16, of which an e5m2 value is the upper byte.  Off by 2^-11 of a weight (and fp16's 2^-12), or half
+// of e5m2's least step, 2^-17, which is 2^-23 of the weight at the running maximum.
 // The first two parts are the bytes 1 and 3 of hi and mid, the third those of lo, 0 and 1.
+// (NaN leaves the first two by the addition, but not the third.)
 __device__ __forceinline__ void cut_weights(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  constexpr uint32_t UPPER = 0xFF00FF00u;
+  auto upper = [](uint32_t a) { return (a + 0x00800080u) & 0xFF00FF00u; };
   auto minus = [](uint32_t a, uint32_t b) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&d);
   };
-  hi = half_pair<true>(x, y);
-  mid = minus(hi, hi & UPPER);
-  const uint32_t rest = minus(mid, mid & UPPER);
-  uint16_t last;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(last) : "r"(rest));
-  lo = last;
+  const uint32_t whole = half_pair<true>(x, y);
+  hi = upper(whole);
+  const uint32_t rest = minus(whole, hi);
+  mid = upper(rest);
+  const uint32_t last = minus(rest, mid);
+  uint16_t codes;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(codes) : "r"(last));
+  lo = codes;
 }
 
 // A code that is NaN among the four of a word: 0x7F or 0xFF.
