@@ -308,7 +308,7 @@ __device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendA
 }
 
 // Two weights in three e5m2 parts, each the nearest to what the ones before leave: as
-// fp16, of which an e5m2 value is the upper byte.  Off by 2^-11 of a weight (and fp16's 2^-12), or half
+// fp16, of which an e5m2 value is the upper byte.  Off by 2^-11 of a weight (and fp16's 2^-11), or half
 // of e5m2's least step, 2^-17, which is 2^-23 of the weight at the running maximum.
 // The first two parts are the bytes 1 and 3 of hi and mid, the third those of lo, 0 and 1.
 // (NaN leaves the first two by the addition, but not the third.)

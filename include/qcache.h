@@ -11,7 +11,7 @@
  * exact but for values below 2^-6 of the new scale, whose last bits go.  So a
  * value is off by 2^-4 of itself or half of 2^-9 scales at most, and by one
  * more such half for each time its page's scale grew.  Values that are not
- * finite become the code NaN.  Attention takes any finite scales.
+ * finite become the code NaN.  Attention takes any finite scales that are not negative.
  */
 #ifndef QCACHE_H
 #define QCACHE_H
@@ -65,13 +65,17 @@ moe_status attn_qcache_trim(const attn_qcache *c, const int32_t *slots_d, const 
  *   scale      0 means 1 / sqrt(head_dim)
  *   ws_d       workspace of attn_qcache_attend_workspace_bytes(c, B, n_rows, max_rows, Hq), scratch
  *   o_d        [n_rows][Hq][head_dim], q's type (written; rows of no sequence are left as they are)
+ * Arithmetic: the codes are tensor-core operands as they are, q and the softmax
+ * weights sums of 8-bit parts that keep all bits of q but for those below 2^-18 of its
+ * row's largest value, and 2^-10 of a weight or 2^-23 of the largest; fp32 sums, o
+ * rounded once.
  * What a row does not see cannot change it, whatever its bits; a NaN among its
  * scores, or among the values it sees, makes it NaN.  Supported: Hq a multiple of
- * n_kv_heads, at most 128 query heads per KV head, B <= 1024.  B == 0 or
- * n_rows == 0 returns MOE_OK with nothing enqueued.  Device checks (slots,
- * offsets, lengths, pages) set MOE_ERR_DEVICE_BOUNDS in the cache's status
- * word; the output of that sequence is then not valid.  o_d overlaps no input,
- * ws_d nothing else.
+ * n_kv_heads, at most 128 query heads per KV head, B <= 1024, n_rows * Hq < 2^30.
+ * B == 0 or n_rows == 0 returns MOE_OK with nothing enqueued.  Device checks
+ * (slots, offsets, lengths, pages) set MOE_ERR_DEVICE_BOUNDS in the cache's status
+ * word; the output of that sequence is then not valid.  MOE_ERR_DEVICE_TIMEOUT
+ * there: a wait for a copy gave up.  o_d overlaps no input, ws_d nothing else.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED,
  * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA. */
 size_t attn_qcache_attend_workspace_bytes(const attn_qcache *c, int32_t B, int32_t n_rows, int32_t max_rows,

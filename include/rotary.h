@@ -17,7 +17,7 @@
  *
  * Arithmetic: a rate is held as the fraction of a turn in 64-bit fixed point, so
  * that position times rate, taken modulo one turn by its overflow, is off by
- * |p| * 2^-53 turns at most whatever the position; cos, sin and the products
+ * |p| * 2^-53 turns or so whatever the position; cos, sin and the products
  * in fp32, rounded once.  A negative position turns backwards, which is also
  * the gradient's way through a rotation.
  *
@@ -58,7 +58,8 @@ moe_status attn_rotary_plan(const attn_rotary_config *cfg, attn_rotary_table *ta
  *   x_d          bf16 or fp16 (dtype), row r's heads at x_d + r * x_stride, one after another (read)
  *   positions_d  int32 [n_rows], any value (read)
  *   o_d          the same type, rows o_stride apart (written; nothing between the rows is)
- * o_d may be x_d with the same stride (in place); else the two overlap nowhere.
+ * o_d may be x_d with the same stride (in place); else the two address ranges, from
+ * the first row's first value to the last row's last, lie apart.
  * Strides in values, multiples of 8, at least n_heads * head_dim; head_dim 64,
  * 128 or 256, not below the table's dim; n_heads 1 .. 65536.  n_rows == 0 returns
  * MOE_OK with nothing enqueued.
