@@ -51,7 +51,7 @@ struct DCfg {
   static constexpr int OFF_P = CHUNKS * Q_SPAN;
   static constexpr int OFF_RING = OFF_P + 2 * P_TILE;
   static constexpr int OFF_V = OFF_RING + NSK * SLOT, OFF_MISC = OFF_V + NSV * SLOT;
-  static constexpr int MISC = D == 64 ? 4096 : 3072, SMEM = OFF_MISC + MISC;
+  static constexpr int MISC = (D == 64 ? 4 : 3) * 1024, SMEM = OFF_MISC + MISC;
   static_assert(SMEM <= 227 * 1024 && OFF_P % 1024 == 0 && OFF_RING % 1024 == 0, "shared memory");
   // Tensor memory columns: two S tiles, O of each 128 values of a head.
   static constexpr int O_TILES = D == 256 ? 2 : 1;
@@ -357,44 +357,44 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
 #pragma unroll 1
       for (int ot = 0; ot < C::O_TILES; ++ot) {
-          const int d = ot * 128 + at;
-          uint32_t v[C::HALF];
-          __syncwarp();
-          read_columns(lanes + C::O_COL + ot * C::N, v);
-          ptx::tmem_wait_ld();
-          if (D == 64 && at >= 64) continue;
-          float o[RT];
+        const int d = ot * 128 + at;
+        uint32_t v[C::HALF];
+        __syncwarp();
+        read_columns(lanes + C::O_COL + ot * C::N, v);
+        ptx::tmem_wait_ld();
+        if (D == 64 && at >= 64) continue;
+        float o[RT];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) o[i] = three(v, i) * ref;
-          if (fix) {  // codes NaN that were taken out of the edge's tiles, for the rows that see them
-            const int p1 = min(un.some_see, (un.t0 + un.n) * QT_TILE);
-            const int32_t *table = c.table + (size_t)un.slot * c.max_pages;
-            for (int p = max(un.all_see, un.t0 * QT_TILE); p < p1; ++p) {
-              const unsigned page = (unsigned)table[p >> c.page_shift];
-              if (page >= (unsigned)c.n_pages) continue;
-              const uint8_t code =
-                  a.v_layer[((((size_t)page << c.page_shift) + (p & ((1 << c.page_shift) - 1))) * a.Hkv + un.g) * D + d];
-              if ((code & 0x7F) != 0x7F) continue;
+        for (int i = 0; i < RT; ++i) o[i] = three(v, i) * ref;
+        if (fix) {  // codes NaN that were taken out of the edge's tiles, for the rows that see them
+          const int p1 = min(un.some_see, (un.t0 + un.n) * QT_TILE);
+          const int32_t *table = c.table + (size_t)un.slot * c.max_pages;
+          for (int p = max(un.all_see, un.t0 * QT_TILE); p < p1; ++p) {
+            const unsigned page = (unsigned)table[p >> c.page_shift];
+            if (page >= (unsigned)c.n_pages) continue;
+            const uint8_t code =
+                a.v_layer[((((size_t)page << c.page_shift) + (p & ((1 << c.page_shift) - 1))) * a.Hkv + un.g) * D + d];
+            if ((code & 0x7F) != 0x7F) continue;
 #pragma unroll
-              for (int i = 0; i < RT; ++i)
-                if (p <= un.pos0 + ((r0 + i) * a.g_mul >> 16)) o[i] = NAN;
-            }
-          }
-          uint16_t *out = a.o + ((size_t)(un.lo + un.token0) * a.Hq + un.g * a.G) * D + d;
-          float *part = a.j.part + pslot * a.j.rows_cap * D + d;
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const int r = r0 + i, token = r * a.g_mul >> 16;
-            if (r >= un.rows) continue;
-            if (whole) {
-              const float y = sum[i] == 0.f ? 0.f : o[i] * (1.f / sum[i]);
-              out[((size_t)token * a.Hq + (r - token * a.G)) * D] =
-                  fp16 ? __half_as_ushort(__float2half_rn(y)) : f32_to_bf16(y);
-            } else {
-              part[(size_t)r * D] = o[i];
-            }
+            for (int i = 0; i < RT; ++i)
+              if (p <= un.pos0 + ((r0 + i) * a.g_mul >> 16)) o[i] = NAN;
           }
         }
+        uint16_t *out = a.o + ((size_t)(un.lo + un.token0) * a.Hq + un.g * a.G) * D + d;
+        float *part = a.j.part + pslot * a.j.rows_cap * D + d;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int r = r0 + i, token = r * a.g_mul >> 16;
+          if (r >= un.rows) continue;
+          if (whole) {
+            const float y = sum[i] == 0.f ? 0.f : o[i] * (1.f / sum[i]);
+            out[((size_t)token * a.Hq + (r - token * a.G)) * D] =
+                fp16 ? __half_as_ushort(__float2half_rn(y)) : f32_to_bf16(y);
+          } else {
+            part[(size_t)r * D] = o[i];
+          }
+        }
+      }
       ptx::tc_fence_before();
       arrive(&m->o_free);
       return true;
