@@ -419,26 +419,17 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
           tmax = fmaxf(tmax, exchange(tmax, ok));
           if (!ok) break;
           const bool grows = in && tmax > mx + QT_SLACK, wider = vmax > ref * QT_WIDER;  // also the first a row sees
-          if (__any_sync(0xffffffffu, grows || wider)) {
-            float f = grows ? (mx == -INFINITY ? 0.f : exp2f(mx - tmax)) : 1.f;
-            if (grows) mx = tmax;
-            sum *= f;
-            if (wider) {
-              f *= ref / vmax;
-              ref = vmax;
+          const bool rescales = __any_sync(0xffffffffu, grows || wider);
+          float o_f = 1.f;  // what O's earlier tiles are to be multiplied by
+          if (rescales) {
+            if (grows) {
+              o_f = mx == -INFINITY ? 0.f : exp2f(mx - tmax);
+              mx = tmax;
+              sum *= o_f;
             }
-            if (j > 0) {  // O holds the earlier tiles
-              if (!(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
-              ptx::tc_fence_after();
-#pragma unroll 1
-              for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
-                uint32_t v[32];
-                ptx::tmem_ld_x32(lanes + d, v);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                ptx::tmem_st_x32(lanes + d, v);
-              }
+            if (wider) {
+              o_f *= ref / vmax;
+              ref = vmax;
             }
           }
           const float base = QT_TOP - (mx == -INFINITY ? 0.f : mx), inv_ref = ref > 0.f ? 1.f / ref : 0.f;
@@ -462,9 +453,21 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
             part[2][i / 4] = __byte_perm(l0, l1, 0x5410);
           }
           sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          // the product with the tile before is done: its P has been used up
+          // the product with the tile before is done: its P has been used up, and O may be changed
+          // (here, not where the maximum is found, which would be to wait for the product before the weights are made)
           if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
           ptx::tc_fence_after();
+          if (rescales && j > 0) {
+#pragma unroll 1
+            for (int d = half * OCOLS; d < (half + 1) * OCOLS; d += 32) {
+              uint32_t v[32];
+              ptx::tmem_ld_x32(lanes + d, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * o_f);
+              ptx::tmem_st_x32(lanes + d, v);
+            }
+          }
 #pragma unroll
           for (int k = 0; k < 3; ++k) ptx::tmem_st_x16(lanes + C::P_COL + k * C::P_PART + half * (COLS / 4), part[k]);
           ptx::tmem_wait_st();

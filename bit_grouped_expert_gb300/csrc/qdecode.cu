@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           const volatile int *f = m->grows[turn][half];
           grows = (f[0] | f[1] | f[2] | f[3]) != 0;
         }
+        float f[RT];  // what O's earlier tiles are to be multiplied by
         if (grows) {
           float v_f = 1.f;
           if (vmax > ref * QT_WIDER) {
@@ -520,7 +521,6 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < RT / 4; ++i) m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
           if (!(ok = meet())) break;
-          float f[RT];
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
@@ -536,27 +536,6 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           if (quad == 0 && lane == 0)
 #pragma unroll
             for (int i = 0; i < RT; ++i) m->base[half][i] = x[i];
-          if (j > 0) {  // O holds the earlier tiles
-            if (!(ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int ot = 0; ot < C::O_TILES; ++ot) {
-              const uint32_t col = lanes + C::O_COL + ot * C::N;
-              uint32_t v[C::HALF];
-              read_columns(col, v);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 3 * RT; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[i % RT]);
-#pragma unroll
-              for (int i = 0; i < C::HALF; i += 16) {
-                uint32_t y[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) y[q] = v[i + q];
-                ptx::tmem_st_x16(col + i, y);
-              }
-            }
-            ptx::tmem_wait_st();
-          }
           if (!(ok = meet())) break;  // the maxima are there
           over_maximum();
         }
@@ -583,6 +562,28 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         for (int i = 0; i < C::HALF; i += 16)
           *reinterpret_cast<uint4 *>(p_tile + ((half * C::HALF + i) ^ (at & 7) << 4)) =
               make_uint4(p_row[i / 4], p_row[i / 4 + 1], p_row[i / 4 + 2], p_row[i / 4 + 3]);
+        // O, once the product with the tile before is done (the weights are made meanwhile)
+        if (grows && j > 0) {
+          if (!(ok = q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status))) break;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int ot = 0; ot < C::O_TILES; ++ot) {
+            const uint32_t col = lanes + C::O_COL + ot * C::N;
+            uint32_t v[C::HALF];
+            read_columns(col, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 3 * RT; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[i % RT]);
+#pragma unroll
+            for (int i = 0; i < C::HALF; i += 16) {
+              uint32_t y[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) y[q] = v[i + q];
+              ptx::tmem_st_x16(col + i, y);
+            }
+          }
+          ptx::tmem_wait_st();
+        }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         arrive(&m->p_ready[jj & 1]);
