@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
             kf[g] = fmaxf(q_scale * sc[0][half * (COLS / QT_GROUP) + g], 1e-37f);
             float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < QT_GROUP; ++i)
-              most[i & 1] = fmaxf(most[i & 1], __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]));
+            for (int i = 0; i < QT_GROUP; i += 2)
+              most[i / 2 & 1] = largest_of(most[i / 2 & 1], __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]),
+                                           __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i + 1]));
             tmax = fmaxf(tmax, fmaxf(most[0], most[1]) * kf[g]);
           }
 #pragma unroll
@@ -434,25 +435,27 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
           }
           const float base = QT_TOP - (mx == -INFINITY ? 0.f : mx), inv_ref = ref > 0.f ? 1.f / ref : 0.f;
           uint32_t part[3][COLS / 4];
-          float acc[4] = {};
+          float2 acc[2] = {};
 #pragma unroll
           for (int i = 0; i < COLS; i += 4) {
             const float vf = sc[1][half * (COLS / QT_GROUP) + i / QT_GROUP] * inv_ref;
-            float p[4];
+            float2 p[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              p[k] = ex2(fmaf(__uint_as_float(x[(i + k) / 32][(i + k) % 32]), kf[i / QT_GROUP], base));
-              acc[k] += p[k];
-              p[k] *= vf;
+            for (int k = 0; k < 2; ++k) {
+              p[k] = fma_both(__uint_as_float(x[i / 32][i % 32 + 2 * k]), __uint_as_float(x[i / 32][i % 32 + 2 * k + 1]),
+                              kf[i / QT_GROUP], base);
+              p[k] = make_float2(ex2(p[k].x), ex2(p[k].y));
+              acc[k] = add_both(acc[k], p[k]);
+              p[k] = mul_both(p[k], vf);
             }
             uint32_t h0, m0, l0, h1, m1, l1;
-            cut_weights(p[0], p[1], h0, m0, l0);
-            cut_weights(p[2], p[3], h1, m1, l1);
+            cut_weights(p[0].x, p[0].y, h0, m0, l0);
+            cut_weights(p[1].x, p[1].y, h1, m1, l1);
             part[0][i / 4] = __byte_perm(h0, h1, 0x7531);
             part[1][i / 4] = __byte_perm(m0, m1, 0x7531);
             part[2][i / 4] = __byte_perm(l0, l1, 0x5410);
           }
-          sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           // the product with the tile before is done: its P has been used up, and O may be changed
           // (here, not where the maximum is found, which would be to wait for the product before the weights are made)
           if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;

@@ -307,6 +307,35 @@ __device__ __forceinline__ void load_tiles(const CUtensorMap *map, const AttendA
     for (uint32_t i = tiles > (uint32_t)NS ? tiles - NS : 0; i < tiles; ++i) q_drain(&full[i % NS], (i / NS) & 1u);
 }
 
+// Two of a kind in one instruction (an issue slot for both).
+__device__ __forceinline__ float2 fma_both(float x, float y, float a, float b) {  // x a + b, y a + b
+  float2 r;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 s, {%5, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x), "f"(y), "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 mul_both(float2 x, float a) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 add_both(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float largest_of(float a, float b, float c) {  // (passes over NaN)
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Two weights in three e5m2 parts, each the nearest to what the ones before leave: as
 // fp16, of which an e5m2 value is the upper byte.  Off by 2^-11 of a weight (and fp16's 2^-11), or half
 // of e5m2's least step, 2^-17, which is 2^-23 of the weight at the running maximum.
