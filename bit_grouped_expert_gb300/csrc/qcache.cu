@@ -1,19 +1,24 @@
 // Appending to the 8-bit paged KV cache (qcache.h); its forks and cuts are the
 // 16-bit cache's (cache.cu), which move codes as they are.
 //
-// After the plan (cache.cu) a CTA takes one part, the rows that the call adds to one
-// page, of K or of V in some layers.  Its warps go over them twice, a few rows of one
-// (layer, head) at a time: for the largest value of each (layer, head), and, with the
-// scales settled, for the codes;
-// the second time the rows come from L2, and nothing waits in registers, so that
-// an SM has 24 warps to hide the loads behind.  Then the page's earlier codes
-// are rounded anew where their scale grew (or moved, where the page is a copy).
-// A lane has sixteen values of one row, the same of every (layer, head) that its warp goes
+// For a page's part x of some rows (one layer and head, K or V) with the scale s before,
+//   s' = max(s, 2^e), e the least with max |x| <= 448 * 2^e;   code = e4m3(x / s');   old codes: e4m3(code s / s')
+// (without earlier rows s' = 2^e).  After the plan (cache.cu) a CTA takes one part, the rows that
+// the call adds to one page, of K or of V in some layers.  Its warps go over them twice, a few
+// rows of one (layer, head) at a time: for the largest value of each (layer, head), and, with the
+// scales settled, for the codes; the second time most rows come from L2, and nothing waits in
+// registers, so that an SM has 24 warps to hide the loads behind (16: 158 us for 130 in the case
+// below).  Then the page's earlier codes are rounded anew where their scale grew (or moved, where the page is
+// a copy).  A lane has sixteen values of one row, the same of every (layer, head) that its warp goes
 // over, so that their angles are made once for all of these.
 //
-// Large calls are bound by instructions (a value is unpacked, turned, compared, scaled
-// and rounded, twice for K): infinities and NaN, which do not count for the scale and
-// become NaN, are looked for only where a maximum shows that there are any.
+// 9,318 rows for 24 prompts, 10 layers of 2 heads of 256, fp16, all of K turned: 130 us for 286 MB with the
+// trim and the plan before it (17 of them), floor 42.  In copies that leave a part of the work out: V's
+// maxima 26 us, its codes 35, K's 32 and 38: each is a stream through the SMs of 4.5 TB/s at most with
+// half of the issue slots used.  Infinities and NaN, which do not count for the scale and become
+// NaN, are looked for only where a maximum shows that there are any.
+// (Rows backwards the second time, so that the last ones read are the first ones wanted, takes 54 MB of
+// reads off DRAM and no time; places gone on to by adding instead of multiplying 133 us.)
 #include "qcache.cuh"
 #include "rotary.cuh"
 #include "tc_ptx.cuh"
@@ -344,8 +349,9 @@ extern "C" moe_status attn_qcache_append(const attn_qcache *c, const attn_rotary
   g.turns = table != nullptr;
   if (table) g.table = *table;
   // Jobs of a part, of K and of V: one a layer, or as many as give the CTAs that run at once
-  // one of each (K's rows then make their angles less often), or one of both where a part has
-  // few rows; but each of QA_MOST (layer, head)s at most.
+  // one of each (K's rows then make their angles less often: 24 prompts' chunks of up to 500 rows 137 us, with twice
+  // as many jobs 144), or one of both where a part has few rows (one row for each of 48 sequences: 18.8 us for
+  // 22.1); but each of QA_MOST (layer, head)s at most.
   const long long parts = (long long)n_rows / c->page_size + B;
   const int layers = c->n_layers, least = (layers * c->n_kv_heads + moe::QA_MOST - 1) / moe::QA_MOST;
   const int fewest = least > 1 ? layers / (moe::QA_MOST / c->n_kv_heads) + 1 : 1;
@@ -353,7 +359,12 @@ extern "C" moe_status attn_qcache_append(const attn_qcache *c, const attn_rotary
     const long long want = (ctas + parts - 1) / parts, g = want < fewest ? fewest : want;
     return (int)(g < layers ? g : layers);
   };
-  g.k_groups = g.v_groups = groups(n_rows <= 8 * B ? moe::QA_CTAS / 2 : moe::QA_CTAS);
+  const bool few = n_rows <= 8 * B;
+  g.k_groups = g.v_groups = groups(few ? moe::QA_CTAS / 2 : moe::QA_CTAS);
+  // Long V jobs, the last to be handed out, are halved, so that the CTAs end closer to one another (parts of
+  // 128 rows, 5 (layer, head)s of 256 a job: 137 us whole, 130 halved; of 16 rows, 20 a job: 119 and 124).
+  if (!few && (long long)c->page_size * layers * c->n_kv_heads * c->head_dim / g.v_groups >= 128 << 10)
+    g.v_groups = 2 * g.v_groups < layers ? 2 * g.v_groups : layers;
   const long long jobs = (parts + B) * (g.k_groups + g.v_groups);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = moe::launch_append_plan(g.a, s);
