@@ -65,12 +65,14 @@ struct DMisc : QRing<C> {
   uint64_t s_full[2], s_free[2], meet[2];
   int nonfinite[4];                  // by the unit's number: that unit, if NaN was taken out of its V
   __align__(16) float q_f[4][C::R];  // by the unit's number: what a row's scores are multiplied by
-  float base[2][RT];                 // 2^6 over the running maximum, in log2; infinity before the first score
+  // [half][warp], each warp its own: 2^6 over the running maximum, in log2; infinity before the first score
+  __align__(16) float base[2][4][RT];
   union {
     long long wsum[C::WARPS];
     struct {                         // later: what the four warps of a half exchange
       int grows[2][2][4];            // [turn][half][warp]
       float most[2][4][RT];          // [half][warp][row]
+      float sums[2][4][RT];
     };
   };
 };
@@ -191,8 +193,8 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
   } else if (tid >= 64 && tid < 64 + C::SCALES) {
     ptx::mbar_init(&m->sc_full[tid - 64], 16);
     ptx::fence_mbar_init();
-  } else if (tid >= 128 && tid < 128 + 2 * RT) {
-    m->base[0][tid - 128] = INFINITY;
+  } else if (tid >= 128 && tid < 128 + 8 * RT) {
+    m->base[0][0][tid - 128] = INFINITY;
   } else if (tid == 96) {
     m->abort_flag = 0;
     ptx::mbar_init(&m->q_full, C::ROW_WARPS);
@@ -331,22 +333,22 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       fold(sum, mine4, [](float x, float y) { return x + y; });
       if ((lane & 7) == 0)
 #pragma unroll
-        for (int i = 0; i < RT / 4; ++i) m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
+        for (int i = 0; i < RT / 4; ++i) m->sums[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
       if (!meet()) return false;
 #pragma unroll
       for (int i = 0; i < RT; ++i)
-        sum[i] = (m->most[half][0][i] + m->most[half][1][i]) + (m->most[half][2][i] + m->most[half][3][i]);
-      if (at < RT) {  // the maxima: to the joining kernel, and from the start for the next unit
+        sum[i] = (m->sums[half][0][i] + m->sums[half][1][i]) + (m->sums[half][2][i] + m->sums[half][3][i]);
+      if (lane < RT) {  // the maxima: to the joining kernel, and from the start for the next unit
         float mine = 0.f;
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          if (i == at) mine = sum[i];
-        if (!whole && r0 + at < un.rows)
-          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r0 + at) * 2) =
-              make_float2(QT_TOP - m->base[half][at], mine);
-        m->base[half][at] = INFINITY;
+          if (i == lane) mine = sum[i];
+        if (quad == 0 && !whole && r0 + lane < un.rows)
+          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r0 + lane) * 2) =
+              make_float2(QT_TOP - m->base[half][quad][lane], mine);
+        m->base[half][quad][lane] = INFINITY;
       }
-      if (!meet()) return false;  // read by all before they are written again
+      __syncwarp();
       if (!q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
       if (!whole && starts) {
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           float most = -INFINITY;
 #pragma unroll
           for (int i = 0; i < RT; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(&m->base[half][i]);
+            const float4 f = *reinterpret_cast<const float4 *>(&m->base[half][quad][i]);
             const float base[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[i + k] = s[i + k] + base[k];
@@ -525,18 +527,19 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           for (int i = 0; i < RT; ++i) {
             const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
                                      fmaxf(m->most[half][2][i], m->most[half][3][i]));
-            const float was = m->base[half][i];
+            const float was = m->base[half][quad][i];
             const bool up = most > -INFINITY && most + was > QT_TOP + QT_SLACK;  // (of a row that has seen nothing yet: any score)
             f[i] = up ? ex2(QT_TOP - most - was) : 1.f;
             sum[i] *= f[i];
             f[i] *= v_f;
             x[i] = up ? QT_TOP - most : was;
           }
-          if (!(ok = meet())) break;  // read by all before they are written again
-          if (quad == 0 && lane == 0)
+          // (the exchanged maxima are written again after the next tile's meeting at the earliest)
+          __syncwarp();
+          if (lane == 0)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) m->base[half][i] = x[i];
-          if (!(ok = meet())) break;  // the maxima are there
+            for (int i = 0; i < RT; ++i) m->base[half][quad][i] = x[i];
+          __syncwarp();
           over_maximum();
         }
         // the weights: this position's row of the tile, a byte a row and part
