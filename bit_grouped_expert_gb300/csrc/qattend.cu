@@ -48,7 +48,9 @@ struct QCfg {
   static constexpr int CHUNKS = D / ROWB;           // column spans
   static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11;
   static constexpr int WARPS = 12, THREADS = WARPS * 32;  // (168 registers a thread; 13 warps would have 128)
-  static constexpr int OVERHEAD = 3;                // what a unit costs besides its tiles, in tiles
+  // What a unit costs besides its tiles, in tiles.  (4 prompts' 500 rows over 8,000 positions, heads of 256, with
+  // 3, 4, 5, 6: 174, 171.5, 172.5, 173.5 us; 20 of 80 over 4,000, heads of 128: 66.0, 67.6, 67.1, 68.9.)
+  static constexpr int OVERHEAD = D == 256 ? 4 : 3;
   static constexpr int SLOT = QT_TILE * D, SPAN = QT_TILE * ROWB;  // a tile of K or V, one column span of it
   static constexpr int Q_SPAN = QT_ROWS * ROWB, Q_PART = CHUNKS * Q_SPAN;
   static constexpr int NSK = D == 256 ? 2 : D == 128 ? 5 : 8, NSV = D == 256 ? 5 - PARTS : NSK;  // ring slots of K, of V
