@@ -46,14 +46,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 // o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split
 // unit.  A thread has sixteen values of one row (rows run fastest, in the
-// parts as in the threads, so that a warp reads whole lines); up to eight
+// parts as in the threads, so that a warp reads whole lines); up to `most_groups`
 // groups of a block's threads share the parts of the same values (a unit is
 // split over as few as two CTAs and as many as all of them).
 constexpr int JOIN_THREADS = 256;
 
 // (One group always, this rule, eight always, whole calls in us: 1 node over 3,000
 // positions 17.4, 14.8, 14.4; 4 x 5 over 9,000 29.8, 25.0, 24.3; 24 x 5 over 6,000
-// 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.)
+// 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.  More than 32 parts, over the 8-bit cache,
+// whose units are fewer rows: one row over 131,000 positions in 32 groups 38.4 us, in eight 43.0; five 53.7 and 55.2.)
 __device__ __forceinline__ int part_groups(int parts, int most) {
   return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : parts <= 32 ? 8 : most;
 }

@@ -28,8 +28,14 @@
 // with the pages' scales and V, each into a ring of its own), two issue the MMAs
 // of S (of the next tile during the softmax of this one) and of O.  The queries' parts
 // are made beforehand, by a kernel of their own, so that they come as they are needed, by
-// TMA.  (Four warps that cut the next unit's took 12 us for 128 rows.)  Who waits on a barrier's parity must know that the phase
-// before has passed: the comments at the waits say from what.
+// TMA.  (Four warps that cut the next unit's took 12 us for 128 rows.)  Who waits on a
+// barrier's parity must know that the phase before has passed: the comments at the waits say from what.
+//
+// A tile of 128 rows, heads of 256, bf16, is 1,024 cycles of MMA for S and 1,536 for O; the rows
+// take 3,100 to 3,600 and bound it, K and V are there in time.  4 sequences' 500 rows over 8,000
+// positions, 16 heads on 2: 172 us with the cut (8.5) and the join (14), 1,050 TFLOP/s; 5 rows over
+// 131,000 positions 45.7 us, 2.9 TB/s.  (Sixteen row warps of 96 registers: 220 and 53.7 us where these
+// eight took 215 and 50.3.)
 //
 // Every wait is bounded: after one second the kernel records
 // MOE_ERR_DEVICE_TIMEOUT, drains its copies and MMAs, frees tensor memory
@@ -47,7 +53,7 @@ struct QCfg {
   static constexpr int ROWB = D < 128 ? D : 128;    // bytes of a row in a column span
   static constexpr int CHUNKS = D / ROWB;           // column spans
   static constexpr int ROW_WARPS = 8, LOAD_K = 8, ISSUE_S = 9, ISSUE_O = 10, LOAD_V = 11;
-  static constexpr int WARPS = 12, THREADS = WARPS * 32;  // (168 registers a thread; 13 warps would have 128)
+  static constexpr int WARPS = 12, THREADS = WARPS * 32;  // (168 registers a thread at most)
   // What a unit costs besides its tiles, in tiles.  (4 prompts' 500 rows over 8,000 positions, heads of 256, with
   // 3, 4, 5, 6: 174, 171.5, 172.5, 173.5 us; 20 of 80 over 4,000, heads of 128: 66.0, 67.6, 67.1, 68.9.)
   static constexpr int OVERHEAD = D == 256 ? 4 : 3;
@@ -67,7 +73,7 @@ struct QCfg {
   // column.  The rows take a whole S tile into registers first thing, so that the next one's
   // MMAs run during the softmax, and write P last thing, when the product with the one
   // before is done.  (Two tiles, each first S and then P, made the scores of a tile wait for the
-  // product of two before: 2.2 us a tile of 128 rows instead of 1.6.)
+  // product of two before: 2.2 us a tile of 128 rows where this took 1.75.)
   static constexpr uint32_t S_COL = D, P_COL = D + QT_TILE, P_PART = QT_TILE / 4, TMEM = 512;
   static_assert(P_COL + 3 * P_PART <= TMEM, "tensor memory");
 };
@@ -459,7 +465,8 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
           }
           sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           // the product with the tile before is done: its P has been used up, and O may be changed
-          // (here, not where the maximum is found, which would be to wait for the product before the weights are made)
+          // (Here, not where the maximum is found, which is to wait for the product before the weights are made:
+          // 181 us for 215 in the case above, whose heads of large scores rescale in most tiles.)
           if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
           ptx::tc_fence_after();
           if (rescales && j > 0) {

@@ -2,7 +2,10 @@
 // the paged cache with the K rows turned on the way.
 //
 // A lane turns sixteen values of a head, the same ones of every head that its
-// warp goes over, so that a position's cosines and sines are made once.
+// warp goes over, so that a position's cosines and sines are made once: with
+// that HBM bounds large calls (8,191 rows of 16 heads of 256, bf16: 26.4 us, 5.1 TB/s; in
+// the append, where 24 prompts' 9,318 rows in 10 layers of 2 heads are copied as well as turned, 69.5 us,
+// 5.5 TB/s), the host small ones (one row 6.9 us).
 #include "rotary.cuh"
 
 #include <math.h>
