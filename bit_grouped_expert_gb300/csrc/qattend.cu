@@ -83,7 +83,10 @@ struct QMisc : QRing<C> {
   uint64_t s_full, s_free, pair_bar[4];
   int nonfinite[4];                // by the unit's number: that unit, if NaN was taken out of its V
   union {
-    long long wsum[C::WARPS];
+    struct {
+      long long wsum[C::WARPS];
+      int2 wunits[C::WARPS];  // units, the longest
+    };
     float row[2][2][QT_ROWS];      // later: what the two threads of a row exchange, [turn][half]
   };
 };
@@ -151,17 +154,15 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
   // what the kernel before writes (lengths, tables, codes, scales, queries) from here on,
   // by ordinary loads: a read-only one may look at what was there before
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  long long end, T;
-  int runs;
-  const long long count = find_run<C>(a, m, end, T, runs);
+  const QRun run = find_run<C>(a, m);
   const uint32_t tmem = m->tmem;
   const int cta = blockIdx.x;
-  if (count == 0) {  // less to do than CTAs
+  if (run.count == 0) {  // less to do than CTAs
     if (tid == 0) a.j.desc[cta].parts = 0;
     if (warp == C::ISSUE_S) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
-  QWalk<C> w(a, m->b0, m->s0, m->off0, count);
+  QWalk<C> w(a, m->b0, m->s0, m->off0, run);
   uint8_t *k_ring = smem + C::OFF_RING, *v_ring = smem + C::OFF_V;
   int32_t *status = c.status;
 
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
-        split = SplitDesc{(int)q_mul_div(u1 * runs + T - 1, 1, T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
+        split = SplitDesc{(int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       const bool more = w.next();
       if (un.n > 0) ok = finish();
       if (!more || !ok) break;
-      un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, 0, 0, end - w.left};
+      un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, 0, 0, run.end - w.left};
       const int pos0 = w.s.L - w.s.n + un.token0;  // of the first token
       un.all_see = max(0, pos0 + 1);
       un.some_see = max(0, pos0 + w.tokens());

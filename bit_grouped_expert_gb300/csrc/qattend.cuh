@@ -18,6 +18,10 @@ constexpr int QT_MAX_SMS = JOIN_MAX_CTAS / 2;
 // running maximum is 2^6, and O is rescaled only where the maximum grows by more than
 // 2^7 or the largest scale of V by more than 2^2, so that weights stay below 2^15.
 constexpr float QT_TOP = 6.f, QT_SLACK = 7.f, QT_WIDER = 4.f;
+// Where units are not cut.  (One token, heads of 256, without and with it: 64 sequences of 700, 1,400, 3,000
+// positions 24.7 and 19.5, 30.5 and 25.4, 45.8 and 40.8 us; one of 350 14.2 and 12.9; one of 1,400, which counts 14
+// tiles more than its share, 15.0, uncut 17.7.  8 sequences' 100 rows over 1,500 41.7 and 37.8, 50 rows over 350 19.7 and 20.0.)
+constexpr int QT_SPARES = 8;
 constexpr unsigned long long QT_TIMEOUT_NS = 1000000000ull;
 
 struct QMaps {
@@ -82,11 +86,16 @@ __device__ __forceinline__ int tiles_of(const AttendArgs &a, const QSeq &s, int 
   return max(1, (sees_of(a, s, rt) + QT_TILE - 1) / QT_TILE);
 }
 __device__ __forceinline__ int row_tiles(const AttendArgs &a, const QSeq &s) { return (s.n + a.nt - 1) / a.nt; }
+// What a unit counts: its tiles and what it costs besides, or each the same (0: not).
+template <typename C>
+__device__ __forceinline__ int unit_count(int tiles, int each) {
+  return each ? each : C::OVERHEAD + tiles;
+}
 // The count of a sequence's units, of one KV head.
 template <typename C>
-__device__ __forceinline__ long long head_count(const AttendArgs &a, const QSeq &s) {
+__device__ __forceinline__ long long head_count(const AttendArgs &a, const QSeq &s, int each) {
   long long t = 0;
-  for (int rt = 0, rts = row_tiles(a, s); rt < rts; ++rt) t += C::OVERHEAD + tiles_of(a, s, rt);
+  for (int rt = 0, rts = row_tiles(a, s); rt < rts; ++rt) t += unit_count<C>(tiles_of(a, s, rt), each);
   return t;
 }
 
@@ -95,6 +104,13 @@ __device__ __forceinline__ long long q_mul_div(long long x, int y, long long z) 
   const long long p = x * y;
   return (p | z) < (1ll << 31) ? (long long)((uint32_t)p / (uint32_t)z) : q_div_long(p, z);
 }
+
+// A CTA's run: its length (0: none) and where it ends in the count T of all units, which `runs` CTAs share.
+struct QRun {
+  long long count, end, T;
+  int runs;
+  int each;  // not 0: a unit is a run, and counts this
+};
 
 // A CTA's walk over the units of its run, in the order sequence, KV head, row
 // tile.  A unit counts OVH + its tiles, the overhead first.
@@ -109,14 +125,15 @@ struct QWalk {
   int nt_all;      // tiles of the unit
   int t0, n;       // this CTA's: the first, and how many
   bool fresh;
+  const int each;
 
-  __device__ QWalk(const AttendArgs &a_, int b0, const QSeq &s0, long long off0, long long count)
-      : a(a_), b(b0), left(count), s(s0), rt(0), fresh(true) {
-    const long long each = head_count<C>(a, s);
-    g = (int)q_mul_div(off0, 1, each);
-    off0 -= g * each;
-    while (off0 >= OVH + (nt_all = tiles_of(a, s, rt))) {
-      off0 -= OVH + nt_all;
+  __device__ QWalk(const AttendArgs &a_, int b0, const QSeq &s0, long long off0, const QRun &run)
+      : a(a_), b(b0), left(run.count), s(s0), rt(0), fresh(true), each(run.each) {
+    const long long head = head_count<C>(a, s, each);
+    g = (int)q_mul_div(off0, 1, head);
+    off0 -= g * head;
+    while (off0 >= unit_count<C>(nt_all = tiles_of(a, s, rt), each)) {
+      off0 -= unit_count<C>(nt_all, each);
       ++rt;
     }
     off = (int)off0;
@@ -139,10 +156,10 @@ struct QWalk {
         nt_all = tiles_of(a, s, rt);
       }
       fresh = false;
-      const int take = (int)(left < OVH + nt_all - off ? left : (long long)(OVH + nt_all - off));
+      const int all = unit_count<C>(nt_all, each), take = (int)(left < all - off ? left : (long long)(all - off));
       left -= take;
       t0 = max(0, off - OVH);
-      n = max(0, off + take - OVH) - t0;
+      n = min(nt_all, max(0, off + take - OVH)) - t0;
       if (n > 0) return true;
     }
     return false;
@@ -187,45 +204,70 @@ __device__ __forceinline__ void q_drain(uint64_t *bar, uint32_t parity) {
 
 // This CTA's run: every thread adds up some sequences' units, a scan gives
 // their places, and the thread whose sequences hold the run's start writes
-// down where that is.  Returns the run's length, 0 for none; end: where it
-// ends in the count T of all units, which `runs` CTAs share.  All threads call it.
+// down where that is.  All threads call it.
+// Where there are no more units than CTAs, and the longest of them is no more than QT_SPARES
+// tiles above an equal share, each is a run: the joining kernel then has nothing to do.
 template <typename C, typename M>
-__device__ __forceinline__ long long find_run(const AttendArgs &a, M *m, long long &end, long long &T, int &runs) {
+__device__ __forceinline__ QRun find_run(const AttendArgs &a, M *m) {
+  constexpr int MANY = QT_MAX_SMS + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + C::THREADS - 1) / C::THREADS, sb = min(a.B, tid * per), se = min(a.B, sb + per);
   QSeq seq{0, 0, 0, 0};
   long long held = 0;
+  int units = 0, longest = 0;
   for (int b = sb; b < se; ++b) {
     seq = q_load_seq(a, b);
-    held += a.Hkv * head_count<C>(a, seq);
+    if (seq.n == 0) continue;
+    const int rts = row_tiles(a, seq);
+    held += a.Hkv * head_count<C>(a, seq, 0);
+    units = rts < MANY ? min(MANY, units + a.Hkv * rts) : MANY;
+    longest = max(longest, C::OVERHEAD + tiles_of(a, seq, rts - 1));  // (the last rows see the most)
   }
   long long inc = held;
+  int u_inc = units;
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
+    const int u = __shfl_up_sync(0xffffffffu, u_inc, o);
+    if (lane >= o) inc += t, u_inc += u;
   }
-  if (lane == 31) m->wsum[warp] = inc;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) m->wsum[warp] = inc, m->wunits[warp] = make_int2(u_inc, longest);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  QRun run;
   long long before = inc - held;
-  T = 0;
+  int u_before = u_inc - units, u_all = 0;
+  run.T = 0;
   for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += m->wsum[w];
-    T += m->wsum[w];
+    const int2 u = m->wunits[w];
+    if (w < warp) before += m->wsum[w], u_before += u.x;
+    run.T += m->wsum[w];
+    u_all += u.x;
+    longest = max(longest, u.y);
   }
-  runs = (int)(T < (long long)gridDim.x ? T : (long long)gridDim.x);
-  if ((int)blockIdx.x >= runs) return end = 0;
-  const long long first = q_mul_div(T, blockIdx.x, runs);
-  end = q_mul_div(T, blockIdx.x + 1, runs);
+  const int ctas = gridDim.x;
+  run.each = u_all <= ctas && longest - q_mul_div(run.T, 1, ctas) <= QT_SPARES ? longest : 0;
+  if (run.each) {
+    held = (long long)units * longest;
+    before = (long long)u_before * longest;
+    run.T = (long long)u_all * longest;
+    run.runs = u_all;
+  } else {
+    run.runs = (int)(run.T < (long long)ctas ? run.T : (long long)ctas);
+  }
+  run.count = run.end = 0;
+  if ((int)blockIdx.x >= run.runs) return run;
+  const long long first = q_mul_div(run.T, blockIdx.x, run.runs);
+  run.end = q_mul_div(run.T, blockIdx.x + 1, run.runs);
   if (first >= before && first < before + held) {
     long long at = before;
     int b = sb;
     if (per > 1)
       for (;; ++b) {
         seq = q_load_seq(a, b);
-        const long long t = a.Hkv * head_count<C>(a, seq);
+        const long long t = a.Hkv * head_count<C>(a, seq, run.each);
         if (first < at + t) break;
         at += t;
       }
@@ -234,7 +276,8 @@ __device__ __forceinline__ long long find_run(const AttendArgs &a, M *m, long lo
     m->off0 = first - at;
   }
   __syncthreads();
-  return end - first;
+  run.count = run.end - first;
+  return run;
 }
 
 // A loading warp: a unit's K tiles and the scales of K and V, or its V tiles, into their ring.

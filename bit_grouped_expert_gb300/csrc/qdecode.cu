@@ -73,7 +73,10 @@ struct DMisc : QRing<C> {
   // [half][warp], each warp its own: 2^6 over the running maximum, in log2; infinity before the first score
   __align__(16) float base[2][4][RT];
   union {
-    long long wsum[C::WARPS];
+    struct {
+      long long wsum[C::WARPS];
+      int2 wunits[C::WARPS];  // units, the longest
+    };
     struct {                         // later: what the four warps of a half exchange
       int grows[2][2][4];            // [turn][half][warp]
       float most[2][4][RT];          // [half][warp][row]
@@ -218,17 +221,15 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
   // what the kernel before writes (lengths, tables, codes, scales, queries) from here on,
   // by ordinary loads: a read-only one may look at what was there before
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  long long end, T;
-  int runs;
-  const long long count = find_run<C>(a, m, end, T, runs);
+  const QRun run = find_run<C>(a, m);
   const uint32_t tmem = m->tmem;
   const int cta = blockIdx.x;
-  if (count == 0) {  // less to do than CTAs
+  if (run.count == 0) {  // less to do than CTAs
     if (tid == 0) a.j.desc[cta].parts = 0;
     if (warp == C::ISSUE_S) ptx::tmem_dealloc(tmem, C::TMEM);
     return;
   }
-  QWalk<C> w(a, m->b0, m->s0, m->off0, count);
+  QWalk<C> w(a, m->b0, m->s0, m->off0, run);
   uint8_t *k_ring = smem + C::OFF_RING, *v_ring = smem + C::OFF_V, *p_tiles = smem + C::OFF_P;
   int32_t *status = c.status;
 
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       ptx::tc_fence_after();
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
-        split = SplitDesc{(int)q_mul_div(u1 * runs + T - 1, 1, T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
+        split = SplitDesc{(int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     }
     while (ok && more) {
       const int pos0 = w.s.L - w.s.n + w.token0();
-      un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, pos0, 0, 0, end - w.left};
+      un = Unit{w.s.slot, w.s.lo, w.token0(), w.tokens() * a.G, w.g, w.t0, w.n, w.nt_all, pos0, 0, 0, run.end - w.left};
       un.all_see = max(0, pos0 + 1);
       un.some_see = max(0, pos0 + w.tokens());
       more = w.next();  // the unit behind this one

@@ -537,6 +537,19 @@ def test_row_counts_at_which_the_kernel_changes(rows):
     c.check()
 
 
+# units that are not cut, and next to those that are: as many as there are CTAs and one more, the longest at
+# eight tiles above an equal share and beyond, sequences without rows among them, several row tiles
+@pytest.mark.parametrize("lens,counts,Hq,Hkv", [
+    ([700] * 40, [1] * 40, 8, 2), ([300] * 76, [1] * 76, 4, 2), ([300] * 77, [1] * 77, 4, 2),
+    ([640], [1], 4, 1), ([641], [1], 4, 1), ([769], [1], 4, 1), ([3000, 2500, 0, 2900] * 30, [1, 2, 0, 1] * 30, 2, 1),
+    ([3000] + [100] * 149, [1] * 150, 2, 1), ([400, 90, 350], [40, 33, 0], 8, 1), ([700, 660], [150, 130], 16, 2),
+    ([0] * 5, [0] * 5, 2, 1), ([0, 5, 0], [3, 0, 0], 2, 1)])
+def test_units_that_are_runs(lens, counts, Hq, Hkv):
+    c = Case(24, lens, counts, Hq, Hkv, 128, 32)
+    c.run()
+    c.check()
+
+
 def test_a_long_cache():
     c = Case(14, [131000], [3], 4, 1, 256, 128)
     c.run()
