@@ -460,26 +460,26 @@ def _kind(name, dtype):
 def _rows_given(name, t, dtype, device, shape):
     """Address and row stride of rows [n, H, D] whose heads lie one after another."""
     n, H, D = shape
-    strides = t.stride() if t.dim() == 3 else ()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or (t.numel() and (
-            strides[2] != 1 or (H > 1 and strides[1] != D))):
-        raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} on cuda:{device} wanted, each row's heads one "
-                         f"after another, got {t.dtype} {tuple(t.shape)} with strides {strides} on {t.device}")
-    return t.data_ptr(), strides[0] if n > 1 else H * D
+    strides = t.stride()
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device and
+            (strides[2] == 1 and (H == 1 or strides[1] == D) or not t.numel())):
+        return t.data_ptr(), strides[0] if n > 1 else H * D
+    raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} on cuda:{device} wanted, each row's heads one "
+                     f"after another, got {t.dtype} {tuple(t.shape)} with strides {strides} on {t.device}")
 
 
 def attn_rotary(rotary: Rotary, x, positions, o, stream=None):
     """Rows turned by their positions (rotary.h): x, o [n, H, D] bf16 or fp16
     (rows may lie apart; o may be x), positions int32 [n]."""
     import torch
-    dev, shape = x.get_device(), x.shape
+    dev, shape, dtype = x.get_device(), x.shape, x.dtype
     _here("x", dev)
     if len(shape) != 3:
         raise ValueError(f"x: [n, H, D] wanted, got {tuple(shape)}")
     n, H, D = shape
-    kind = _kind("x", x.dtype)
-    x_at, x_stride = _rows_given("x", x, x.dtype, dev, shape)
-    o_at, o_stride = _rows_given("o", o, x.dtype, dev, shape)
+    kind = MOE_BF16 if dtype is torch.bfloat16 else _kind("x", dtype)
+    x_at, x_stride = _rows_given("x", x, dtype, dev, shape)
+    o_at, o_stride = (x_at, x_stride) if o is x else _rows_given("o", o, dtype, dev, shape)
     _check("attn_rotary", lib().attn_rotary(
         rotary.ref, x_at, x_stride, kind, _given("positions", positions, torch.int32, dev, (n,)), n, H, D, o_at, o_stride,
         _raw_stream(stream, dev)))

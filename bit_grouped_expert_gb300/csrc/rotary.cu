@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const __grid_consta
     const int p = a.positions[row];
     const uint16_t *x = a.x + row * a.x_stride;
     uint16_t *o = a.o + row * a.o_stride;
-    constexpr int AHEAD = 4;  // groups in flight
+    constexpr int AHEAD = 4;  // groups in flight (2, 4, 8 in the case above: 33.3, 26.9, 37.5 us)
     bool first = true;
     for (int g = g0; g < g1; g += AHEAD) {
       uint4 u[AHEAD], v[AHEAD];
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(COPY_THREADS)
     const size_t src = (size_t)layer * from +
                        (size_t)(g.src + (a.path ? a.path[(size_t)b * a.path_stride + i] : i)) * c.row;
     const int groups = (heads + together - 1) / together, all = layers * groups;
-    constexpr int AHEAD = 2;  // heads in flight
+    constexpr int AHEAD = 2;  // heads in flight (1, 2, 4: the whole call 89.6, 80.8, 106 us)
     bool first = true;
     for (int n = 0; n < all; n += AHEAD) {
       uint4 k0[AHEAD], k1[AHEAD], v0[AHEAD], v1[AHEAD];
