@@ -350,16 +350,16 @@ extern "C" moe_status attn_qcache_append(const attn_qcache *c, const attn_rotary
   if (table) g.table = *table;
   // Jobs of a part, of K and of V: one a layer, or as many as give the CTAs that run at once
   // one of each (K's rows then make their angles less often: 24 prompts' chunks of up to 500 rows 137 us, with twice
-  // as many jobs 144), or one of both where a part has few rows (one row for each of 48 sequences: 18.8 us for
-  // 22.1); but each of QA_MOST (layer, head)s at most.
+  // as many jobs 144), or one of both at most where a part has few rows (one row for each of 48 sequences: 17.3 us;
+  // two jobs for some of the CTAs 19.0, for all 22.1); but each of QA_MOST (layer, head)s at most.
   const long long parts = (long long)n_rows / c->page_size + B;
   const int layers = c->n_layers, least = (layers * c->n_kv_heads + moe::QA_MOST - 1) / moe::QA_MOST;
   const int fewest = least > 1 ? layers / (moe::QA_MOST / c->n_kv_heads) + 1 : 1;
+  const bool few = n_rows <= 8 * B;
   auto groups = [&](int ctas) {
-    const long long want = (ctas + parts - 1) / parts, g = want < fewest ? fewest : want;
+    const long long want = few ? ctas / parts : (ctas + parts - 1) / parts, g = want < fewest ? fewest : want;
     return (int)(g < layers ? g : layers);
   };
-  const bool few = n_rows <= 8 * B;
   g.k_groups = g.v_groups = groups(few ? moe::QA_CTAS / 2 : moe::QA_CTAS);
   // Long V jobs, the last to be handed out, are halved, so that the CTAs end closer to one another (parts of
   // 128 rows, 5 (layer, head)s of 256 a job: 137 us whole, 130 halved; of 16 rows, 20 a job: 119 and 124).
