@@ -55,8 +55,9 @@ constexpr int JOIN_THREADS = 256;
 // positions 17.4, 14.8, 14.4; 4 x 5 over 9,000 29.8, 25.0, 24.3; 24 x 5 over 6,000
 // 63.9, 62.2, 65.9; 48 x 16 over 1,800, fp16, 78.0, 75.9, 93.5.  More than 32 parts, over the 8-bit cache,
 // whose units are fewer rows: one row over 131,000 positions in 32 groups 38.4 us, in eight 43.0; five 53.7 and 55.2.)
+// The groups' log2.
 __device__ __forceinline__ int part_groups(int parts, int most) {
-  return parts <= 2 ? 1 : parts <= 4 ? 2 : parts <= 8 ? 4 : parts <= 32 ? 8 : most;
+  return parts <= 2 ? 0 : parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 32 || most == 8 ? 3 : 5;
 }
 
 template <int D, bool FP16>
@@ -73,8 +74,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   constexpr int PER = (MAXU + JOIN_THREADS - 1) / JOIN_THREADS;
   SplitDesc d[PER];
   auto items_of = [&](const SplitDesc &x) {
-    const int each = JOIN_THREADS / part_groups(x.parts, a.most_groups);
-    return (cells + each - 1) / each;
+    const int each = 8 - part_groups(x.parts, a.most_groups);  // log2 of a group's threads
+    static_assert(JOIN_THREADS == 1 << 8, "threads");
+    return (cells + (1 << each) - 1) >> each;
   };
   int packed = 0;  // units << 20 | items: at most 320, and 320 * 16 * 128 / 8 below 2^17 of them
 #pragma unroll
@@ -116,8 +118,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     for (int step = 256; step; step >>= 1)
       if (u + step < units && item_s[u + step] <= item) u += step;
     const SplitDesc ds = desc_s[u];
-    const int c0 = cta_s[u], groups = part_groups(ds.parts, a.most_groups), each = JOIN_THREADS / groups, grp = tid / each;
-    const int e = (item - item_s[u]) * each + tid % each, c4 = e / a.rows_cap * 4, r = e % a.rows_cap;
+    const int c0 = cta_s[u], group_bits = part_groups(ds.parts, a.most_groups), groups = 1 << group_bits;
+    const int each = JOIN_THREADS >> group_bits, grp = tid >> (8 - group_bits);
+    const int e = (item - item_s[u]) * each + (tid & (each - 1)), c4 = e / a.rows_cap * 4, r = e % a.rows_cap;
     const bool in = e < cells && r < ds.rows;
     float M = -INFINITY, den = 0.f;
     float4 acc[4] = {};

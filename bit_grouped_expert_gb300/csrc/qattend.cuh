@@ -248,7 +248,7 @@ __device__ __forceinline__ QRun find_run(const AttendArgs &a, M *m) {
     longest = max(longest, u.y);
   }
   const int ctas = gridDim.x;
-  run.each = u_all <= ctas && longest - q_mul_div(run.T, 1, ctas) <= QT_SPARES ? longest : 0;
+  run.each = u_all <= ctas && (long long)(longest - QT_SPARES) * ctas <= run.T ? longest : 0;
   if (run.each) {
     held = (long long)units * longest;
     before = (long long)u_before * longest;
