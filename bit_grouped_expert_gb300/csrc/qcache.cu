@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(QA_THREADS, 3) qcache_append_kernel(const __gr
     const int i0 = min(shares, warp * each), i1 = min(shares, i0 + each);
     RotaryPairs angle;
     // f(run a, run b, row, (layer, head), head's place in a row, layer) for each of them (rows that are not there
-    // as the last one), their values coming through the warp's ring; a lane reads what it has copied itself
+    // as the last one, at its position, so that they raise no maximum), their values coming through the warp's ring; a lane reads what it has copied itself
     auto go = [&](auto f) {
       int row, vh, l, h;
       auto begin = [&]() {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(QA_THREADS, 3) qcache_append_kernel(const __gr
       for (int i = i0; i < i1; ++i) {
         copy(i + QA_AHEAD - 1);  // to the place that was read last
         if (fresh && is_k && g.turns)
-          angle.at(first + row, [&](int k) { return rate_s[k][j]; }, g.table.factor);
+          angle.at(first + min(row, count - 1), [&](int k) { return rate_s[k][j]; }, g.table.factor);
         asm volatile("cp.async.wait_group %0;" ::"n"(QA_AHEAD - 1) : "memory");
         f(ring_s[warp][i % QA_AHEAD][0][lane], ring_s[warp][i % QA_AHEAD][1][lane], row, vh, h * D, l);
         fresh = next();

@@ -236,6 +236,37 @@ def test_rotation_on_the_way(page, dim, dtype, rdim, inter):
             np.testing.assert_array_equal(scales[:, table[s, b]], want)
 
 
+# Few rows for each sequence, each with values in its fastest pairs only, whose largest turned value hangs on the
+# position: the scale is that of the rows that are there (a warp takes 2, 4 or 8 rows at a time).
+@pytest.mark.parametrize("dim,rdim,inter", [(64, 64, False), (64, 48, True), (128, 32, False), (256, 64, True), (256, 256, False)])
+@pytest.mark.parametrize("n", [1, 3, 9])
+def test_scales_of_few_turned_rows(dim, rdim, inter, n):
+    B, page = 60, 16
+    t = Twin(page, 2, dim, "bf16", pages=100, slots=B, max_pages=1, layers=2, seed=n)
+    rot, w = moe.make_rotary(rdim, base=100.0, interleaved=inter), rates(rdim, base=100.0)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    for first in (0, n % 5):
+        if first:  # rows before these, small ones
+            small = torch.full((2, B * first, 2, dim), 2.0 ** -20, dtype=torch.bfloat16, device=DEV)
+            moe.attn_qcache_append(t.cache, rot, small, small, i32([first * b for b in range(B + 1)]), B, ws)
+        kn = t.normal(2, B * n, 2, dim)
+        pairs = torch.arange(dim, device=DEV)
+        fast = pairs // 2 < 2 if inter else pairs % (rdim // 2) < 2
+        kn = (kn * (fast & (pairs < rdim))).contiguous()
+        before = int(t.lens[0])
+        moe.attn_qcache_append(t.cache, rot, kn, kn, i32([n * b for b in range(B + 1)]), B, ws)
+        x = f64(kn).reshape(2, B, n, 2, dim)
+        pos = range(before, before + n)
+        turned = np.stack([[rotate(x[l, b], pos, w, inter) for l in range(2)] for b in range(B)])
+        most, ks = np.abs(turned).max((2, 4)), f64(t.ks)[:, t.table.cpu().numpy()[:, 0]].transpose(1, 0, 2)
+        want = np.vectorize(scale_of)(most)
+        clear = np.abs(most / (448 * want) - 1) > 2.0 ** -12
+        clear &= np.abs(most / (224 * want) - 1) > 2.0 ** -12
+        assert clear.sum() > 200 and int(t.status[0]) == 0
+        assert (ks[clear] == want[clear]).all(), np.argwhere(clear & (ks != want))[:5]
+        moe.attn_qcache_trim(t.cache, None, i32([0] * B), B)
+
+
 @pytest.mark.parametrize("heads,dim,layers,page", [(256, 64, 3, 16), (100, 128, 2, 32), (3, 256, 7, 256)])
 def test_many_heads_and_layers(heads, dim, layers, page):
     t = Twin(page, heads, dim, "bf16", pages=8, slots=2, max_pages=3, layers=layers)
