@@ -80,7 +80,7 @@ struct QCfg {
 
 template <typename C>
 struct QMisc : QRing<C> {
-  uint64_t s_full, s_free, pair_bar[4];
+  uint64_t q_free, s_full, s_free, p_ready, pv_done, pair_bar[4];
   int nonfinite[4];                // by the unit's number: that unit, if NaN was taken out of its V
   union {
     struct {
@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
     ptx::mbar_init(&m->final_bar, 2);
     ptx::fence_mbar_init();
   } else if (tid == 96) {
-    ptx::mbar_init(&m->p_ready[0], C::ROW_WARPS);
-    ptx::mbar_init(&m->pv_done[0], 1);
+    ptx::mbar_init(&m->p_ready, C::ROW_WARPS);
+    ptx::mbar_init(&m->pv_done, 1);
     ptx::mbar_init(&m->s_full, 1);
     ptx::mbar_init(&m->s_free, C::ROW_WARPS);
     ptx::mbar_init(&m->o_free, C::ROW_WARPS);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
     };
     auto values = [&](uint32_t t, bool first) {  // O += P V of running tile t
       const uint32_t slot = t % C::NSV;
-      if (!q_wait_warp(&m->p_ready[0], t & 1u, m, status) ||
+      if (!q_wait_warp(&m->p_ready, t & 1u, m, status) ||
           (first && units > 0 && !q_wait_warp(&m->o_free, (units - 1) & 1u, m, status)) ||
           !q_wait_warp(&m->v_full[slot], (t / C::NSV) & 1u, m, status))
         return false;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
             ptx::mma_ts_f8(tmem, p_col + part * C::P_PART + 8 * i, vd + i * 32 * C::ROWB / 16, id_o,
                              !first || part > 0 || i > 0);
         ptx::mma_commit(&m->v_empty[slot]);
-        ptx::mma_commit(&m->pv_done[0]);
+        ptx::mma_commit(&m->pv_done);
       }
       __syncwarp();
       return true;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
     bool in = false;
     int own = -1;  // the last position that this row sees
     auto finish = [&]() {
-      if (!q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status)) return false;
+      if (!q_wait_warp(&m->pv_done, (jj - 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
       bool got;
       sum += exchange(sum, got);
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
-        split = SplitDesc{(int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
+        const int ends = (int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T);
+        split = SplitDesc{ends - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
           // the product with the tile before is done: its P has been used up, and O may be changed
           // (Here, not where the maximum is found, which is to wait for the product before the weights are made:
           // 181 us for 215 in the case above, whose heads of large scores rescale in most tiles.)
-          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
+          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done, (jj - 1) & 1u, m, status))) break;
           ptx::tc_fence_after();
           if (rescales && j > 0) {
 #pragma unroll 1
@@ -487,10 +488,10 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
         } else {
           arrive(&m->s_free);
           // (as the others: who is ahead of the product by two would take a phase of p_ready for the one before)
-          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done[0], (jj - 1) & 1u, m, status))) break;
+          if (jj >= 1 && !(ok = q_wait_warp(&m->pv_done, (jj - 1) & 1u, m, status))) break;
         }
         ptx::tc_fence_before();
-        arrive(&m->p_ready[0]);
+        arrive(&m->p_ready);
       }
       ++units;
     }

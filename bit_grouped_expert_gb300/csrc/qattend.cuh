@@ -55,7 +55,7 @@ struct QShared {
   int b0;
   QSeq s0;
   long long off0;
-  uint64_t q_full, q_free, o_free, final_bar, p_ready[2], pv_done[2];
+  uint64_t q_full, o_free, final_bar;
 };
 template <typename C>
 struct QRing : QShared {

@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(QA_THREADS, 3) qcache_append_kernel(const __gr
     const int i0 = min(shares, warp * each), i1 = min(shares, i0 + each);
     RotaryPairs angle;
     // f(run a, run b, row, (layer, head), head's place in a row, layer) for each of them (rows that are not there
-    // as the last one, at its position, so that they raise no maximum), their values coming through the warp's ring; a lane reads what it has copied itself
+    // as the last one, at its position, so that they raise no maximum), their values coming through the warp's
+    // ring; a lane reads what it has copied itself
     auto go = [&](auto f) {
       int row, vh, l, h;
       auto begin = [&]() {

@@ -67,7 +67,7 @@ struct DCfg {
 
 template <typename C, int RT>
 struct DMisc : QRing<C> {
-  uint64_t s_full[2], s_free[2], meet[2];
+  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], meet[2];
   int nonfinite[4];                  // by the unit's number: that unit, if NaN was taken out of its V
   __align__(16) float q_f[4][C::R];  // by the unit's number: what a row's scores are multiplied by
   // [half][warp], each warp its own: 2^6 over the running maximum, in log2; infinity before the first score
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       ptx::tc_fence_after();
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
-        split = SplitDesc{(int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T) - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
+        const int ends = (int)q_mul_div(u1 * run.runs + run.T - 1, 1, run.T);
+        split = SplitDesc{ends - cta, 1, un.rows, un.lo + un.token0, un.g * a.G, {}};
       }
       // PV has ended, and with it every write of the flag
       const bool fix = *reinterpret_cast<volatile int *>(&m->nonfinite[(units - 1) & 3]) == units - 1;
@@ -534,7 +535,8 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
             const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
                                      fmaxf(m->most[half][2][i], m->most[half][3][i]));
             const float was = m->base[half][quad][i];
-            const bool up = most > -INFINITY && most + was > QT_TOP + QT_SLACK;  // (of a row that has seen nothing yet: any score)
+            // (of a row that has seen nothing yet: any score)
+            const bool up = most > -INFINITY && most + was > QT_TOP + QT_SLACK;
             f[i] = up ? ex2(QT_TOP - most - was) : 1.f;
             sum[i] *= f[i];
             f[i] *= v_f;
