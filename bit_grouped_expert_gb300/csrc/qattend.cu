@@ -5,7 +5,7 @@
 // serves all of them.  The codes are matrix operands as they lie in the pages:
 // per tile of 128 positions
 //   S[128 rows x 128] = (Qh + Ql) . K^T          tcgen05 (e4m3), K in shared memory
-//   P = 2^(S scales - m)                         two threads a row, running maximum m and sum l
+//   P = 2^(S scales + log2 V scales - u)         two threads a row, running maxima and sum
 //   O[128 rows x D]  += (Ph + Pm + Pl) . V       tcgen05 (e5m2 x e4m3), P in tensor memory, V in shared memory
 // An MMA over 8-bit values runs twice as fast as one over 16-bit ones, so that
 // factors may be sums of 8-bit parts, each the nearest to what the ones before leave:
@@ -16,8 +16,8 @@
 //   running maximum.  (Two e4m3 parts keep 2^-9 of the large ones, but their range is
 //   small: O had to be rescaled wherever a maximum grew by more than 2^1.75, most
 //   tiles of 32 rows.)
-// A page's K scale multiplies its columns of S, its V scale its columns of P, taken
-// relative to the largest V scale so far, so that O stays one sum of one unit.
+// A page's K scale multiplies its columns of S, its V scale its columns of P, which are taken
+// relative to the largest that the row sees (qattend.cuh), so that O stays one sum of one unit.
 //
 // A unit is (sequence, KV head, up to 128 rows); its tiles are the positions
 // that its last row sees.  All units' tiles, in a row, are cut into one equal run
@@ -283,15 +283,21 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       int all_see, some_see;  // positions that all of its rows see, that its last one does
       long long done;         // where this CTA's part ends in the count of all
     } un{};
-    float mx = -INFINITY, sum = 0.f, ref = 0.f;
+    // of this thread's half of the positions the largest score and the sum, of the row the largest score + log2 (V scale)
+    float mx = -INFINITY, sum = 0.f, most = -INFINITY;
     bool in = false;
     int own = -1;  // the last position that this row sees
     auto finish = [&]() {
       if (!q_wait_warp(&m->pv_done, (jj - 1) & 1u, m, status)) return false;
       ptx::tc_fence_after();
+      // the halves' maxima and sums to the row's (a half that saw nothing has the sum 0; NaN stays)
       bool got;
+      const float row_mx = fmaxf(mx, exchange(mx, got));
+      if (!got) return false;
+      if (mx != row_mx) sum *= exp2f(mx - row_mx);
       sum += exchange(sum, got);
       if (!got) return false;
+      const float o_unit = most == -INFINITY ? 0.f : exp2f(most - row_mx);  // what a one in O is
       const bool whole = un.n == un.nt_all, starts = un.t0 == 0;
       if (!whole && starts) {
         const long long u1 = un.done - un.n + un.nt_all;  // the unit's end in the count of all
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       }
       if ((warp & 3) * 32 < un.rows) {
         uint16_t *out = a.o + ((size_t)(un.lo + un.token0 + my_token) * a.Hq + un.g * a.G + my_head) * D;
-        const float f = whole ? ref * inv : ref;
+        const float f = whole ? o_unit * inv : o_unit;
         auto put = [&](int d, uint32_t (&v)[32]) {  // columns d .. d + 31 of this row
           if (whole) {
 #pragma unroll
@@ -359,7 +365,7 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
           if (in) put(d, v);
         }
         if (in && !whole && half == 0)
-          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r) * 2) = make_float2(mx, sum);
+          *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r) * 2) = make_float2(row_mx, sum);
       }
       ptx::tc_fence_before();
       arrive(&m->o_free);
@@ -376,8 +382,8 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
       in = r < un.rows;
       own = in ? pos0 + my_token : -1;
       const bool active = (warp & 3) * 32 < un.rows;  // the warp has rows
-      mx = -INFINITY;
-      sum = ref = 0.f;
+      mx = most = -INFINITY;
+      sum = 0.f;
       const float q_scale =
           in ? a.q_factor[(size_t)(un.lo + un.token0 + my_token) * a.Hq + un.g * a.G + my_head] * a.scale_log2 : 0.f;
       for (int j = 0; j < un.n; ++j, ++jj) {
@@ -413,42 +419,42 @@ __global__ void __launch_bounds__(QCfg<D, 2>::THREADS, 1)
               if (i >= left) x[i / 32][i % 32] = 0xFF800000u;  // -infinity
           }
           const float(*sc)[8] = m->scales[jj % C::SCALES];
-          float kf[COLS / QT_GROUP], tmax = -INFINITY, vmax = 0.f;
+          float kf[COLS / QT_GROUP], vl[COLS / QT_GROUP], tmax = -INFINITY, umax = -INFINITY;
 #pragma unroll
           for (int g = 0; g < COLS / QT_GROUP; ++g) {
             // (not zero: it multiplies -infinity; and a scale of zero leaves scores of next to nothing)
             kf[g] = fmaxf(q_scale * sc[0][half * (COLS / QT_GROUP) + g], 1e-37f);
-            float most[2] = {-INFINITY, -INFINITY};
+            float two[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < QT_GROUP; i += 2)
-              most[i / 2 & 1] = largest_of(most[i / 2 & 1], __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]),
-                                           __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i + 1]));
-            tmax = fmaxf(tmax, fmaxf(most[0], most[1]) * kf[g]);
+              two[i / 2 & 1] = largest_of(two[i / 2 & 1], __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i]),
+                                          __uint_as_float(x[g / 2][g % 2 * QT_GROUP + i + 1]));
+            const float s = fmaxf(two[0], two[1]) * kf[g];
+            vl[g] = v_log2(sc[1][half * (COLS / QT_GROUP) + g]);
+            tmax = fmaxf(tmax, s);
+            umax = fmaxf(umax, s + vl[g]);
           }
-#pragma unroll
-          for (int g = 0; g < 8; ++g) vmax = fmaxf(vmax, sc[1][g]);
-          tmax = fmaxf(tmax, exchange(tmax, ok));
+          umax = fmaxf(umax, exchange(umax, ok));
           if (!ok) break;
-          const bool grows = in && tmax > mx + QT_SLACK, wider = vmax > ref * QT_WIDER;  // also the first a row sees
-          const bool rescales = __any_sync(0xffffffffu, grows || wider);
+          // (also the first a row sees)
+          const bool grows = in && tmax > mx + QT_SLACK, wider = in && umax > most + QT_SLACK;
+          const bool rescales = __any_sync(0xffffffffu, wider);
           float o_f = 1.f;  // what O's earlier tiles are to be multiplied by
-          if (rescales) {
-            if (grows) {
-              o_f = mx == -INFINITY ? 0.f : exp2f(mx - tmax);
-              mx = tmax;
-              sum *= o_f;
-            }
-            if (wider) {
-              o_f *= ref / vmax;
-              ref = vmax;
-            }
+          if (grows) {
+            sum *= mx == -INFINITY ? 0.f : exp2f(mx - tmax);
+            mx = tmax;
           }
-          const float base = QT_TOP - (mx == -INFINITY ? 0.f : mx), inv_ref = ref > 0.f ? 1.f / ref : 0.f;
+          if (wider) {
+            o_f = most == -INFINITY ? 0.f : exp2f(most - umax);
+            most = umax;
+          }
+          const float base = QT_TOP - (mx == -INFINITY ? 0.f : mx), apart = mx == -INFINITY ? 0.f : mx - most;
           uint32_t part[3][COLS / 4];
           float2 acc[2] = {};
 #pragma unroll
           for (int i = 0; i < COLS; i += 4) {
-            const float vf = sc[1][half * (COLS / QT_GROUP) + i / QT_GROUP] * inv_ref;
+            // (finite also for scales that this row does not see: it multiplies their weights, zeros)
+            const float vf = ex2(fminf(vl[i / QT_GROUP] + apart, 127.f));
             float2 p[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {

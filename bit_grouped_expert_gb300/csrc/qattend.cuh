@@ -14,10 +14,13 @@ constexpr int QT_ROWS = 128;      // rows of a unit (MMA M)
 constexpr int QT_TILE = 128;      // positions of a tile
 constexpr int QT_GROUP = 16;      // positions that share scales at least (the smallest page)
 constexpr int QT_MAX_SMS = JOIN_MAX_CTAS / 2;
-// Weights are cut into three e5m2 parts, whose range is wide: a weight at the
-// running maximum is 2^6, and O is rescaled only where the maximum grows by more than
-// 2^7 or the largest scale of V by more than 2^2, so that weights stay below 2^15.
-constexpr float QT_TOP = 6.f, QT_SLACK = 7.f, QT_WIDER = 4.f;
+// A row has two maxima over what it sees: m of its scores s, for the sum of its weights, and u of
+// s + log2 (V scale), for what its weights are as factors of the codes:
+//   l = sum 2^(s - m),   P = 2^(s + log2 (V scale) - u),   o = O 2^(u - m) / l.
+// So no page takes bits from another that the row's result does not take from it.  P is cut into
+// three e5m2 parts, whose range is wide: at the running maximum it is 2^6, and O is rescaled only where
+// that grows by more than 2^7, so that P stays below 2^13.  (l is held the same way.)
+constexpr float QT_TOP = 6.f, QT_SLACK = 7.f;
 // Where units are not cut.  (One token, heads of 256, without and with it: 64 sequences of 700, 1,400, 3,000
 // positions 24.7 and 19.5, 30.5 and 25.4, 45.8 and 40.8 us; one of 350 14.2 and 12.9; one of 1,400, which counts 14
 // tiles more than its share, 15.0, uncut 17.7.  8 sequences' 100 rows over 1,500 41.7 and 37.8, 50 rows over 350 19.7 and 20.0.)
@@ -379,9 +382,9 @@ __device__ __forceinline__ float largest_of(float a, float b, float c) {  // (pa
   return r;
 }
 
-// Two weights in three e5m2 parts, each the nearest to what the ones before leave: as
+// Two weights (P) in three e5m2 parts, each the nearest to what the ones before leave: as
 // fp16, of which an e5m2 value is the upper byte.  Off by 2^-11 of a weight (and fp16's 2^-11), or half
-// of e5m2's least step, 2^-17, which is 2^-23 of the weight at the running maximum.
+// of e5m2's least step, 2^-17, which is 2^-23 of the one at the running maximum.
 // The first two parts are the bytes 1 and 3 of hi and mid, the third those of lo, 0 and 1.
 // (NaN leaves the first two by the addition, but not the third.)
 __device__ __forceinline__ void cut_weights(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
@@ -398,6 +401,14 @@ __device__ __forceinline__ void cut_weights(float x, float y, uint32_t &hi, uint
   uint16_t codes;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(codes) : "r"(last));
   lo = codes;
+}
+
+// log2 of a page's V scale.  Always finite, so that it adds to -infinity, the score of what is not seen: zero
+// as -300 (below the least scale), infinity and NaN, which only pages that no row sees may hold, as 300.
+__device__ __forceinline__ float v_log2(float scale) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(fabsf(scale)));
+  return fmaxf(fminf(y, 300.f), -300.f);
 }
 
 // A code that is NaN among the four of a word: 0x7F or 0xFF.

@@ -7,14 +7,14 @@
 // 128 lanes of an MMA, so that a thread has one position and a share of the
 // rows, and little work is repeated for rows that are not there:
 //   S^T[128 positions x 3 R] = K . [Qh Qm Ql]^T    tcgen05 (e4m3), all in shared memory
-//   P = 2^(S scales - m)                           a position's rows by two threads
+//   P = 2^(S scales + log2 V scales - u)           a position's rows by two threads
 //   O^T[D x 3 R]            += V^T . [Ph Pm Pl]^T  tcgen05 (e4m3 x e5m2), all in shared memory
 // The parts of q (three e4m3 here, which keep fp16 whole too) and of the weights (qattend.cu)
 // are columns of one product, added up where it is read: K and V go through the tensor
 // cores once.
 //
-// A row's maximum is spread over 128 threads, and is not needed as long as no
-// score passes the running one by 2^7: each tile the four warps that share the
+// A row's maxima (qattend.cuh) are spread over 128 threads, and are not needed as long as nothing
+// passes a running one by 2^7: each tile the four warps that share the
 // rows exchange one flag, and only where it is up they find the maxima and rescale.
 // Sums stay in their threads until the unit ends.
 //
@@ -72,6 +72,7 @@ struct DMisc : QRing<C> {
   __align__(16) float q_f[4][C::R];  // by the unit's number: what a row's scores are multiplied by
   // [half][warp], each warp its own: 2^6 over the running maximum, in log2; infinity before the first score
   __align__(16) float base[2][4][RT];
+  __align__(16) float apart[2][4][RT];  // the same: the running maximum less that of score + log2 (V scale); 0 at first
   union {
     struct {
       long long wsum[C::WARPS];
@@ -79,7 +80,8 @@ struct DMisc : QRing<C> {
     };
     struct {                         // later: what the four warps of a half exchange
       int grows[2][2][4];            // [turn][half][warp]
-      float most[2][4][RT];          // [half][warp][row]
+      float most[2][4][RT];          // [half][warp][row]: scores
+      float most_v[2][4][RT];        // with their V scales' log2
       float sums[2][4][RT];
     };
   };
@@ -203,6 +205,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
     ptx::fence_mbar_init();
   } else if (tid >= 128 && tid < 128 + 8 * RT) {
     m->base[0][0][tid - 128] = INFINITY;
+    m->apart[0][0][tid - 128] = 0.f;
   } else if (tid == 96) {
     m->abort_flag = 0;
     ptx::mbar_init(&m->q_full, C::ROW_WARPS);
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       int all_see, some_see;  // positions that all of its rows see, that its last one does
       long long done;         // where this CTA's part ends in the count of all
     } un{};
-    float sum[RT], ref = 0.f;
+    float sum[RT];
     // the sum of a row's three parts
     auto three = [](const uint32_t(&v)[C::HALF], int i) {
       return (__uint_as_float(v[i]) + __uint_as_float(v[RT + i])) + __uint_as_float(v[2 * RT + i]);
@@ -344,6 +347,10 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < RT; ++i)
         sum[i] = (m->sums[half][0][i] + m->sums[half][1][i]) + (m->sums[half][2][i] + m->sums[half][3][i]);
+      float by[RT];  // what the rows of O are to be multiplied by
+#pragma unroll
+      for (int i = 0; i < RT; ++i) by[i] = ex2(-m->apart[half][quad][i]) * (whole ? 1.f / sum[i] : 1.f);
+      __syncwarp();
       if (lane < RT) {  // the maxima: to the joining kernel, and from the start for the next unit
         float mine = 0.f;
 #pragma unroll
@@ -353,6 +360,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           *reinterpret_cast<float2 *>(a.j.ml + (pslot * a.j.rows_cap + r0 + lane) * 2) =
               make_float2(QT_TOP - m->base[half][quad][lane], mine);
         m->base[half][quad][lane] = INFINITY;
+        m->apart[half][quad][lane] = 0.f;
       }
       __syncwarp();
       if (!q_wait_warp(&m->pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1u, m, status)) return false;
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         if (D == 64 && at >= 64) continue;
         float o[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) o[i] = three(v, i) * ref;
+        for (int i = 0; i < RT; ++i) o[i] = three(v, i) * by[i];
         if (fix) {  // codes NaN that were taken out of the edge's tiles, for the rows that see them
           const int p1 = min(un.some_see, (un.t0 + un.n) * QT_TILE);
           const int32_t *table = c.table + (size_t)un.slot * c.max_pages;
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           const int r = r0 + i, token = r * a.g_mul >> 16;
           if (r >= un.rows) continue;
           if (whole) {
-            const float y = sum[i] == 0.f ? 0.f : o[i] * (1.f / sum[i]);
+            const float y = sum[i] == 0.f ? 0.f : o[i];
             out[((size_t)token * a.Hq + (r - token * a.G)) * D] =
                 fp16 ? __half_as_ushort(__float2half_rn(y)) : f32_to_bf16(y);
           } else {
@@ -433,7 +441,6 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
       more = w.next();  // the unit behind this one
 #pragma unroll
       for (int i = 0; i < RT; ++i) sum[i] = 0.f;
-      ref = 0.f;
       for (int j = 0; j < un.n; ++j, ++jj) {
         const int t = un.t0 + j;
         const bool edge = (t + 1) * QT_TILE > un.all_see;
@@ -456,12 +463,9 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           __syncwarp();
         }
         const float(*sc)[8] = m->scales[jj % C::SCALES];
-        const float ks = sc[0][at / QT_GROUP], vs = sc[1][at / QT_GROUP];
-        float vmax = 0.f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) vmax = fmaxf(vmax, sc[1][g]);
-        // this position's scores
-        float s[RT], x[RT];
+        const float ks = sc[0][at / QT_GROUP], vl = v_log2(sc[1][at / QT_GROUP]);
+        // this position's scores; they and, with the V scale, the weights' exponents over the running maxima
+        float s[RT], x[RT], y[RT];
         {
           uint32_t v[C::HALF];
           read_columns(lanes + (jj & 1) * C::N, v);
@@ -489,23 +493,27 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
           for (int i = 0; i < RT; ++i)
             if (r0 + i >= un.rows || first + ((r0 + i) * a.g_mul >> 16) < 0) s[i] = -INFINITY;
         }
-        // what they are over the running maximum; infinite where that is still to be found
-        bool grows = vmax > ref * QT_WIDER;
+        // (infinite where the maxima are still to be found)
+        bool grows = false;
         auto over_maximum = [&]() {
           float most = -INFINITY;
 #pragma unroll
           for (int i = 0; i < RT; i += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(&m->base[half][quad][i]);
-            const float base[4] = {f.x, f.y, f.z, f.w};
+            const float4 h = *reinterpret_cast<const float4 *>(&m->apart[half][quad][i]);
+            const float base[4] = {f.x, f.y, f.z, f.w}, apart[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[i + k] = s[i + k] + base[k];
+            for (int k = 0; k < 4; ++k) {
+              x[i + k] = s[i + k] + base[k];
+              y[i + k] = x[i + k] + (vl + apart[k]);
+            }
           }
           if (edge)
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-              if (s[i] == -INFINITY) x[i] = -INFINITY;  // (and not NaN before the first score)
+              if (s[i] == -INFINITY) x[i] = y[i] = -INFINITY;  // (and not NaN before the first score)
 #pragma unroll
-          for (int i = 0; i < RT; ++i) most = fmaxf(most, x[i]);
+          for (int i = 0; i < RT; ++i) most = largest_of(most, x[i], y[i]);
           grows |= most > QT_TOP + QT_SLACK;
         };
         over_maximum();
@@ -519,51 +527,57 @@ __global__ void __launch_bounds__(DCfg<D, RT>::THREADS, 1)
         }
         float f[RT];  // what O's earlier tiles are to be multiplied by
         if (grows) {
-          float v_f = 1.f;
-          if (vmax > ref * QT_WIDER) {
-            v_f = ref / vmax;
-            ref = vmax;
-          }
-          float mine4[RT / 4];
-          fold(s, mine4, [](float x, float y) { return fmaxf(x, y); });
+          float mine4[RT / 4], mine4_v[RT / 4];
+          auto larger = [](float x, float y) { return fmaxf(x, y); };
+          fold(s, mine4, larger);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) y[i] = s[i] + vl;
+          fold(y, mine4_v, larger);
           if ((lane & 7) == 0)
 #pragma unroll
-            for (int i = 0; i < RT / 4; ++i) m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
+            for (int i = 0; i < RT / 4; ++i) {
+              m->most[half][quad][lane / 8 * (RT / 4) + i] = mine4[i];
+              m->most_v[half][quad][lane / 8 * (RT / 4) + i] = mine4_v[i];
+            }
           if (!(ok = meet())) break;
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const float most = fmaxf(fmaxf(m->most[half][0][i], m->most[half][1][i]),
-                                     fmaxf(m->most[half][2][i], m->most[half][3][i]));
-            const float was = m->base[half][quad][i];
+            auto of_four = [i, half](const float(&v)[2][4][RT]) {
+              return fmaxf(fmaxf(v[half][0][i], v[half][1][i]), fmaxf(v[half][2][i], v[half][3][i]));
+            };
+            const float most = of_four(m->most), most_v = of_four(m->most_v);
+            const float was = m->base[half][quad][i], apart = m->apart[half][quad][i];
             // (of a row that has seen nothing yet: any score)
             const bool up = most > -INFINITY && most + was > QT_TOP + QT_SLACK;
-            f[i] = up ? ex2(QT_TOP - most - was) : 1.f;
-            sum[i] *= f[i];
-            f[i] *= v_f;
+            const bool wider = most_v > -INFINITY && most_v + was + apart > QT_TOP + QT_SLACK;
+            const float mx = up ? most : QT_TOP - was;
+            if (up) sum[i] *= ex2(QT_TOP - most - was);
+            f[i] = wider ? ex2(QT_TOP - was - most_v - apart) : 1.f;
             x[i] = up ? QT_TOP - most : was;
+            // (the other maximum stays where it is: this one's growth comes to what is between them)
+            y[i] = wider ? mx - most_v : up ? apart + (most - (QT_TOP - was)) : apart;
           }
           // (the exchanged maxima are written again after the next tile's meeting at the earliest)
           __syncwarp();
           if (lane == 0)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) m->base[half][quad][i] = x[i];
+            for (int i = 0; i < RT; ++i) m->base[half][quad][i] = x[i], m->apart[half][quad][i] = y[i];
           __syncwarp();
           over_maximum();
         }
         // the weights: this position's row of the tile, a byte a row and part
-        const float vf = ref > 0.f ? vs / ref : 0.f;
         uint32_t p_row[C::HALF / 4] = {};
 #pragma unroll
         for (int i = 0; i < RT; i += 4) {
           float p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            p[k] = ex2(x[i + k]);
-            sum[i + k] += p[k];
+            sum[i + k] += ex2(x[i + k]);
+            p[k] = ex2(y[i + k]);
           }
           uint32_t h0, m0, l0, h1, m1, l1;
-          cut_weights(p[0] * vf, p[1] * vf, h0, m0, l0);
-          cut_weights(p[2] * vf, p[3] * vf, h1, m1, l1);
+          cut_weights(p[0], p[1], h0, m0, l0);
+          cut_weights(p[2], p[3], h1, m1, l1);
           p_row[i / 4] = __byte_perm(h0, h1, 0x7531);
           p_row[(RT + i) / 4] = __byte_perm(m0, m1, 0x7531);
           p_row[(2 * RT + i) / 4] = __byte_perm(l0, l1, 0x5410);

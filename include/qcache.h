@@ -66,11 +66,12 @@ moe_status attn_qcache_trim(const attn_qcache *c, const int32_t *slots_d, const 
  *   ws_d       workspace of attn_qcache_attend_workspace_bytes(c, B, n_rows, max_rows, Hq), scratch
  *   o_d        [n_rows][Hq][head_dim], q's type (written; rows of no sequence are left as they are)
  * Arithmetic: the codes are tensor-core operands as they are, q and the softmax
- * weights sums of 8-bit parts that keep all bits of q but for those below 2^-18 of its
- * row's largest value, and 2^-10 of a weight or 2^-23 of the largest; fp32 sums, o
- * rounded once.
- * What a row does not see cannot change it, whatever its bits; a NaN among its
- * scores, or among the values it sees, makes it NaN.  Supported: Hq a multiple of
+ * weights times V's scales sums of 8-bit parts that keep all bits of q but for those below 2^-18 of
+ * its row's largest value, and 2^-10 of a weight or 2^-23 of the largest product of a weight and its V
+ * scale that the row sees; fp32 sums, o rounded once.  Weights below 2^-110 of the row's
+ * largest may count as none, and values above 2^80 may pass the range of the sums.
+ * What a row does not see cannot change it, codes and scales whatever their bits; a NaN
+ * among its scores, or among the values it sees, makes it NaN.  Supported: Hq a multiple of
  * n_kv_heads, at most 128 query heads per KV head, B <= 1024, n_rows * Hq < 2^30.
  * B == 0 or n_rows == 0 returns MOE_OK with nothing enqueued.  Device checks
  * (slots, offsets, lengths, pages) set MOE_ERR_DEVICE_BOUNDS in the cache's status
