@@ -52,15 +52,18 @@ struct RotaryPairs {
 
   // p times the rate overflows by whole turns: what is left is the angle, whose
   // nearest quarter turn is taken off as a whole number.  The rest, within an eighth of a
-  // turn, keeps 2^-24 of itself in fp32, and the series of sine and cosine to the
+  // turn, comes as two signed words, so that fp32 keeps 2^-23 of it however small it is (as one word of
+  // 64 bits: 8,191 rows of 16 heads of 256 27.6 us), and the series of sine and cosine to the
   // ninth and tenth power are off by 2^-29 there.
   template <typename F>
   __device__ __forceinline__ void at(int p, F rate, float factor) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t turn = (uint32_t)((uint64_t)(int64_t)p * rate(i) >> 32);
-      const uint32_t quarter = (turn + 0x20000000u) >> 30;
-      const float x = (float)(int32_t)(turn - (quarter << 30)) * (6.283185307f * 0x1p-32f), xx = x * x;
+      const uint64_t turn = (uint64_t)(int64_t)p * rate(i);
+      const uint32_t low = (uint32_t)turn, high = (uint32_t)(turn >> 32) + (low >> 31);  // low as a signed word
+      const uint32_t quarter = (high + 0x20000000u) >> 30;
+      const float x = fmaf((float)(int32_t)(high - (quarter << 30)), 6.283185307f * 0x1p-32f,
+                           (float)(int32_t)low * (6.283185307f * 0x1p-64f)), xx = x * x;
       const float v = fmaf(x * xx, fmaf(xx, fmaf(xx, fmaf(xx, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
       const float u =
           fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);

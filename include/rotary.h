@@ -17,8 +17,9 @@
  *
  * Arithmetic: a rate is held as the fraction of a turn in 64-bit fixed point, so
  * that position times rate, taken modulo one turn by its overflow, is off by
- * |p| * 2^-53 turns or so whatever the position; cos, sin and the products
- * in fp32, rounded once.  A negative position turns backwards, which is also
+ * 2^-50 of itself or |p| * 2^-64 turns whatever the position.  What is left beyond the nearest
+ * quarter turn keeps 2^-23 of itself in fp32, so that the sines of small angles keep their
+ * bits; cos, sin and the products in fp32, rounded once.  A negative position turns backwards, which is also
  * the gradient's way through a rotation.
  *
  * Conventions as in moe.h.

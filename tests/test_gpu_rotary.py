@@ -4,8 +4,8 @@ against the fp64 oracle.
 Tolerance, from the arithmetic: with u half a step of the type (bf16 2^-8, fp16
 2^-11, and half of fp16's least step 2^-24), o is rounded once: u |o|.  The angle: the rate is off
 by 2^-53 of itself (a few: pow and two products) or 2^-64 turns, times the
-position; the fraction is cut to 2^-32 turns and rounded to 2^-24 of itself, half
-a turn at most: 2^-22.3 radians.  cos and sin are off by 2^-23, the two products and
+position; what it is beyond a quarter turn is rounded to 2^-24 of itself, an eighth of
+a turn at most, and multiplied by 2 pi: below 2^-22.3 radians.  cos and sin are off by 2^-23, the two products and
 their sum by 2^-24 each, the factor by 2^-24: all in all (|x| + |y|) |factor|
 (2^-20 + |p| 2^-49).
 """
@@ -317,3 +317,26 @@ def test_an_append_that_fails_changes_nothing():
     assert all(torch.equal(x, y) for x, y in zip(was, (t.k, t.v, t.refs, t.table, t.lens)))
     with pytest.raises(moe.MoeError):  # more is turned than a head has
         moe.attn_cache_append_rotary(t.cache, plan(128)[0], kn, vn, i32([0, 2, 34]), 2, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("stretch", [1.0, 32.0, 1e4, 1e7])
+def test_small_angles_keep_their_bits(stretch, inter, dtype):
+    # Pairs (x, 0) become (x cos a, x sin a), so that the second value is as exact as a itself: the fraction of a turn is
+    # rounded to 2^-24 of itself, then multiplied by 2 pi (2^-24, the constant 2^-25); the series, the factor
+    # and the product with x another 2^-24 each, the rate 2^-50 and 2^-64 turns of 1 / (turns a position): 2^-21 together.
+    D = 256
+    rot, w = plan(D, inter, base=1e6, stretch=stretch)
+    x = normal(12, 8, 2, D, dtype=dtype).abs() + 0.5
+    second = slice(1, D, 2) if inter else slice(D // 2, D)
+    x[..., second] = 0.0
+    positions = [0, 1, -1, 10, -37, 1000, 4097, -100000]
+    o = torch.empty_like(x)
+    moe.attn_rotary(rot, x, i32(positions), o)
+    ref = rotate(f64(x), positions, w, inter)[..., second]
+    small = np.abs(np.outer(positions, w))[:, None, :] < np.pi / 4   # beyond, the quarter turns' own errors count
+    lim = np.abs(ref) * (HALF[dtype] + 2.0 ** -21 + 2.0 ** -64 * 2 * np.pi / w) + 2.0 ** -25 * (dtype == "fp16")
+    err = np.abs(f64(o)[..., second] - ref)
+    assert (err <= lim)[np.broadcast_to(small, err.shape)].all(), float((err / np.maximum(lim, 1e-300) * small).max())
+    check(o, x, w, positions, dtype, inter)
