@@ -33,8 +33,8 @@
 //
 // A tile of 128 rows, heads of 256, bf16, is 1,024 cycles of MMA for S and 1,536 for O; the rows
 // take 3,100 to 3,600 and bound it, K and V are there in time.  4 sequences' 500 rows over 8,000
-// positions, 16 heads on 2: 172 us with the cut (8.5) and the join (14), 1,050 TFLOP/s; 5 rows over
-// 131,000 positions 45.7 us, 2.9 TB/s.  (Sixteen row warps of 96 registers: 220 and 53.7 us where these
+// positions, 16 heads on 2: 171 to 178 us with the cut (8.5) and the join (13.5), 1,020 TFLOP/s and more; 5 rows over
+// 131,000 positions 45.5 us, 2.9 TB/s.  (Sixteen row warps of 96 registers: 220 and 53.7 us where these
 // eight took 215 and 50.3.)
 //
 // Every wait is bounded: after one second the kernel records

@@ -22,8 +22,8 @@
 // and two P buffers, and the row warps cutting the queries between units.
 //
 // HBM bounds it between the ends of a call and of its units: 48 tokens over up to 9,000 positions, 16 heads on 2
-// of 256, bf16, 53.8 us (4.9 TB/s) with the join (7); 64 x 2 tokens over up to 3,000, 32 heads on 8 of 128, fp16, 58.8 us
-// (3.85 TB/s); one token over 700 positions 14.4 us, latency.
+// of 256, bf16, 53.8 us (4.9 TB/s) with the join (6.4); 64 x 2 tokens over up to 3,000, 32 heads on 8 of 128, fp16, 58.2 us
+// (3.9 TB/s); one token over 700 positions 14.4 us, latency.
 #include <math.h>
 
 #include "qattend.cuh"

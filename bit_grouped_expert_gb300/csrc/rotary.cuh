@@ -52,8 +52,8 @@ struct RotaryPairs {
 
   // p times the rate overflows by whole turns: what is left is the angle, whose
   // nearest quarter turn is taken off as a whole number.  The rest, within an eighth of a
-  // turn, comes as two signed words, so that fp32 keeps 2^-23 of it however small it is (as one word of
-  // 64 bits: 8,191 rows of 16 heads of 256 27.6 us), and the series of sine and cosine to the
+  // turn, comes as two signed words, so that fp32 keeps 2^-23 of it however small it is (8,191 rows of
+  // 16 heads of 256 26.3 us, as one word of 64 bits 27.6), and the series of sine and cosine to the
   // ninth and tenth power are off by 2^-29 there.
   template <typename F>
   __device__ __forceinline__ void at(int p, F rate, float factor) {
